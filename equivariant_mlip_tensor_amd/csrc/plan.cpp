@@ -19,8 +19,6 @@
 
 namespace tpconv {
 
-namespace {
-
 bool parse_irreps(const char* text, std::vector<Segment>& out, std::string& why) {
   out.clear();
   if (text == nullptr) {
@@ -82,8 +80,6 @@ bool parse_irreps(const char* text, std::vector<Segment>& out, std::string& why)
   }
   return true;
 }
-
-}  // namespace
 
 tpconv_status Plan::build(const char* irreps_in, int sh_lmax_, const char* irreps_out, tpconv_dtype dt,
                           Plan& p) {

@@ -76,6 +76,9 @@ struct Graph {
   int32_t* src_order = nullptr;
 };
 
+// "mul x l p" terms joined by '+'; false with the reason in `why`.
+bool parse_irreps(const char* text, std::vector<Segment>& out, std::string& why);
+
 // Records the message for tpconv_last_error() and returns the status.
 tpconv_status fail(tpconv_status st, const std::string& msg);
 

@@ -31,6 +31,8 @@ Modules:
              and the gradient through the edge frames to the edge vectors.
   radial  -- per-edge weights from the radial network's last layer, W = h M,
              and the convolution's gradients with respect to h and M.
+  node    -- what a mixture-of-experts potential runs on its atoms: species
+             embedding, routing to experts, the experts' maps, dropout.
 
 Every function here is pinned by a test in ``tests/test_oracle_*.py`` against
 mathematics it does not itself use (library routines, closed forms,
