@@ -1,22 +1,517 @@
 // node_experts.hip -- the experts' equivariant maps on irreps rows and their
-// gradients.
+// gradients:
+//   out[i][v][m]    = sum_a g_ia sum_u M_e[u][v] x[i][u][m],  e = e(i, a)
+//   grad_x[i][u][m] = sum_a g_ia sum_v M_e[u][v] G[i][v][m]
+//   grad_g[i][a]    = sum_{u,m} x[i][u][m] (M_e G_i)[u][m]
+//   grad_M_e[u][v]  = sum_{(i,a): e(i,a) = e} g_ia sum_m x[i][u][m] G[i][v][m]
+// for each pair of equal (l, parity) segments.  A row has 2l+1 components that
+// all see the same matrix, so a map is a matrix product whose rows are the
+// (atom, component) pairs of an expert's atoms; it runs on the matrix cores
+// (v_mfma_f32_16x16x4f32, v_mfma_f64_16x16x4f64: the library's data types).
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "node_internal.hpp"
 
 namespace tpconv {
 namespace {
 
+// ------------------------------------------------------------ matrix cores
+// D[i][j] += sum_k A[i][k] B[k][j], 16 x 16 x 4: lane holds A[lane % 16]
+// [lane / 16], B[lane / 16][lane % 16] and the four D[row(lane / 16, r)][lane % 16].
+template <class T>
+struct Mfma;
+template <>
+struct Mfma<float> {
+  typedef float Acc __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ Acc step(float a, float b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int g, int r) { return 4 * g + r; }
+};
+template <>
+struct Mfma<double> {
+  typedef double Acc __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ Acc step(double a, double b, Acc c) {
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int g, int r) { return 4 * r + g; }
+};
+
+template <class T>
+struct alignas(16) Pack {  // one 16-byte load
+  T v[16 / sizeof(T)];
+};
+
 int blocks_for(int64_t n, int block) {
   const int64_t g = (n + block - 1) / block;
   return static_cast<int>(g < 1 ? 1 : (g > 65536 ? 65536 : g));
 }
 
-struct MapArgs {
-  int64_t n_rows, dim_in, dim_out, weight_numel;
-  int32_t X, k;
-  ExpertMap m;
+size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+
+// ------------------------------------------------------------------ layout
+// Rows are taken in groups of kGroup (or n / 64 when that is more, so that
+// there are at most 64 groups); each group is sorted by itself, which needs
+// no exchange between blocks: one launch whatever the size.
+//   order    the group's rows by the pair (smallest, next) of their experts, so
+//            that a tile of consecutive rows meets few experts
+//   entries  the group's entries (row * top_k + place) by expert, entries of an
+//            expert in ascending order (the sums over them are taken in it)
+//   first    [group][X + 1] where each expert's entries start in `entries`,
+//            relative to the group's first
+//   piece    [group][X + 1] the same in pieces of at most kPiece entries
+constexpr int64_t kGroup = 2048;
+constexpr int kMaxBins = 4096;
+
+struct LayoutShape {
+  int64_t group, n_groups;
+  int64_t piece;       // entries of a piece
+  int64_t max_pieces;  // pieces of a group, at most
+  size_t order, entries, first, pieces, total;
 };
+
+LayoutShape layout_shape(int64_t n, int X, int k) {
+  LayoutShape L{};
+  L.group = std::max<int64_t>(kGroup, (n + 63) / 64);
+  L.n_groups = std::max<int64_t>(1, (n + L.group - 1) / L.group);
+  const int64_t most = std::min(L.group, std::max<int64_t>(n, 1)) * k;
+  L.piece = std::max<int64_t>(256, (most + 63) / 64);
+  L.max_pieces = most / L.piece + X;
+  size_t o = 0;
+  auto take = [&](int64_t ints) {
+    const size_t at = o;
+    o = align_up(o + sizeof(int32_t) * static_cast<size_t>(ints));
+    return at;
+  };
+  L.order = take(n);
+  L.entries = take(n * k);
+  L.first = take(L.n_groups * (X + 1));
+  L.pieces = take(L.n_groups * (X + 1));
+  L.total = std::max<size_t>(o, 256);
+  return L;
+}
+
+// Exclusive sum over the block's values (one per thread) plus the total.
+__device__ __forceinline__ int block_exclusive(int v, int* wave_sums, int& total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(s, o, 64);
+    if (lane >= o) s += t;
+  }
+  __syncthreads();
+  if (lane == 63) wave_sums[w] = s;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int q = 0; q < nw; ++q) {
+    const int t = wave_sums[q];
+    before += q < w ? t : 0;
+    total += t;
+  }
+  return before + s - v;
+}
+
+// In-place exclusive sums of n counters in LDS; returns their total.
+__device__ int scan_counters(int* c, int n, int* wave_sums) {
+  int carry = 0;
+  const int per = (n + blockDim.x - 1) / blockDim.x;
+  const int at = threadIdx.x * per, end = min(n, at + per);
+  int mine = 0;
+  for (int q = at; q < end; ++q) mine += c[q];
+  int total;
+  carry = block_exclusive(mine, wave_sums, total);
+  for (int q = at; q < end; ++q) {
+    const int t = c[q];
+    c[q] = carry;
+    carry += t;
+  }
+  __syncthreads();
+  return total;
+}
+
+// One block per group.  Bins of the row order: (smallest expert) * H + (next
+// * H / X), H = min(X, 4096 / X); rows without experts last.  Rows of one bin
+// come in no fixed order (an integer atomic hands out the places): a row's
+// results do not depend on its neighbours.  Entries are ranked by counting in
+// order, so theirs is fixed.  Latency bound: 28000 rows are 14 blocks.
+__global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group, int64_t piece,
+                                                 const int32_t* __restrict__ experts, int32_t* __restrict__ order,
+                                                 int32_t* __restrict__ entries, int32_t* __restrict__ first,
+                                                 int32_t* __restrict__ pieces) {
+  __shared__ int bins[kMaxBins + 1];
+  __shared__ int wave_sums[16];
+  const int64_t r0 = blockIdx.x * group;
+  const int rows = static_cast<int>(min(group, n - r0));
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, nw = blockDim.x >> 6;
+  const int32_t* ex = experts + r0 * k;
+
+  auto bin_of = [&](int r) {
+    int lo = X, hi = X;
+    for (int a = 0; a < k; ++a) {
+      const int e = ex[int64_t(r) * k + a];
+      if (e < 0 || e >= X) continue;
+      if (e < lo) {
+        hi = lo;
+        lo = e;
+      } else if (e > lo && e < hi) {
+        hi = e;
+      }
+    }
+    if (lo == X) return X * H;
+    if (hi == X) hi = lo;
+    return lo * H + hi * H / X;
+  };
+  for (int q = tid; q <= X * H; q += blockDim.x) bins[q] = 0;
+  __syncthreads();
+  for (int r = tid; r < rows; r += blockDim.x) atomicAdd(&bins[bin_of(r)], 1);
+  __syncthreads();
+  scan_counters(bins, X * H + 1, wave_sums);
+  for (int r = tid; r < rows; r += blockDim.x)
+    order[r0 + atomicAdd(&bins[bin_of(r)], 1)] = static_cast<int32_t>(r0 + r);
+  __syncthreads();
+
+  // entries by expert: each wavefront counts, then places, its own run of them;
+  // counters [expert][wavefront], scanned in that order
+  const int total = rows * k;
+  const int run = ((total + nw - 1) / nw + 63) / 64 * 64;
+  const int q0 = w * run, q1 = min(total, q0 + run);
+  for (int q = tid; q < X * nw; q += blockDim.x) bins[q] = 0;
+  __syncthreads();
+  for (int q = q0 + lane; q < q1; q += 64) {
+    const int e = ex[q];
+    if (e >= 0 && e < X) atomicAdd(&bins[e * nw + w], 1);
+  }
+  __syncthreads();
+  const int placed = scan_counters(bins, X * nw, wave_sums);
+  int32_t* const fst = first + blockIdx.x * int64_t(X + 1);
+  int32_t* const pcs = pieces + blockIdx.x * int64_t(X + 1);
+  int mine = 0;  // X <= 256 <= blockDim
+  if (tid < X) {
+    const int at = bins[tid * nw], end = tid + 1 < X ? bins[(tid + 1) * nw] : placed;
+    fst[tid] = at;
+    mine = static_cast<int>((end - at + piece - 1) / piece);
+  }
+  int n_pieces;
+  const int before = block_exclusive(mine, wave_sums, n_pieces);
+  if (tid < X) pcs[tid] = before;
+  if (tid == 0) {
+    fst[X] = placed;
+    pcs[X] = n_pieces;
+  }
+  __syncthreads();
+  for (int q = q0; q < q1; q += 64) {
+    const int e = q + lane < q1 ? ex[q + lane] : -1;
+    const bool live = e >= 0 && e < X;
+    uint64_t peers = __ballot(live);  // lanes of this pass with the same expert
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t on = __ballot(live && ((e >> b) & 1));
+      peers &= ((e >> b) & 1) ? on : ~on;
+    }
+    if (live) {
+      const int rank = __popcll(peers & ((uint64_t(1) << lane) - 1));
+      int base = 0;
+      if (rank == 0) base = atomicAdd(&bins[e * nw + w], __popcll(peers));
+      base = __shfl(base, __ffsll(static_cast<unsigned long long>(peers)) - 1, 64);
+      entries[r0 * k + base + rank] = static_cast<int32_t>(r0 * k + q + lane);
+    }
+  }
+}
+
+// entries of each expert, summed over the groups
+__global__ void k_load(int X, int64_t n_groups, const int32_t* __restrict__ first, int32_t* __restrict__ load) {
+  const int e = threadIdx.x;
+  if (e >= X) return;
+  int c = 0;
+  for (int64_t g = 0; g < n_groups; ++g) c += first[g * (X + 1) + e + 1] - first[g * (X + 1) + e];
+  load[e] = c;
+}
+
+// ----------------------------------------------------- rows: out and grad_x
+// A block takes a tile of rows (in the layout's order) and one map: the tile's
+// segment goes to LDS once, the tile's experts are listed with their member
+// rows, and for each expert the members' (row, component) pairs are packed
+// into 16-row matrix tiles, so a tile that meets many experts still fills the
+// matrix cores.  The products, times the gates, are added into the tile's
+// output in LDS, which is written once: x is read once and out written once
+// whatever top_k, and each row's sum runs over its experts in ascending order.
+// A wavefront owns 16 output channels at a time, so no two wavefronts add into
+// the same place.  ADJ runs the transposed maps on grad_out; GG also dots the
+// ungated products with x for the gates' gradient (a partial sum per map).
+struct RowMap {
+  int32_t src_off, dst_off;  // first columns in a row of src / dst
+  int32_t K, N;              // channels summed over / produced
+  int32_t V;                 // row length of the map's weights
+  int32_t d, woff;
+  int32_t tile;              // rows of a tile, at most 32
+  int32_t ld_src, ld_dst;    // LDS elements between a tile's rows
+  int32_t first;             // first block of this map
+  int32_t vec;               // bit 0 / 1: 16-byte aligned rows of src / dst; bit 2: of the weights along K
+};
+
+struct RowArgs {
+  int64_t n_rows, ld_src, ld_dst, weight_numel;
+  int32_t X, k, n_maps, waves;
+  RowMap map[kMaxMaps];
+};
+
+// LDS of a block, in elements of the data type and 32-bit words.
+struct RowLds {
+  size_t src, acc, dot, rowsum, gate, mask, start, list, rows, total;
+};
+
+RowLds row_lds(const RowMap& m, int X, int k, int waves, bool gg, size_t size) {
+  RowLds L{};
+  size_t o = 0;
+  auto take = [&](size_t n, size_t each) {
+    const size_t at = o;
+    o = (o + n * each + 15) / 16 * 16;
+    return at;
+  };
+  const size_t t = m.tile;
+  L.src = take(t * m.ld_src, size);
+  L.acc = take(t * m.ld_dst, size);
+  L.dot = take(gg ? t * m.ld_dst : 0, size);
+  L.rowsum = take(gg ? t * k * m.d * waves : 0, size);
+  L.gate = take(t * k, size);
+  L.mask = take(X, 4);
+  L.start = take(X, 4);
+  L.list = take(2 * (t * k + 1), 4);
+  L.rows = take(t * k * m.d, 4);
+  L.total = o;
+  return L;
+}
+
+// Rows of `len` elements between global memory (ld apart, picked by row()) and
+// LDS (lds_ld apart): groups of lanes, a power of two, share a row.
+template <class T, class Row, class Move>
+__device__ __forceinline__ void each_piece(int rows, int len, int step, Row row, Move move) {
+  const int pieces = len / step;
+  int lanes = 64;
+  while (lanes > 1 && lanes / 2 >= pieces) lanes >>= 1;
+  const int lane = threadIdx.x & 63, per = 64 / lanes;
+  const int sub = lane & (lanes - 1);
+  for (int s = (threadIdx.x >> 6) * per + lane / lanes; s < rows; s += (blockDim.x >> 6) * per) {
+    const int64_t at = row(s);
+    for (int c = sub; c < pieces; c += lanes) move(s, at, c * step);
+  }
+}
+
+template <class T, int KS, bool ADJ, bool GG>
+__global__ __launch_bounds__(256) void k_rows(RowArgs a, RowLds L0, const T* __restrict__ src,
+                                              const T* __restrict__ weights, const int32_t* __restrict__ experts,
+                                              const T* __restrict__ gates, const int32_t* __restrict__ order,
+                                              T* __restrict__ dst, const T* __restrict__ other,
+                                              T* __restrict__ gate_part) {
+  extern __shared__ char lds[];
+  int mi = 0;
+  while (mi + 1 < a.n_maps && static_cast<int>(blockIdx.x) >= a.map[mi + 1].first) ++mi;
+  const RowMap m = a.map[mi];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, k = a.k, d = m.d;
+  const int64_t base = int64_t(static_cast<int>(blockIdx.x) - m.first) * m.tile;
+  const int rows = static_cast<int>(min<int64_t>(m.tile, a.n_rows - base));
+  T* const xs = reinterpret_cast<T*>(lds + L0.src);
+  T* const acc = reinterpret_cast<T*>(lds + L0.acc);
+  T* const dot = reinterpret_cast<T*>(lds + L0.dot);
+  T* const rowsum = reinterpret_cast<T*>(lds + L0.rowsum);
+  T* const gate = reinterpret_cast<T*>(lds + L0.gate);
+  uint32_t* const mask = reinterpret_cast<uint32_t*>(lds + L0.mask);  // members of each expert, a bit per row
+  int* const start = reinterpret_cast<int*>(lds + L0.start);          // their first place in the list of members
+  int* const list = reinterpret_cast<int*>(lds + L0.list);            // the tile's experts: (expert, first place)
+  uint32_t* const rtab = reinterpret_cast<uint32_t*>(lds + L0.rows);  // matrix row -> row, component, place
+
+  auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
+
+  // the tile's rows, and the list of its experts while they arrive
+  constexpr int kPer = 16 / sizeof(T);
+  const int len = m.K * d, olen = m.N * d;
+  auto stage = [&](const T* from, int64_t ld, int off, int n, bool vec, T* to, int to_ld) {
+    if (vec)
+      each_piece<T>(rows, n, kPer, [&](int s) { return row_of(s) * ld + off; },
+                    [&](int s, int64_t at, int c) {
+                      const Pack<T> p = *reinterpret_cast<const Pack<T>*>(from + at + c);
+#pragma unroll
+                      for (int q = 0; q < kPer; ++q) to[s * to_ld + c + q] = p.v[q];
+                    });
+    else
+      each_piece<T>(rows, n, 1, [&](int s) { return row_of(s) * ld + off; },
+                    [&](int s, int64_t at, int c) { to[s * to_ld + c] = from[at + c]; });
+  };
+  stage(src, a.ld_src, m.src_off, len, m.vec & 1, xs, m.ld_src);
+  if (GG) stage(other, a.ld_dst, m.dst_off, olen, m.vec & 2, dot, m.ld_dst);
+  // channels up to the next multiple of 4 KS are summed over too: zero
+  const int padded = (m.K + 4 * KS - 1) / (4 * KS) * 4 * KS * d;
+  if (padded > len)
+    each_piece<T>(rows, padded - len, 1, [&](int s) { return int64_t(s); },
+                  [&](int s, int64_t, int c) { xs[s * m.ld_src + len + c] = T(0); });
+  for (int q = tid; q < rows * m.ld_dst; q += blockDim.x) acc[q] = T(0);
+  for (int q = tid; q < a.X; q += blockDim.x) mask[q] = 0;
+  if (GG)
+    for (int q = tid; q < a.waves * m.tile * k * d; q += blockDim.x) rowsum[q] = T(0);
+  __syncthreads();
+  const int n_entries = rows * k;
+  auto entry = [&](int q, int& s, int64_t& at) {
+    s = q / k;
+    at = row_of(s) * k + (q - s * k);
+    const int e = experts[at];
+    return e >= 0 && e < a.X ? e : -1;
+  };
+  for (int q = tid; q < n_entries; q += blockDim.x) {
+    int s;
+    int64_t at;
+    const int e = entry(q, s, at);
+    if (e >= 0) atomicOr(&mask[e], 1u << s);
+  }
+  __syncthreads();
+  // experts present, ascending, with the first place of their members
+  if (w == 0) {
+    int n_here = 0, places = 0;
+    for (int e0 = 0; e0 < a.X; e0 += 64) {
+      const uint32_t mk = e0 + lane < a.X ? mask[e0 + lane] : 0;
+      const int c = __popc(mk);
+      int s = c;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int t = __shfl_up(s, o, 64);
+        if (lane >= o) s += t;
+      }
+      const uint64_t here = __ballot(c > 0);
+      if (c > 0) {
+        const int j = n_here + __popcll(here & ((uint64_t(1) << lane) - 1));
+        list[2 * j] = e0 + lane;
+        list[2 * j + 1] = places + s - c;
+      }
+      if (e0 + lane < a.X) start[e0 + lane] = places + s - c;
+      places += __shfl(s, 63, 64);
+      n_here += __popcll(here);
+    }
+    if (lane == 0) {
+      list[2 * n_here] = -1;
+      list[2 * n_here + 1] = places;
+    }
+  }
+  __syncthreads();
+  // members' gates (an expert that stands twice in a row: their sum) and matrix rows
+  for (int q = tid; q < n_entries; q += blockDim.x) {
+    int s;
+    int64_t at;
+    const int e = entry(q, s, at);
+    if (e < 0) continue;
+    const int64_t r0 = at - (q - s * k);
+    bool leads = true;
+    T g = 0;
+    for (int b = 0; b < k; ++b)
+      if (experts[r0 + b] == e) {
+        leads = leads && r0 + b >= at;
+        g += gates[r0 + b];
+      }
+    if (!leads) continue;
+    const int place = start[e] + __popc(mask[e] & ((1u << s) - 1));
+    gate[place] = g;
+    for (int c = 0; c < d; ++c) rtab[place * d + c] = uint32_t(place) << 16 | uint32_t(s) << 8 | uint32_t(c);
+  }
+  __syncthreads();
+
+  // each wavefront: 16 output channels, all experts of the tile
+  const int i16 = lane & 15, g4 = lane >> 4;
+  for (int n0 = w * 16; n0 < m.N; n0 += a.waves * 16) {
+    const int col = n0 + i16;
+    const bool col_in = col < m.N;
+    for (int k0 = 0; k0 < m.K; k0 += 4 * KS) {
+      for (int j = 0; list[2 * j] >= 0; ++j) {
+        const int e = __builtin_amdgcn_readfirstlane(list[2 * j]);
+        const int p0 = list[2 * j + 1], p1 = list[2 * j + 3];
+        // lane's channels of the sum: k0 + g4 KS + 0 .. KS-1
+        const T* wp = weights + e * a.weight_numel + m.woff;
+        T b[KS];
+        const int kk = k0 + g4 * KS;
+        if (ADJ) {
+          const T* row = wp + int64_t(col_in ? col : 0) * m.V + kk;
+          if (KS >= kPer && (m.vec & 4)) {
+#pragma unroll
+            for (int s = 0; s < KS; s += kPer) {
+              const bool in = col_in && kk + s < m.K;  // K is a multiple of the vector here
+              const Pack<T> p = in ? *reinterpret_cast<const Pack<T>*>(row + s) : Pack<T>{};
+#pragma unroll
+              for (int q = 0; q < kPer; ++q) b[s + q] = p.v[q];
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) b[s] = col_in && kk + s < m.K ? row[s] : T(0);
+          }
+        } else {
+          const T* at = wp + int64_t(kk) * m.V + col;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) b[s] = col_in && kk + s < m.K ? at[int64_t(s) * m.V] : T(0);
+        }
+        const int r_end = p1 * d;
+        for (int r = p0 * d; r < r_end; r += 16) {
+          const uint32_t me = rtab[min(r + i16, r_end - 1)];
+          const T* ap = xs + ((me >> 8) & 255) * m.ld_src + (me & 255) + kk * d;
+          typename Mfma<T>::Acc acc4 = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) acc4 = Mfma<T>::step(ap[s * d], b[s], acc4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int rr = r + Mfma<T>::row(g4, q);
+            const bool live = rr < r_end && col_in;
+            const uint32_t t = rtab[min(rr, r_end - 1)];
+            const int at = ((t >> 8) & 255) * m.ld_dst + (col_in ? col : 0) * d + (t & 255);
+            if (GG) {
+              T v = live ? acc4[q] * dot[at] : T(0);
+#pragma unroll
+              for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 16);
+              if (i16 == 0 && rr < r_end) rowsum[w * (m.tile * k * d) + rr] += v;
+            }
+            if (live) acc[at] += gate[t >> 16] * acc4[q];
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (dst != nullptr) {
+    if (m.vec & 2)
+      each_piece<T>(rows, olen, kPer, [&](int s) { return row_of(s) * a.ld_dst + m.dst_off; },
+                    [&](int s, int64_t at, int c) {
+                      Pack<T> p;
+#pragma unroll
+                      for (int q = 0; q < kPer; ++q) p.v[q] = acc[s * m.ld_dst + c + q];
+                      *reinterpret_cast<Pack<T>*>(dst + at + c) = p;
+                    });
+    else
+      each_piece<T>(rows, olen, 1, [&](int s) { return row_of(s) * a.ld_dst + m.dst_off; },
+                    [&](int s, int64_t at, int c) { dst[at + c] = acc[s * m.ld_dst + c]; });
+  }
+  if (GG) {
+    for (int q = tid; q < n_entries; q += blockDim.x) {
+      int s;
+      int64_t at;
+      const int e = entry(q, s, at);
+      T v = 0;
+      if (e >= 0) {
+        const int place = start[e] + __popc(mask[e] & ((1u << s) - 1));
+        for (int ww = 0; ww < a.waves; ++ww)
+          for (int c = 0; c < d; ++c) v += rowsum[ww * (m.tile * k * d) + place * d + c];
+      }
+      gate_part[mi * (a.n_rows * k) + at] = v;
+    }
+  }
+}
+
+// gates' gradient: the maps' partial sums, in order
+template <class T>
+__global__ void k_gate_sum(int64_t total, int n_maps, const T* __restrict__ part, T* __restrict__ out) {
+  const int64_t q = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+  if (q >= total) return;
+  T s = 0;
+  for (int p = 0; p < n_maps; ++p) s += part[p * total + q];
+  out[q] = s;
+}
 
 template <class T>
 __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t len, T* __restrict__ out) {
@@ -25,30 +520,12 @@ __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t
     out[(q / len) * dim + off + q % len] = T(0);
 }
 
-// rows of out (ADJ: of grad_x) for one map, a thread per element
-template <class T, bool ADJ>
-__global__ void k_rows(MapArgs a, const T* __restrict__ x, const T* __restrict__ weights,
-                       const int32_t* __restrict__ experts, const T* __restrict__ gates, T* __restrict__ out) {
-  const int d = a.m.d, K = ADJ ? a.m.mul_out : a.m.mul_in, N = ADJ ? a.m.mul_in : a.m.mul_out;
-  const int64_t ldx = ADJ ? a.dim_out : a.dim_in, ldo = ADJ ? a.dim_in : a.dim_out;
-  const int xo = ADJ ? a.m.out_off : a.m.in_off, oo = ADJ ? a.m.in_off : a.m.out_off;
-  const int64_t len = int64_t(N) * d, total = a.n_rows * len, step = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t q = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; q < total; q += step) {
-    const int64_t i = q / len;
-    const int col = int(q - i * len), v = col / d, mm = col - v * d;
-    T s = 0;
-    for (int j = 0; j < a.k; ++j) {
-      const int e = experts[i * a.k + j];
-      if (e < 0 || e >= a.X) continue;
-      const T* M = weights + e * a.weight_numel + a.m.woff;
-      const T* xr = x + i * ldx + xo + mm;
-      T t = 0;
-      for (int u = 0; u < K; ++u) t += xr[u * d] * M[ADJ ? v * a.m.mul_out + u : u * a.m.mul_out + v];
-      s += gates[i * a.k + j] * t;
-    }
-    out[i * ldo + oo + col] = s;
-  }
-}
+// ------------------------------------------------------- weights' gradient
+struct MapArgs {
+  int64_t n_rows, dim_in, dim_out, weight_numel;
+  int32_t X, k;
+  ExpertMap m;
+};
 
 // gradient of one map's weights, a thread per weight over all rows
 template <class T>
@@ -72,105 +549,187 @@ __global__ void k_wgrad(MapArgs a, const T* __restrict__ x, const int32_t* __res
   }
 }
 
-// gradient of the gates, a wavefront per entry; the maps after the first add
-template <class T>
-__global__ void k_ggrad(MapArgs a, bool add, const T* __restrict__ x, const T* __restrict__ weights,
-                        const int32_t* __restrict__ experts, const T* __restrict__ grad, T* __restrict__ out) {
-  const int lane = threadIdx.x & 63, d = a.m.d, V = a.m.mul_out;
-  const int64_t total = a.n_rows * a.k, step = int64_t(gridDim.x) * (blockDim.x >> 6);
-  for (int64_t q = blockIdx.x * int64_t(blockDim.x >> 6) + (threadIdx.x >> 6); q < total; q += step) {
-    const int64_t i = q / a.k;
-    const int e = experts[q];
-    T s = 0;
-    if (e >= 0 && e < a.X) {
-      const T* M = weights + e * a.weight_numel + a.m.woff;
-      const T* xr = x + i * a.dim_in + a.m.in_off;
-      const T* gr = grad + i * a.dim_out + a.m.out_off;
-      for (int v = lane; v < V; v += 64)
-        for (int u = 0; u < a.m.mul_in; ++u) {
-          T t = 0;
-          for (int m = 0; m < d; ++m) t += xr[u * d + m] * gr[v * d + m];
-          s += t * M[u * V + v];
-        }
-    }
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-    if (lane == 0) out[q] = add ? out[q] + s : s;
+// -------------------------------------------------------------------- host
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <class T, int KS, bool ADJ, bool GG>
+hipError_t rows_ks(const RowArgs& a, const RowLds& L, int64_t blocks, const T* src, const T* weights,
+                   const int32_t* experts, const T* gates, const int32_t* order, T* dst, const T* other, T* part,
+                   hipStream_t s) {
+  auto* const f = k_rows<T, KS, ADJ, GG>;
+  if (L.total > 64 * 1024) {  // above the default limit of dynamic LDS
+    const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
+    if (he != hipSuccess) return he;
   }
+  hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * a.waves), L.total, s, a, L, src, weights, experts, gates, order, dst,
+                     other, part);
+  return hipGetLastError();
 }
 
-__global__ void k_load(int64_t total, int X, const int32_t* __restrict__ experts, int32_t* __restrict__ load) {
-  const int e = blockIdx.x;
-  int c = 0;
-  for (int64_t q = threadIdx.x; q < total; q += blockDim.x) c += experts[q] == e;
-  for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o, 64);
-  if (threadIdx.x == 0) load[e] = c;
-}
-
-MapArgs args_of(const Experts& p, int64_t n_rows, const ExpertMap& m) {
-  return MapArgs{n_rows, p.dim_in, p.dim_out, p.weight_numel, p.n_experts, p.top_k, m};
-}
-
-template <class T, bool ADJ>
-void rows(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates, T* out,
-          hipStream_t s) {
+template <class T, bool ADJ, bool GG>
+hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, const int32_t* experts, const T* gates,
+                const int32_t* order, T* dst, const T* other, T* part, hipStream_t s) {
+  RowArgs a{};
+  a.n_rows = n;
+  a.ld_src = ADJ ? p.dim_out : p.dim_in;
+  a.ld_dst = ADJ ? p.dim_in : p.dim_out;
+  a.weight_numel = p.weight_numel;
+  a.X = p.n_experts;
+  a.k = p.top_k;
+  a.n_maps = static_cast<int32_t>(p.maps.size());
+  const int per = 16 / static_cast<int>(sizeof(T));
+  int maxK = 0, maxN = 0;
+  for (int q = 0; q < a.n_maps; ++q) {
+    const ExpertMap& e = p.maps[q];
+    RowMap& m = a.map[q];
+    m.src_off = ADJ ? e.out_off : e.in_off;
+    m.dst_off = ADJ ? e.in_off : e.out_off;
+    m.K = ADJ ? e.mul_out : e.mul_in;
+    m.N = ADJ ? e.mul_in : e.mul_out;
+    m.V = e.mul_out;
+    m.d = e.d;
+    m.woff = e.woff;
+    const bool vs = aligned16(src) && a.ld_src % per == 0 && m.src_off % per == 0 && (m.K * m.d) % per == 0;
+    const bool vd = (dst == nullptr || aligned16(dst)) && (!GG || aligned16(other)) && a.ld_dst % per == 0 &&
+                    m.dst_off % per == 0 && (m.N * m.d) % per == 0;
+    const bool vw = aligned16(weights) && a.weight_numel % per == 0 && m.woff % per == 0 && m.V % per == 0;
+    m.vec = (vs ? 1 : 0) | (vd ? 2 : 0) | (vw ? 4 : 0);
+    maxK = std::max(maxK, m.K);
+    maxN = std::max(maxN, m.N);
+  }
+  const int KS = maxK <= 16 ? 4 : (maxK <= 32 ? 8 : 16);
+  a.waves = std::min(4, (maxN + 15) / 16);
+  // Tile: as many rows (32 at most: a bit each) as leave LDS for 8 wavefronts
+  // on a CU, 20 KiB for each of the block's; one row at least.  With few rows
+  // the tiles are made smaller, to have two blocks for each of the 256 CUs.
+  std::sort(a.map, a.map + a.n_maps, [](const RowMap& x, const RowMap& y) {
+    return int64_t(x.K) * x.N * x.d > int64_t(y.K) * y.N * y.d;  // long maps first
+  });
+  RowLds L{};
+  const int64_t spread = std::max<int64_t>(1, n * a.n_maps / 512);
+  int64_t blocks = 0;
+  for (int q = 0; q < a.n_maps; ++q) {
+    RowMap& m = a.map[q];
+    // rows in LDS start d (rounded up to 4) banks apart, modulo the 64 banks
+    auto pitch = [&](int channels) {
+      const int want = (m.d + 3) / 4 * 4, full = channels * m.d;
+      return full + ((want - full) % 64 + 64) % 64;
+    };
+    m.ld_src = pitch((m.K + 4 * KS - 1) / (4 * KS) * 4 * KS);
+    m.ld_dst = pitch(m.N);
+    for (m.tile = 32; m.tile > 1; --m.tile)
+      if (m.tile <= spread && row_lds(m, a.X, a.k, a.waves, GG, sizeof(T)).total <= size_t(20480) * a.waves) break;
+    m.first = static_cast<int32_t>(blocks);
+    blocks += (n + m.tile - 1) / m.tile;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const RowLds one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
+    // one launch for all maps: each region as large as the map that needs most
+    auto grow = [](size_t& x, size_t y) { x = std::max(x, y); };
+    grow(L.acc, one.acc - one.src);
+    grow(L.dot, one.dot - one.acc);
+    grow(L.rowsum, one.rowsum - one.dot);
+    grow(L.gate, one.gate - one.rowsum);
+    grow(L.mask, one.mask - one.gate);
+    grow(L.start, one.start - one.mask);
+    grow(L.list, one.list - one.start);
+    grow(L.rows, one.rows - one.list);
+    grow(L.total, one.total - one.rows);
+  }
+  // sizes to offsets
+  size_t o = 0;
+  for (size_t* at : {&L.acc, &L.dot, &L.rowsum, &L.gate, &L.mask, &L.start, &L.list, &L.rows, &L.total}) {
+    o += *at;
+    *at = o;
+  }
+  if (L.total > 160 * 1024) return hipErrorInvalidValue;
   for (const ColumnRun& r : ADJ ? p.bare_in : p.bare_out)
-    hipLaunchKernelGGL(k_zero_columns<T>, dim3(blocks_for(n * r.len, 256)), dim3(256), 0, s, n,
-                       ADJ ? p.dim_in : p.dim_out, r.off, r.len, out);
-  for (const ExpertMap& m : p.maps)
-    hipLaunchKernelGGL((k_rows<T, ADJ>), dim3(blocks_for(n * (ADJ ? m.mul_in : m.mul_out) * m.d, 256)), dim3(256), 0,
-                       s, args_of(p, n, m), x, weights, experts, gates, out);
+    if (dst != nullptr)
+      hipLaunchKernelGGL(k_zero_columns<T>, dim3(blocks_for(n * r.len, 256)), dim3(256), 0, s, n, a.ld_dst, r.off,
+                         r.len, dst);
+  switch (KS) {
+    case 4: return rows_ks<T, 4, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
+    case 8: return rows_ks<T, 8, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
+    default: return rows_ks<T, 16, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
+  }
+}
+
+const int32_t* order_in(const Experts& p, int64_t n, const void* layout) {
+  if (layout == nullptr) return nullptr;
+  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
+  return reinterpret_cast<const int32_t*>(static_cast<const char*>(layout) + L.order);
 }
 
 template <class T>
-void backward(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates,
-              const T* grad, T* gx, T* gw, T* gg, hipStream_t s) {
-  if (gx != nullptr && n > 0) rows<T, true>(p, n, grad, weights, experts, gates, gx, s);
-  for (size_t q = 0; q < p.maps.size(); ++q) {
-    const MapArgs a = args_of(p, n, p.maps[q]);
-    if (gw != nullptr)
-      hipLaunchKernelGGL(k_wgrad<T>, dim3(blocks_for(int64_t(a.X) * a.m.mul_in * a.m.mul_out, 256)), dim3(256), 0, s,
-                         a, x, experts, gates, grad, gw);
-    if (gg != nullptr && n > 0)
-      hipLaunchKernelGGL(k_ggrad<T>, dim3(blocks_for(n * a.k, 4)), dim3(256), 0, s, a, q > 0, x, weights, experts,
-                         grad, gg);
+hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates,
+                    const void* layout, const T* grad, T* gx, T* gw, T* gg, void* ws, hipStream_t s) {
+  const int32_t* order = order_in(p, n, layout);
+  hipError_t he = hipSuccess;
+  if (n > 0 && gg != nullptr) {
+    T* part = static_cast<T*>(ws);
+    he = rows<T, true, true>(p, n, grad, weights, experts, gates, order, gx, x, part, s);
+    const int64_t total = n * p.top_k;
+    hipLaunchKernelGGL(k_gate_sum<T>, dim3(blocks_for(total, 256)), dim3(256), 0, s, total, int(p.maps.size()), part,
+                       gg);
+  } else if (n > 0 && gx != nullptr) {
+    he = rows<T, true, false>(p, n, grad, weights, experts, gates, order, gx, nullptr, nullptr, s);
   }
+  if (he != hipSuccess) return he;
+  for (size_t q = 0; gw != nullptr && q < p.maps.size(); ++q) {
+    const MapArgs a{n, p.dim_in, p.dim_out, p.weight_numel, p.n_experts, p.top_k, p.maps[q]};
+    hipLaunchKernelGGL(k_wgrad<T>, dim3(blocks_for(int64_t(a.X) * a.m.mul_in * a.m.mul_out, 256)), dim3(256), 0, s, a,
+                       x, experts, gates, grad, gw);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t experts_layout_bytes(const Experts&, int64_t) { return 256; }
-size_t experts_workspace(const Experts&, int64_t) { return 256; }
+size_t experts_layout_bytes(const Experts& p, int64_t n) { return layout_shape(n, p.n_experts, p.top_k).total; }
 
-hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* experts, void*, int32_t* load,
+size_t experts_workspace(const Experts& p, int64_t n) {
+  return align_up(std::max<size_t>(256, p.maps.size() * n * p.top_k * (p.f64 ? 8 : 4)));
+}
+
+hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* experts, void* layout, int32_t* load,
                                  hipStream_t s) {
-  if (load != nullptr)
-    hipLaunchKernelGGL(k_load, dim3(p.n_experts), dim3(64), 0, s, n * p.top_k, p.n_experts, experts, load);
+  const int X = p.n_experts;
+  const LayoutShape L = layout_shape(n, X, p.top_k);
+  char* const at = static_cast<char*>(layout);
+  auto ints = [&](size_t off) { return reinterpret_cast<int32_t*>(at + off); };
+  const int H = std::min(X, kMaxBins / X);
+  const int threads = std::min(L.group, n) > 1024 ? 1024 : 256;
+  hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(L.n_groups)), dim3(threads), 0, s, n, X, p.top_k, H,
+                     L.group, L.piece, experts, ints(L.order), ints(L.entries), ints(L.first), ints(L.pieces));
+  if (load != nullptr) hipLaunchKernelGGL(k_load, dim3(1), dim3(256), 0, s, X, L.n_groups, ints(L.first), load);
   return hipGetLastError();
 }
 
 hipError_t launch_experts_forward(const Experts& p, int64_t n, const void* x, const void* weights,
-                                  const int32_t* experts, const void* gates, const void*, void* out, hipStream_t s) {
+                                  const int32_t* experts, const void* gates, const void* layout, void* out,
+                                  hipStream_t s) {
+  const int32_t* order = order_in(p, n, layout);
   if (p.f64)
-    rows<double, false>(p, n, static_cast<const double*>(x), static_cast<const double*>(weights), experts,
-                        static_cast<const double*>(gates), static_cast<double*>(out), s);
-  else
-    rows<float, false>(p, n, static_cast<const float*>(x), static_cast<const float*>(weights), experts,
-                       static_cast<const float*>(gates), static_cast<float*>(out), s);
-  return hipGetLastError();
+    return rows<double, false, false>(p, n, static_cast<const double*>(x), static_cast<const double*>(weights),
+                                      experts, static_cast<const double*>(gates), order, static_cast<double*>(out),
+                                      nullptr, nullptr, s);
+  return rows<float, false, false>(p, n, static_cast<const float*>(x), static_cast<const float*>(weights), experts,
+                                   static_cast<const float*>(gates), order, static_cast<float*>(out), nullptr,
+                                   nullptr, s);
 }
 
 hipError_t launch_experts_backward(const Experts& p, int64_t n, const void* x, const void* weights,
-                                   const int32_t* experts, const void* gates, const void*, const void* grad_out,
-                                   void* grad_x, void* grad_weights, void* grad_gates, void*, hipStream_t s) {
+                                   const int32_t* experts, const void* gates, const void* layout, const void* grad_out,
+                                   void* grad_x, void* grad_weights, void* grad_gates, void* ws, hipStream_t s) {
   if (p.f64)
-    backward(p, n, static_cast<const double*>(x), static_cast<const double*>(weights), experts,
-             static_cast<const double*>(gates), static_cast<const double*>(grad_out), static_cast<double*>(grad_x),
-             static_cast<double*>(grad_weights), static_cast<double*>(grad_gates), s);
-  else
-    backward(p, n, static_cast<const float*>(x), static_cast<const float*>(weights), experts,
-             static_cast<const float*>(gates), static_cast<const float*>(grad_out), static_cast<float*>(grad_x),
-             static_cast<float*>(grad_weights), static_cast<float*>(grad_gates), s);
-  return hipGetLastError();
+    return backward(p, n, static_cast<const double*>(x), static_cast<const double*>(weights), experts,
+                    static_cast<const double*>(gates), layout, static_cast<const double*>(grad_out),
+                    static_cast<double*>(grad_x), static_cast<double*>(grad_weights),
+                    static_cast<double*>(grad_gates), ws, s);
+  return backward(p, n, static_cast<const float*>(x), static_cast<const float*>(weights), experts,
+                  static_cast<const float*>(gates), layout, static_cast<const float*>(grad_out),
+                  static_cast<float*>(grad_x), static_cast<float*>(grad_weights), static_cast<float*>(grad_gates), ws,
+                  s);
 }
 
 }  // namespace tpconv
