@@ -64,10 +64,10 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 //   piece    [group][X + 1] the same in pieces of at most kPiece entries
 constexpr int64_t kGroup = 2048;
 constexpr int kMaxBins = 4096;
+constexpr int kPiece = 256;
 
 struct LayoutShape {
   int64_t group, n_groups;
-  int64_t piece;       // entries of a piece
   int64_t max_pieces;  // pieces of a group, at most
   size_t order, entries, first, pieces, total;
 };
@@ -77,8 +77,7 @@ LayoutShape layout_shape(int64_t n, int X, int k) {
   L.group = std::max<int64_t>(kGroup, (n + 63) / 64);
   L.n_groups = std::max<int64_t>(1, (n + L.group - 1) / L.group);
   const int64_t most = std::min(L.group, std::max<int64_t>(n, 1)) * k;
-  L.piece = std::max<int64_t>(256, (most + 63) / 64);
-  L.max_pieces = most / L.piece + X;
+  L.max_pieces = most / kPiece + X;
   size_t o = 0;
   auto take = [&](int64_t ints) {
     const size_t at = o;
@@ -138,7 +137,7 @@ __device__ int scan_counters(int* c, int n, int* wave_sums) {
 // come in no fixed order (an integer atomic hands out the places): a row's
 // results do not depend on its neighbours.  Entries are ranked by counting in
 // order, so theirs is fixed.  Latency bound: 28000 rows are 14 blocks.
-__global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group, int64_t piece,
+__global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group,
                                                  const int32_t* __restrict__ experts, int32_t* __restrict__ order,
                                                  int32_t* __restrict__ entries, int32_t* __restrict__ first,
                                                  int32_t* __restrict__ pieces) {
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
   if (tid < X) {
     const int at = bins[tid * nw], end = tid + 1 < X ? bins[(tid + 1) * nw] : placed;
     fst[tid] = at;
-    mine = static_cast<int>((end - at + piece - 1) / piece);
+    mine = static_cast<int>((end - at + kPiece - 1) / kPiece);
   }
   int n_pieces;
   const int before = block_exclusive(mine, wave_sums, n_pieces);
@@ -503,16 +502,6 @@ __global__ __launch_bounds__(256) void k_rows(RowArgs a, RowLds L0, const T* __r
   }
 }
 
-// gates' gradient: the maps' partial sums, in order
-template <class T>
-__global__ void k_gate_sum(int64_t total, int n_maps, const T* __restrict__ part, T* __restrict__ out) {
-  const int64_t q = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
-  if (q >= total) return;
-  T s = 0;
-  for (int p = 0; p < n_maps; ++p) s += part[p * total + q];
-  out[q] = s;
-}
-
 template <class T>
 __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t len, T* __restrict__ out) {
   const int64_t total = n_rows * len, step = int64_t(gridDim.x) * blockDim.x;
@@ -521,32 +510,232 @@ __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t
 }
 
 // ------------------------------------------------------- weights' gradient
-struct MapArgs {
-  int64_t n_rows, dim_in, dim_out, weight_numel;
-  int32_t X, k;
-  ExpertMap m;
+// grad_M_e = sum over e's entries and components of x (gate G)^T: a matrix
+// product whose inner dimension is the (entry, component) pairs of an expert.
+// A block takes one piece (at most kPiece entries of one expert and group), one
+// map and one S x S tile of it.  Stages of a few entries are gathered into LDS
+// with the components split out ([component row][channel]), while the next
+// stage's loads are in flight in registers; 4 wavefronts share the tile (S =
+// 16: they share the rows, and are added in order at the end).  Each piece's
+// matrix goes to the workspace; k_join adds an expert's pieces in order.
+struct WgradMap {
+  int32_t in_off, out_off, U, V, d, woff;
+  int32_t nu, nv;     // S x S tiles of the matrix
+  int32_t per_stage;  // entries of a stage, a multiple of 4
+  int32_t inv_d;      // ceil(65536 / d): c / d = c * inv_d >> 16 for c below 64 d
+  int32_t first;      // first block of this map
 };
 
-// gradient of one map's weights, a thread per weight over all rows
-template <class T>
-__global__ void k_wgrad(MapArgs a, const T* __restrict__ x, const int32_t* __restrict__ experts,
-                        const T* __restrict__ gates, const T* __restrict__ grad, T* __restrict__ out) {
-  const int d = a.m.d;
-  const int64_t per = int64_t(a.m.mul_in) * a.m.mul_out, total = a.X * per, step = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t q = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; q < total; q += step) {
-    const int e = int(q / per), r = int(q - e * per), u = r / a.m.mul_out, v = r - u * a.m.mul_out;
-    T s = 0;
-    for (int64_t i = 0; i < a.n_rows; ++i)
-      for (int j = 0; j < a.k; ++j) {
-        if (experts[i * a.k + j] != e) continue;
-        const T* xr = x + i * a.dim_in + a.m.in_off + u * d;
-        const T* gr = grad + i * a.dim_out + a.m.out_off + v * d;
-        T t = 0;
-        for (int m = 0; m < d; ++m) t += xr[m] * gr[m];
-        s += gates[i * a.k + j] * t;
-      }
-    out[e * a.weight_numel + a.m.woff + r] = s;
+struct WgradArgs {
+  int64_t dim_in, dim_out, weight_numel;
+  int64_t max_pieces, group;
+  int64_t slots;  // pieces of all groups, at most
+  int32_t X, k, n_maps;
+  int32_t direct;  // every expert has one piece at most: straight into grad_weights, zeros for those without
+  WgradMap map[kMaxMaps];
+};
+
+constexpr int kStage = 2304;  // channels times rows of a stage, at most
+
+template <int S>
+constexpr int stage_pitch() {  // rows (4 at a time) start 16 banks apart
+  return S == 16 ? 16 : S + 16;
+}
+
+template <class T, int S, bool VEC>
+__global__ __launch_bounds__(256) void k_wgrad(WgradArgs a, const T* __restrict__ x, const T* __restrict__ gates,
+                                               const T* __restrict__ grad, const int32_t* __restrict__ entries,
+                                               const int32_t* __restrict__ first, const int32_t* __restrict__ pieces,
+                                               T* __restrict__ out) {
+  constexpr int P = stage_pitch<S>(), kPer = VEC ? 16 / sizeof(T) : 1;
+  constexpr int kLoads = (kStage / kPer + 255) / 256;  // a thread's loads of a stage and operand
+  constexpr int kTiles = S == 64 ? 2 : 1;
+  constexpr int kRows = kStage / S;
+  __shared__ T xs[kRows * P], gs[kRows * P];
+  __shared__ int64_t at_row[kPiece];
+  __shared__ T at_gate[kPiece];
+  __shared__ int found[2];
+  int mi = 0;
+  while (mi + 1 < a.n_maps && static_cast<int>(blockIdx.x) >= a.map[mi + 1].first) ++mi;
+  const WgradMap m = a.map[mi];
+  const int64_t r = int64_t(blockIdx.x) - m.first;
+  const int64_t slot = r % a.slots;
+  const int uv = static_cast<int>(r / a.slots), u0 = uv / m.nv * S, v0 = uv % m.nv * S;
+  const int64_t grp = slot / a.max_pieces;
+  const int p = static_cast<int>(slot - grp * a.max_pieces);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, d = m.d;
+  const int32_t* const pcs = pieces + grp * (a.X + 1);
+  const int32_t* const fst = first + grp * (a.X + 1);
+  // the piece's expert and entries
+  int e, from, count;
+  if (a.direct) {
+    e = p;
+    from = fst[e];
+    count = fst[e + 1] - from;
+  } else {
+    if (p >= pcs[a.X]) return;
+    if (tid < a.X && pcs[tid] <= p && p < pcs[tid + 1]) {
+      found[0] = tid;
+      found[1] = p - pcs[tid];
+    }
+    __syncthreads();
+    e = found[0];
+    from = fst[e] + found[1] * kPiece;
+    count = min(kPiece, fst[e + 1] - from);
   }
+  if (tid < count) {
+    const int64_t q = entries[grp * a.group * a.k + from + tid];
+    at_row[tid] = q / a.k;
+    at_gate[tid] = gates[q];
+  }
+  __syncthreads();
+
+  // a thread's part of a stage: entry `es`, LDS place of its first element
+  const int ulen = min(S, m.U - u0) * d, vlen = min(S, m.V - v0) * d;
+  auto split = [&](int q, int len, int& es, int& c) {
+    const int idx = (tid + q * 256) * kPer;
+    es = idx / len;
+    c = idx - es * len;
+  };
+  int xe[kLoads], xc[kLoads], ge[kLoads], gc[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    split(q, ulen, xe[q], xc[q]);
+    split(q, vlen, ge[q], gc[q]);
+  }
+  T px[kLoads][kPer], pg[kLoads][kPer];
+  const T* const xb = x + m.in_off + u0 * d;
+  const T* const gb = grad + m.out_off + v0 * d;
+  auto load = [&](int s0) {  // entries s0 .. of the piece; zeros past its end
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int ex = s0 + xe[q], eg = s0 + ge[q];
+      const bool inx = xe[q] < m.per_stage && ex < count, ing = ge[q] < m.per_stage && eg < count;
+      const T g = ing ? at_gate[eg] : T(0);
+      if (VEC) {
+        const Pack<T> a0 = inx ? *reinterpret_cast<const Pack<T>*>(xb + at_row[ex] * a.dim_in + xc[q]) : Pack<T>{};
+        const Pack<T> b0 = ing ? *reinterpret_cast<const Pack<T>*>(gb + at_row[eg] * a.dim_out + gc[q]) : Pack<T>{};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          px[q][j] = a0.v[j];
+          pg[q][j] = b0.v[j] * g;
+        }
+      } else {
+        px[q][0] = inx ? xb[at_row[ex] * a.dim_in + xc[q]] : T(0);
+        pg[q][0] = ing ? gb[at_row[eg] * a.dim_out + gc[q]] * g : T(0);
+      }
+    }
+  };
+  auto store = [&](T* to, int es, int c, const T* v) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int u = (c + j) * m.inv_d >> 16, comp = c + j - u * d;
+      to[(es * d + comp) * P + u] = v[j];
+    }
+  };
+
+  const int i16 = lane & 15, g4 = lane >> 4;
+  const int tu = S == 64 ? (w >> 1) * 32 : (S == 32 ? (w >> 1) * 16 : 0);
+  const int tv = S == 64 ? (w & 1) * 32 : (S == 32 ? (w & 1) * 16 : 0);
+  typename Mfma<T>::Acc acc[kTiles][kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) acc[i][j] = typename Mfma<T>::Acc{0, 0, 0, 0};
+  const int steps = m.per_stage * d / 4;
+  load(0);
+  for (int s0 = 0; s0 < count; s0 += m.per_stage) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      if (xe[q] < m.per_stage) store(xs, xe[q], xc[q], px[q]);
+      if (ge[q] < m.per_stage) store(gs, ge[q], gc[q], pg[q]);
+    }
+    __syncthreads();
+    if (s0 + m.per_stage < count) load(s0 + m.per_stage);
+    for (int st = S == 16 ? w : 0; st < steps; st += S == 16 ? 4 : 1) {
+      const T* xr = xs + (4 * st + g4) * P + tu + i16;
+      const T* gr = gs + (4 * st + g4) * P + tv + i16;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) acc[i][j] = Mfma<T>::step(xr[16 * i], gr[16 * j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+  T* const to = out + (a.direct ? e : slot) * a.weight_numel + m.woff;
+  if (S == 16) {  // the wavefronts' shares of the rows, added in order
+#pragma unroll
+    for (int q = 0; q < 4; ++q) xs[w * 256 + Mfma<T>::row(g4, q) * 16 + i16] = acc[0][0][q];
+    __syncthreads();
+    const int u = u0 + tid / 16, v = v0 + tid % 16;
+    if (u < m.U && v < m.V) to[u * m.V + v] = ((xs[tid] + xs[256 + tid]) + xs[512 + tid]) + xs[768 + tid];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int u = u0 + tu + 16 * i + Mfma<T>::row(g4, q), v = v0 + tv + 16 * j + i16;
+        if (u < m.U && v < m.V) to[u * m.V + v] = acc[i][j][q];
+      }
+}
+
+// Adds what the kernels above left in parts, in order: an expert's pieces
+// (blocks [0, X nw): nw blocks of 256 weights each) and the maps' shares of the
+// gates' gradient (the blocks after them).
+template <class T>
+__global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int n_groups, int64_t max_pieces,
+                                              const int32_t* __restrict__ pieces, const T* __restrict__ part,
+                                              T* __restrict__ out, int64_t n_gates, int n_maps,
+                                              const T* __restrict__ gate_part, T* __restrict__ gate_out) {
+  __shared__ int lo[64], upto[64], list[256];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  if (b >= X * nw) {
+    const int64_t q = int64_t(b - X * nw) * 256 + tid;
+    if (q >= n_gates) return;
+    T s = 0;
+    for (int p = 0; p < n_maps; ++p) s += gate_part[p * n_gates + q];
+    gate_out[q] = s;
+    return;
+  }
+  const int e = b / nw;
+  const int64_t c = int64_t(b - e * nw) * 256 + tid;
+  // pieces of the expert in the groups (64 at most) up to and including each
+  if (tid < 64) {
+    const int64_t at = int64_t(tid) * (X + 1) + e;
+    const int p0 = tid < n_groups ? pieces[at] : 0;
+    int n = tid < n_groups ? pieces[at + 1] - p0 : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(n, o, 64);
+      if (tid >= o) n += t;
+    }
+    lo[tid] = p0;
+    upto[tid] = n;
+  }
+  __syncthreads();
+  const int total = upto[63];
+  T s = 0;
+  for (int q0 = 0; q0 < total; q0 += 256) {
+    const int q = q0 + tid;
+    if (q < total) {
+      int g = 0;  // first group whose count exceeds q
+#pragma unroll
+      for (int step = 32; step > 0; step >>= 1)
+        if (upto[g + step - 1] <= q) g += step;
+      list[tid] = static_cast<int>(g * max_pieces + lo[g] + q - (g > 0 ? upto[g - 1] : 0));
+    }
+    __syncthreads();
+    const int here = min(256, total - q0);
+    if (c < numel) {
+#pragma unroll 8
+      for (int j = 0; j < here; ++j) s += part[list[j] * numel + c];
+    }
+    __syncthreads();
+  }
+  if (c < numel) out[e * numel + c] = s;
 }
 
 // -------------------------------------------------------------------- host
@@ -660,26 +849,108 @@ const int32_t* order_in(const Experts& p, int64_t n, const void* layout) {
   return reinterpret_cast<const int32_t*>(static_cast<const char*>(layout) + L.order);
 }
 
+// Workspace of the backward: the maps' shares of the gates' gradient, then the
+// pieces' matrices.
+struct BackwardSpace {
+  size_t gates, parts, total;
+};
+
+BackwardSpace backward_space(const Experts& p, int64_t n) {
+  const size_t size = p.f64 ? 8 : 4;
+  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
+  BackwardSpace w{};
+  w.parts = align_up(p.maps.size() * n * p.top_k * size);
+  w.total = std::max<size_t>(256, w.parts + align_up(L.n_groups * L.max_pieces * p.weight_numel * size));
+  return w;
+}
+
+template <class T, int S, bool VEC>
+hipError_t wgrad_launch(const WgradArgs& a, int64_t blocks, const T* x, const T* gates, const T* grad,
+                        const int32_t* entries, const int32_t* first, const int32_t* pieces, T* out, hipStream_t s) {
+  hipLaunchKernelGGL((k_wgrad<T, S, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, x, gates, grad,
+                     entries, first, pieces, out);
+  return hipGetLastError();
+}
+
 template <class T>
 hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates,
                     const void* layout, const T* grad, T* gx, T* gw, T* gg, void* ws, hipStream_t s) {
   const int32_t* order = order_in(p, n, layout);
+  const int64_t n_gates = gg != nullptr ? n * p.top_k : 0;
+  const int n_maps = static_cast<int>(p.maps.size()), X = p.n_experts;
+  const BackwardSpace space = backward_space(p, n);
+  T* const gate_part = static_cast<T*>(ws);
   hipError_t he = hipSuccess;
-  if (n > 0 && gg != nullptr) {
-    T* part = static_cast<T*>(ws);
-    he = rows<T, true, true>(p, n, grad, weights, experts, gates, order, gx, x, part, s);
-    const int64_t total = n * p.top_k;
-    hipLaunchKernelGGL(k_gate_sum<T>, dim3(blocks_for(total, 256)), dim3(256), 0, s, total, int(p.maps.size()), part,
-                       gg);
-  } else if (n > 0 && gx != nullptr) {
+  if (n_gates > 0)
+    he = rows<T, true, true>(p, n, grad, weights, experts, gates, order, gx, x, gate_part, s);
+  else if (n > 0 && gx != nullptr)
     he = rows<T, true, false>(p, n, grad, weights, experts, gates, order, gx, nullptr, nullptr, s);
-  }
   if (he != hipSuccess) return he;
-  for (size_t q = 0; gw != nullptr && q < p.maps.size(); ++q) {
-    const MapArgs a{n, p.dim_in, p.dim_out, p.weight_numel, p.n_experts, p.top_k, p.maps[q]};
-    hipLaunchKernelGGL(k_wgrad<T>, dim3(blocks_for(int64_t(a.X) * a.m.mul_in * a.m.mul_out, 256)), dim3(256), 0, s, a,
-                       x, experts, gates, grad, gw);
+  const int64_t gate_blocks = (n_gates + 255) / 256;
+  if (gw == nullptr) {
+    if (gate_blocks > 0)
+      hipLaunchKernelGGL(k_join<T>, dim3(static_cast<unsigned>(gate_blocks)), dim3(256), 0, s, 0, 0, p.weight_numel, 0,
+                         int64_t(0), nullptr, nullptr, nullptr, n_gates, n_maps, gate_part, gg);
+    return hipGetLastError();
   }
+  const LayoutShape L = layout_shape(n, X, p.top_k);
+  const char* const at = static_cast<const char*>(layout);
+  auto ints = [&](size_t off) { return n > 0 ? reinterpret_cast<const int32_t*>(at + off) : nullptr; };
+  WgradArgs a{};
+  a.dim_in = p.dim_in;
+  a.dim_out = p.dim_out;
+  a.weight_numel = p.weight_numel;
+  a.max_pieces = L.max_pieces;
+  a.group = L.group;
+  a.X = X;
+  a.k = p.top_k;
+  a.n_maps = n_maps;
+  // with at most a piece's entries in all, an expert's one piece is its sum
+  a.direct = n * p.top_k <= kPiece;
+  a.slots = a.direct ? X : L.n_groups * L.max_pieces;
+  const int per = 16 / static_cast<int>(sizeof(T));
+  bool vec = aligned16(x) && aligned16(grad) && p.dim_in % per == 0 && p.dim_out % per == 0;
+  int widest = 0;
+  for (const ExpertMap& e : p.maps) {
+    widest = std::max({widest, e.mul_in, e.mul_out});
+    vec = vec && e.in_off % per == 0 && e.out_off % per == 0 && (e.mul_in * e.d) % per == 0 &&
+          (e.mul_out * e.d) % per == 0;
+  }
+  const int S = widest <= 16 ? 16 : (widest <= 32 ? 32 : 64);
+  int64_t blocks = 0;
+  for (int q = 0; q < n_maps; ++q) {
+    const ExpertMap& e = p.maps[q];
+    a.map[q] = WgradMap{e.in_off, e.out_off, e.mul_in, e.mul_out, e.d, e.woff, (e.mul_in + S - 1) / S,
+                        (e.mul_out + S - 1) / S, kStage / S / e.d / 4 * 4, (65536 + e.d - 1) / e.d, 0};
+  }
+  std::sort(a.map, a.map + n_maps, [](const WgradMap& l, const WgradMap& r) {
+    return l.d > r.d;  // long maps first
+  });
+  for (int q = 0; q < n_maps; ++q) {
+    a.map[q].first = static_cast<int32_t>(blocks);
+    blocks += a.slots * a.map[q].nu * a.map[q].nv;
+  }
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  T* const parts = reinterpret_cast<T*>(static_cast<char*>(ws) + space.parts);
+  T* const to = a.direct ? gw : parts;
+  const int32_t *entries = ints(L.entries), *first = ints(L.first), *pcs = ints(L.pieces);
+  if (n > 0) {
+    if (S == 16)
+      he = vec ? wgrad_launch<T, 16, true>(a, blocks, x, gates, grad, entries, first, pcs, to, s)
+               : wgrad_launch<T, 16, false>(a, blocks, x, gates, grad, entries, first, pcs, to, s);
+    else if (S == 32)
+      he = vec ? wgrad_launch<T, 32, true>(a, blocks, x, gates, grad, entries, first, pcs, to, s)
+               : wgrad_launch<T, 32, false>(a, blocks, x, gates, grad, entries, first, pcs, to, s);
+    else
+      he = vec ? wgrad_launch<T, 64, true>(a, blocks, x, gates, grad, entries, first, pcs, to, s)
+               : wgrad_launch<T, 64, false>(a, blocks, x, gates, grad, entries, first, pcs, to, s);
+    if (he != hipSuccess) return he;
+  }
+  const int nw = a.direct && n > 0 ? 0 : static_cast<int>((p.weight_numel + 255) / 256);  // n = 0: zeros
+  if (nw > 0 || gate_blocks > 0)
+    hipLaunchKernelGGL(k_join<T>, dim3(static_cast<unsigned>(int64_t(X) * nw + gate_blocks)), dim3(256), 0, s, X, nw,
+                       p.weight_numel, n > 0 ? static_cast<int>(L.n_groups) : 0, L.max_pieces, pcs, parts, gw, n_gates,
+                       n_maps, gate_part, gg);
   return hipGetLastError();
 }
 
@@ -687,9 +958,7 @@ hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, c
 
 size_t experts_layout_bytes(const Experts& p, int64_t n) { return layout_shape(n, p.n_experts, p.top_k).total; }
 
-size_t experts_workspace(const Experts& p, int64_t n) {
-  return align_up(std::max<size_t>(256, p.maps.size() * n * p.top_k * (p.f64 ? 8 : 4)));
-}
+size_t experts_workspace(const Experts& p, int64_t n) { return backward_space(p, n).total; }
 
 hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* experts, void* layout, int32_t* load,
                                  hipStream_t s) {
@@ -700,7 +969,7 @@ hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* exp
   const int H = std::min(X, kMaxBins / X);
   const int threads = std::min(L.group, n) > 1024 ? 1024 : 256;
   hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(L.n_groups)), dim3(threads), 0, s, n, X, p.top_k, H,
-                     L.group, L.piece, experts, ints(L.order), ints(L.entries), ints(L.first), ints(L.pieces));
+                     L.group, experts, ints(L.order), ints(L.entries), ints(L.first), ints(L.pieces));
   if (load != nullptr) hipLaunchKernelGGL(k_load, dim3(1), dim3(256), 0, s, X, L.n_groups, ints(L.first), load);
   return hipGetLastError();
 }
