@@ -248,8 +248,10 @@ struct RowMap {
   int32_t d, woff;
   int32_t tile;              // rows of a tile, at most 32
   int32_t ld_src, ld_dst;    // LDS elements between a tile's rows
+  int32_t matrix_rows;       // of a tile, at most
   int32_t first;             // first block of this map
   int32_t vec;               // bit 0 / 1: 16-byte aligned rows of src / dst; bit 2: of the weights along K
+  uint32_t inv_src, inv_dst; // ceil(2^32 / pieces of a src / dst segment), 0 for one piece
 };
 
 struct RowArgs {
@@ -258,45 +260,79 @@ struct RowArgs {
   RowMap map[kMaxMaps];
 };
 
-// LDS of a block, in elements of the data type and 32-bit words.
+// LDS of a block (byte offsets), for the map that needs most.
 struct RowLds {
-  size_t src, acc, dot, rowsum, gate, mask, start, list, rows, total;
+  uint32_t src, acc, dot, rowsum, mask, start, list, rtab, rgate, rowid, graw, ents, total;
 };
+
+// Matrix rows of a tile, each expert's rounded up to 16.
+int matrix_rows(int tile, int X, int k, int d) { return tile * k * d + 15 * std::min(X, tile * k); }
 
 RowLds row_lds(const RowMap& m, int X, int k, int waves, bool gg, size_t size) {
   RowLds L{};
-  size_t o = 0;
+  uint32_t o = 0;
   auto take = [&](size_t n, size_t each) {
-    const size_t at = o;
-    o = (o + n * each + 15) / 16 * 16;
+    const uint32_t at = o;
+    o = static_cast<uint32_t>((o + n * each + 15) / 16 * 16);
     return at;
   };
-  const size_t t = m.tile;
+  const size_t t = m.tile, r = matrix_rows(m.tile, X, k, m.d);
   L.src = take(t * m.ld_src, size);
-  L.acc = take(t * m.ld_dst, size);
-  L.dot = take(gg ? t * m.ld_dst : 0, size);
-  L.rowsum = take(gg ? t * k * m.d * waves : 0, size);
-  L.gate = take(t * k, size);
+  L.acc = take((t + 1) * m.ld_dst, size);  // the last row takes what the matrix rows past an expert's last one give
+  L.dot = take(gg ? (t + 1) * m.ld_dst : 0, size);
+  L.rowsum = take(gg ? (t * k * m.d + 1) * waves : 0, size);
   L.mask = take(X, 4);
   L.start = take(X, 4);
-  L.list = take(2 * (t * k + 1), 4);
-  L.rows = take(t * k * m.d, 4);
+  L.list = take(4 * (t * k + 1), 4);
+  L.rtab = take(r, 4);
+  L.rgate = take(r, size);
+  L.rowid = take(t, 8);
+  L.graw = take(t * k, size);
+  L.ents = take(t * k, 4);
   L.total = o;
   return L;
 }
 
-// Rows of `len` elements between global memory (ld apart, picked by row()) and
-// LDS (lds_ld apart): groups of lanes, a power of two, share a row.
-template <class T, class Row, class Move>
-__device__ __forceinline__ void each_piece(int rows, int len, int step, Row row, Move move) {
-  const int pieces = len / step;
-  int lanes = 64;
-  while (lanes > 1 && lanes / 2 >= pieces) lanes >>= 1;
-  const int lane = threadIdx.x & 63, per = 64 / lanes;
-  const int sub = lane & (lanes - 1);
-  for (int s = (threadIdx.x >> 6) * per + lane / lanes; s < rows; s += (blockDim.x >> 6) * per) {
-    const int64_t at = row(s);
-    for (int c = sub; c < pieces; c += lanes) move(s, at, c * step);
+// Sum over the 16 lanes of a row of lanes, in all of them.
+template <int CTRL>
+__device__ __forceinline__ float rotate16(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double rotate16(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, false));
+}
+template <class T>
+__device__ __forceinline__ T sum16(T v) {  // rotations by 8, 4, 2, 1
+  v += rotate16<0x128>(v);
+  v += rotate16<0x124>(v);
+  v += rotate16<0x122>(v);
+  return v + rotate16<0x121>(v);
+}
+
+// Visits the `pieces` pieces of each of `rows` rows, kBatch of them a thread at
+// a time: every load of a batch is issued before the first is waited for (one
+// after the other, a tile of 16 rows took 8 trips to memory).
+constexpr int kBatch = 8;
+
+template <class V, class Load, class Store>
+__device__ __forceinline__ void move_rows(int rows, int pieces, uint32_t inv, Load load, Store store) {
+  const int total = rows * pieces;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * blockDim.x) {
+    V v[kBatch];
+    int s[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * blockDim.x;
+      s[j] = inv != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), inv)) : i;
+      if (i < total) v[j] = load(s[j], i - s[j] * pieces);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * blockDim.x;
+      if (i < total) store(s[j], i - s[j] * pieces, v[j]);
+    }
   }
 }
 
@@ -317,156 +353,192 @@ __global__ __launch_bounds__(256) void k_rows(RowArgs a, RowLds L0, const T* __r
   T* const acc = reinterpret_cast<T*>(lds + L0.acc);
   T* const dot = reinterpret_cast<T*>(lds + L0.dot);
   T* const rowsum = reinterpret_cast<T*>(lds + L0.rowsum);
-  T* const gate = reinterpret_cast<T*>(lds + L0.gate);
   uint32_t* const mask = reinterpret_cast<uint32_t*>(lds + L0.mask);  // members of each expert, a bit per row
-  int* const start = reinterpret_cast<int*>(lds + L0.start);          // their first place in the list of members
-  int* const list = reinterpret_cast<int*>(lds + L0.list);            // the tile's experts: (expert, first place)
-  uint32_t* const rtab = reinterpret_cast<uint32_t*>(lds + L0.rows);  // matrix row -> row, component, place
+  uint32_t* const start = reinterpret_cast<uint32_t*>(lds + L0.start);  // their first place << 16 | matrix row
+  int* const list = reinterpret_cast<int*>(lds + L0.list);  // the tile's experts: expert, first matrix row, rows, place
+  uint32_t* const rtab = reinterpret_cast<uint32_t*>(lds + L0.rtab);  // matrix row -> LDS places in dst << 16 | src
+  T* const rgate = reinterpret_cast<T*>(lds + L0.rgate);
+  int64_t* const rowid = reinterpret_cast<int64_t*>(lds + L0.rowid);
+  T* const graw = reinterpret_cast<T*>(lds + L0.graw);
+  int* const ents = reinterpret_cast<int*>(lds + L0.ents);
 
-  auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
-
-  // the tile's rows, and the list of its experts while they arrive
-  constexpr int kPer = 16 / sizeof(T);
-  const int len = m.K * d, olen = m.N * d;
-  auto stage = [&](const T* from, int64_t ld, int off, int n, bool vec, T* to, int to_ld) {
-    if (vec)
-      each_piece<T>(rows, n, kPer, [&](int s) { return row_of(s) * ld + off; },
-                    [&](int s, int64_t at, int c) {
-                      const Pack<T> p = *reinterpret_cast<const Pack<T>*>(from + at + c);
-#pragma unroll
-                      for (int q = 0; q < kPer; ++q) to[s * to_ld + c + q] = p.v[q];
-                    });
-    else
-      each_piece<T>(rows, n, 1, [&](int s) { return row_of(s) * ld + off; },
-                    [&](int s, int64_t at, int c) { to[s * to_ld + c] = from[at + c]; });
-  };
-  stage(src, a.ld_src, m.src_off, len, m.vec & 1, xs, m.ld_src);
-  if (GG) stage(other, a.ld_dst, m.dst_off, olen, m.vec & 2, dot, m.ld_dst);
-  // channels up to the next multiple of 4 KS are summed over too: zero
-  const int padded = (m.K + 4 * KS - 1) / (4 * KS) * 4 * KS * d;
-  if (padded > len)
-    each_piece<T>(rows, padded - len, 1, [&](int s) { return int64_t(s); },
-                  [&](int s, int64_t, int c) { xs[s * m.ld_src + len + c] = T(0); });
-  for (int q = tid; q < rows * m.ld_dst; q += blockDim.x) acc[q] = T(0);
+  // a thread's entry of the tile (tile * k <= blockDim), read once
+  const int n_entries = rows * k, my_s = tid / k;
+  int64_t my_at = 0;
+  int my_e = -1;
+  T my_g = 0;
+  if (tid < n_entries) {
+    const int64_t row = order != nullptr ? order[base + my_s] : base + my_s;
+    my_at = row * k + (tid - my_s * k);
+    const int e = experts[my_at];
+    my_e = e >= 0 && e < a.X ? e : -1;
+    if (my_e >= 0) my_g = gates[my_at];
+    if (tid == my_s * k) rowid[my_s] = row;
+    ents[tid] = my_e;
+    graw[tid] = my_g;
+  }
   for (int q = tid; q < a.X; q += blockDim.x) mask[q] = 0;
-  if (GG)
-    for (int q = tid; q < a.waves * m.tile * k * d; q += blockDim.x) rowsum[q] = T(0);
-  __syncthreads();
-  const int n_entries = rows * k;
-  auto entry = [&](int q, int& s, int64_t& at) {
-    s = q / k;
-    at = row_of(s) * k + (q - s * k);
-    const int e = experts[at];
-    return e >= 0 && e < a.X ? e : -1;
-  };
-  for (int q = tid; q < n_entries; q += blockDim.x) {
-    int s;
-    int64_t at;
-    const int e = entry(q, s, at);
-    if (e >= 0) atomicOr(&mask[e], 1u << s);
+  const int spare = m.tile * m.ld_dst;
+  for (int q = tid; q < m.matrix_rows; q += blockDim.x) {
+    rtab[q] = uint32_t(spare) << 16;
+    rgate[q] = T(0);
   }
   __syncthreads();
-  // experts present, ascending, with the first place of their members
+  if (my_e >= 0) atomicOr(&mask[my_e], 1u << my_s);
+
+  // the tile's rows
+  constexpr int kPer = 16 / sizeof(T);
+  const int len = m.K * d, olen = m.N * d;
+  auto stage = [&](const T* from, int64_t ld, int n, uint32_t inv, bool vec, T* to, int to_ld) {
+    if (vec)
+      move_rows<Pack<T>>(rows, n / kPer, inv,
+                         [&](int s, int c) { return *reinterpret_cast<const Pack<T>*>(from + rowid[s] * ld + c * kPer); },
+                         [&](int s, int c, const Pack<T>& p) {
+#pragma unroll
+                           for (int q = 0; q < kPer; ++q) to[s * to_ld + c * kPer + q] = p.v[q];
+                         });
+    else
+      move_rows<T>(rows, n, inv, [&](int s, int c) { return from[rowid[s] * ld + c]; },
+                   [&](int s, int c, T v) { to[s * to_ld + c] = v; });
+  };
+  stage(src + m.src_off, a.ld_src, len, m.inv_src, m.vec & 1, xs, m.ld_src);
+  if (GG) stage(other + m.dst_off, a.ld_dst, olen, m.inv_dst, m.vec & 2, dot, m.ld_dst);
+  // channels up to the next multiple of 4 KS are summed over too: zero
+  const int padded = (m.K + 4 * KS - 1) / (4 * KS) * 4 * KS * d;
+  for (int s = w; s < rows && padded > len; s += a.waves)
+    for (int c = len + lane; c < padded; c += 64) xs[s * m.ld_src + c] = T(0);
+  for (int q = tid; q < rows * m.ld_dst; q += blockDim.x) acc[q] = T(0);
+  const int sums = m.tile * k * d + 1;  // a wavefront's sums of the gates' gradient, and a spare place
+  if (GG)
+    for (int q = tid; q < a.waves * sums; q += blockDim.x) rowsum[q] = T(0);
+  __syncthreads();
+  // experts present, ascending: places (members before) and matrix rows before, summed as one word
   if (w == 0) {
-    int n_here = 0, places = 0;
+    int n_here = 0;
+    uint32_t before = 0;
     for (int e0 = 0; e0 < a.X; e0 += 64) {
-      const uint32_t mk = e0 + lane < a.X ? mask[e0 + lane] : 0;
-      const int c = __popc(mk);
-      int s = c;
+      const uint32_t c = __popc(e0 + lane < a.X ? mask[e0 + lane] : 0);
+      const uint32_t mine = c << 16 | ((c * d + 15) & ~15u);
+      uint32_t s = mine;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const int t = __shfl_up(s, o, 64);
+        const uint32_t t = __shfl_up(s, o, 64);
         if (lane >= o) s += t;
       }
+      const uint32_t at = before + s - mine;
       const uint64_t here = __ballot(c > 0);
       if (c > 0) {
-        const int j = n_here + __popcll(here & ((uint64_t(1) << lane) - 1));
-        list[2 * j] = e0 + lane;
-        list[2 * j + 1] = places + s - c;
+        int* const to = list + 4 * (n_here + __popcll(here & ((uint64_t(1) << lane) - 1)));
+        to[0] = e0 + lane;
+        to[1] = at & 0xFFFF;
+        to[2] = c * d;
+        to[3] = at >> 16;
       }
-      if (e0 + lane < a.X) start[e0 + lane] = places + s - c;
-      places += __shfl(s, 63, 64);
+      if (e0 + lane < a.X) start[e0 + lane] = at;
+      before += __shfl(s, 63, 64);
       n_here += __popcll(here);
     }
-    if (lane == 0) {
-      list[2 * n_here] = -1;
-      list[2 * n_here + 1] = places;
-    }
+    if (lane == 0) list[4 * n_here] = -1;
   }
   __syncthreads();
   // members' gates (an expert that stands twice in a row: their sum) and matrix rows
-  for (int q = tid; q < n_entries; q += blockDim.x) {
-    int s;
-    int64_t at;
-    const int e = entry(q, s, at);
-    if (e < 0) continue;
-    const int64_t r0 = at - (q - s * k);
+  int my_place = 0;
+  if (my_e >= 0) {
     bool leads = true;
     T g = 0;
-    for (int b = 0; b < k; ++b)
-      if (experts[r0 + b] == e) {
-        leads = leads && r0 + b >= at;
-        g += gates[r0 + b];
+    for (int b = 0; b < k; ++b) {
+      const int q = my_s * k + b;
+      if (ents[q] == my_e) {
+        leads = leads && q >= tid;
+        g += graw[q];
       }
-    if (!leads) continue;
-    const int place = start[e] + __popc(mask[e] & ((1u << s) - 1));
-    gate[place] = g;
-    for (int c = 0; c < d; ++c) rtab[place * d + c] = uint32_t(place) << 16 | uint32_t(s) << 8 | uint32_t(c);
+    }
+    const uint32_t at = start[my_e], nth = __popc(mask[my_e] & ((1u << my_s) - 1));
+    my_place = (at >> 16) + nth;
+    if (leads) {
+      const int r = (at & 0xFFFF) + nth * d;
+      for (int c = 0; c < d; ++c) {
+        rtab[r + c] = uint32_t(my_s * m.ld_dst + c) << 16 | uint32_t(my_s * m.ld_src + c);
+        rgate[r + c] = g;
+      }
+    }
   }
   __syncthreads();
 
-  // each wavefront: 16 output channels, all experts of the tile
+  // each wavefront: 16 output channels, all experts of the tile, the next
+  // expert's weights on their way while one's are in use
   const int i16 = lane & 15, g4 = lane >> 4;
+  T* const my_sums = GG ? rowsum + w * sums : nullptr;
   for (int n0 = w * 16; n0 < m.N; n0 += a.waves * 16) {
-    const int col = n0 + i16;
-    const bool col_in = col < m.N;
+    const int col = min(n0 + i16, m.N - 1);  // a lane past the last channel fills a column that is not written
+    const int to = (n0 + i16) * d;
     for (int k0 = 0; k0 < m.K; k0 += 4 * KS) {
-      for (int j = 0; list[2 * j] >= 0; ++j) {
-        const int e = __builtin_amdgcn_readfirstlane(list[2 * j]);
-        const int p0 = list[2 * j + 1], p1 = list[2 * j + 3];
-        // lane's channels of the sum: k0 + g4 KS + 0 .. KS-1
+      const int kk = k0 + g4 * KS;  // lane's channels of the sum: kk .. kk + KS - 1
+      const bool full = k0 + 4 * KS <= m.K;
+      auto load_weights = [&](int e, T* b) {  // zero past the last channel of the sum
         const T* wp = weights + e * a.weight_numel + m.woff;
-        T b[KS];
-        const int kk = k0 + g4 * KS;
         if (ADJ) {
-          const T* row = wp + int64_t(col_in ? col : 0) * m.V + kk;
-          if (KS >= kPer && (m.vec & 4)) {
+          const T* row = wp + col * m.V;
+          if (KS >= kPer && full && (m.vec & 4)) {
 #pragma unroll
             for (int s = 0; s < KS; s += kPer) {
-              const bool in = col_in && kk + s < m.K;  // K is a multiple of the vector here
-              const Pack<T> p = in ? *reinterpret_cast<const Pack<T>*>(row + s) : Pack<T>{};
+              const Pack<T> p = *reinterpret_cast<const Pack<T>*>(row + kk + s);
 #pragma unroll
               for (int q = 0; q < kPer; ++q) b[s + q] = p.v[q];
             }
           } else {
 #pragma unroll
-            for (int s = 0; s < KS; ++s) b[s] = col_in && kk + s < m.K ? row[s] : T(0);
+            for (int s = 0; s < KS; ++s) b[s] = row[min(kk + s, m.K - 1)];
           }
+        } else if (full) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) b[s] = wp[(kk + s) * m.V + col];
         } else {
-          const T* at = wp + int64_t(kk) * m.V + col;
 #pragma unroll
-          for (int s = 0; s < KS; ++s) b[s] = col_in && kk + s < m.K ? at[int64_t(s) * m.V] : T(0);
+          for (int s = 0; s < KS; ++s) b[s] = wp[min(kk + s, m.K - 1) * m.V + col];
         }
-        const int r_end = p1 * d;
-        for (int r = p0 * d; r < r_end; r += 16) {
-          const uint32_t me = rtab[min(r + i16, r_end - 1)];
-          const T* ap = xs + ((me >> 8) & 255) * m.ld_src + (me & 255) + kk * d;
-          typename Mfma<T>::Acc acc4 = {0, 0, 0, 0};
+      };
+      T b[KS], next[KS];
+      int e = __builtin_amdgcn_readfirstlane(list[0]);
+      if (e >= 0) load_weights(e, next);
+      for (int j = 0; e >= 0; ++j) {
 #pragma unroll
-          for (int s = 0; s < KS; ++s) acc4 = Mfma<T>::step(ap[s * d], b[s], acc4);
+        for (int s = 0; s < KS; ++s) b[s] = full || kk + s < m.K ? next[s] : T(0);
+        e = __builtin_amdgcn_readfirstlane(list[4 * j + 4]);
+        if (e >= 0) load_weights(e, next);
+        const int r0 = __builtin_amdgcn_readfirstlane(list[4 * j + 1]);
+        const int n_rows = __builtin_amdgcn_readfirstlane(list[4 * j + 2]);
+        const int place = __builtin_amdgcn_readfirstlane(list[4 * j + 3]) * d;
+        for (int r = 0; r < n_rows; r += 16) {
+          const T* ap = xs + (rtab[r0 + r + i16] & 0xFFFF) + kk * d;
+          T av[KS];
+#pragma unroll
+          for (int s = 0; s < KS; ++s) av[s] = ap[s * d];
+          int at[4];
+          T gate[4], sofar[4], other_row[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int rr = r + Mfma<T>::row(g4, q);
-            const bool live = rr < r_end && col_in;
-            const uint32_t t = rtab[min(rr, r_end - 1)];
-            const int at = ((t >> 8) & 255) * m.ld_dst + (col_in ? col : 0) * d + (t & 255);
-            if (GG) {
-              T v = live ? acc4[q] * dot[at] : T(0);
+            const int rr = r0 + r + Mfma<T>::row(g4, q);
+            at[q] = static_cast<int>(rtab[rr] >> 16) + to;
+            gate[q] = rgate[rr];
+          }
 #pragma unroll
-              for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 16);
-              if (i16 == 0 && rr < r_end) rowsum[w * (m.tile * k * d) + rr] += v;
+          for (int q = 0; q < 4; ++q) {
+            sofar[q] = acc[at[q]];
+            if (GG) other_row[q] = dot[at[q]];
+          }
+          typename Mfma<T>::Acc prod = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[at[q]] = sofar[q] + gate[q] * prod[q];
+          if (GG) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int rr = r + Mfma<T>::row(g4, q);
+              const T v = sum16(n0 + i16 < m.N ? prod[q] * other_row[q] : T(0));
+              if (i16 == 0) my_sums[rr < n_rows ? place + rr : sums - 1] += v;
             }
-            if (live) acc[at] += gate[t >> 16] * acc4[q];
           }
         }
       }
@@ -474,31 +546,28 @@ __global__ __launch_bounds__(256) void k_rows(RowArgs a, RowLds L0, const T* __r
   }
   __syncthreads();
   if (dst != nullptr) {
+    T* const to = dst + m.dst_off;
     if (m.vec & 2)
-      each_piece<T>(rows, olen, kPer, [&](int s) { return row_of(s) * a.ld_dst + m.dst_off; },
-                    [&](int s, int64_t at, int c) {
-                      Pack<T> p;
+      move_rows<Pack<T>>(rows, olen / kPer, m.inv_dst,
+                         [&](int s, int c) {
+                           Pack<T> p;
 #pragma unroll
-                      for (int q = 0; q < kPer; ++q) p.v[q] = acc[s * m.ld_dst + c + q];
-                      *reinterpret_cast<Pack<T>*>(dst + at + c) = p;
-                    });
+                           for (int q = 0; q < kPer; ++q) p.v[q] = acc[s * m.ld_dst + c * kPer + q];
+                           return p;
+                         },
+                         [&](int s, int c, const Pack<T>& p) {
+                           *reinterpret_cast<Pack<T>*>(to + rowid[s] * a.ld_dst + c * kPer) = p;
+                         });
     else
-      each_piece<T>(rows, olen, 1, [&](int s) { return row_of(s) * a.ld_dst + m.dst_off; },
-                    [&](int s, int64_t at, int c) { dst[at + c] = acc[s * m.ld_dst + c]; });
+      move_rows<T>(rows, olen, m.inv_dst, [&](int s, int c) { return acc[s * m.ld_dst + c]; },
+                   [&](int s, int c, T v) { to[rowid[s] * a.ld_dst + c] = v; });
   }
-  if (GG) {
-    for (int q = tid; q < n_entries; q += blockDim.x) {
-      int s;
-      int64_t at;
-      const int e = entry(q, s, at);
-      T v = 0;
-      if (e >= 0) {
-        const int place = start[e] + __popc(mask[e] & ((1u << s) - 1));
-        for (int ww = 0; ww < a.waves; ++ww)
-          for (int c = 0; c < d; ++c) v += rowsum[ww * (m.tile * k * d) + place * d + c];
-      }
-      gate_part[mi * (a.n_rows * k) + at] = v;
-    }
+  if (GG && tid < n_entries) {
+    T v = 0;
+    if (my_e >= 0)
+      for (int ww = 0; ww < a.waves; ++ww)
+        for (int c = 0; c < d; ++c) v += rowsum[ww * sums + my_place * d + c];
+    gate_part[mi * (a.n_rows * k) + my_at] = v;
   }
 }
 
@@ -790,12 +859,13 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
   const int KS = maxK <= 16 ? 4 : (maxK <= 32 ? 8 : 16);
   a.waves = std::min(4, (maxN + 15) / 16);
   // Tile: as many rows (32 at most: a bit each) as leave LDS for 8 wavefronts
-  // on a CU, 20 KiB for each of the block's; one row at least.  With few rows
+  // on a CU, 20 KiB for each of the block's; a thread for each entry, one row
+  // at least.  With few rows
   // the tiles are made smaller, to have two blocks for each of the 256 CUs.
   std::sort(a.map, a.map + a.n_maps, [](const RowMap& x, const RowMap& y) {
     return int64_t(x.K) * x.N * x.d > int64_t(y.K) * y.N * y.d;  // long maps first
   });
-  RowLds L{};
+  uint32_t region[sizeof(RowLds) / 4] = {};
   const int64_t spread = std::max<int64_t>(1, n * a.n_maps / 512);
   int64_t blocks = 0;
   for (int q = 0; q < a.n_maps; ++q) {
@@ -806,30 +876,30 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
       return full + ((want - full) % 64 + 64) % 64;
     };
     m.ld_src = pitch((m.K + 4 * KS - 1) / (4 * KS) * 4 * KS);
-    m.ld_dst = pitch(m.N);
-    for (m.tile = 32; m.tile > 1; --m.tile)
-      if (m.tile <= spread && row_lds(m, a.X, a.k, a.waves, GG, sizeof(T)).total <= size_t(20480) * a.waves) break;
+    m.ld_dst = pitch((m.N + 15) / 16 * 16);
+    auto inverse = [](int pieces) { return pieces > 1 ? uint32_t((0xFFFFFFFFull + pieces) / pieces) : 0u; };
+    m.inv_src = inverse(m.K * m.d / (m.vec & 1 ? per : 1));
+    m.inv_dst = inverse(m.N * m.d / (m.vec & 2 ? per : 1));
+    RowLds one{};
+    for (m.tile = std::min(32, 64 * a.waves / a.k); m.tile > 1; --m.tile) {
+      one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
+      if (m.tile <= spread && one.total <= 20480u * a.waves) break;
+    }
+    one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
+    m.matrix_rows = matrix_rows(m.tile, a.X, a.k, m.d);
     m.first = static_cast<int32_t>(blocks);
     blocks += (n + m.tile - 1) / m.tile;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    const RowLds one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
     // one launch for all maps: each region as large as the map that needs most
-    auto grow = [](size_t& x, size_t y) { x = std::max(x, y); };
-    grow(L.acc, one.acc - one.src);
-    grow(L.dot, one.dot - one.acc);
-    grow(L.rowsum, one.rowsum - one.dot);
-    grow(L.gate, one.gate - one.rowsum);
-    grow(L.mask, one.mask - one.gate);
-    grow(L.start, one.start - one.mask);
-    grow(L.list, one.list - one.start);
-    grow(L.rows, one.rows - one.list);
-    grow(L.total, one.total - one.rows);
+    for (size_t f = 0; f < sizeof(RowLds) / 4; ++f) {
+      const uint32_t* const from = reinterpret_cast<const uint32_t*>(&one) + f;
+      region[f] = std::max(region[f], f > 0 ? from[0] - from[-1] : 0u);
+    }
   }
-  // sizes to offsets
-  size_t o = 0;
-  for (size_t* at : {&L.acc, &L.dot, &L.rowsum, &L.gate, &L.mask, &L.start, &L.list, &L.rows, &L.total}) {
-    o += *at;
-    *at = o;
+  RowLds L{};  // the regions' sizes, to offsets
+  for (size_t f = 1; f < sizeof(RowLds) / 4; ++f) {
+    uint32_t* const at = reinterpret_cast<uint32_t*>(&L) + f;
+    at[0] = at[-1] + region[f];
   }
   if (L.total > 160 * 1024) return hipErrorInvalidValue;
   for (const ColumnRun& r : ADJ ? p.bare_in : p.bare_out)
