@@ -64,7 +64,7 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 //   piece    [group][X + 1] the same in pieces of at most kPiece entries
 constexpr int64_t kGroup = 2048;
 constexpr int kMaxBins = 4096;
-constexpr int kPiece = 256;
+constexpr int kPiece = 128;
 
 struct LayoutShape {
   int64_t group, n_groups;
@@ -231,67 +231,49 @@ __global__ void k_load(int X, int64_t n_groups, const int32_t* __restrict__ firs
 }
 
 // ----------------------------------------------------- rows: out and grad_x
-// A block takes a tile of rows (in the layout's order) and one map: the tile's
-// segment goes to LDS once, the tile's experts are listed with their member
-// rows, and for each expert the members' (row, component) pairs are packed
-// into 16-row matrix tiles, so a tile that meets many experts still fills the
-// matrix cores.  The products, times the gates, are added into the tile's
-// output in LDS, which is written once: x is read once and out written once
-// whatever top_k, and each row's sum runs over its experts in ascending order.
-// A wavefront owns 16 output channels at a time, so no two wavefronts add into
-// the same place.  ADJ runs the transposed maps on grad_out; GG also dots the
-// ungated products with x for the gates' gradient (a partial sum per map).
+// A block takes a tile of up to 16 rows (in the layout's order), one map and up
+// to 64 of its output channels, and lists the tile's experts with their member
+// rows.  The tile's (row, component) pairs are its matrix rows, 16 at a time:
+// 2l+1 chunks.
+// The segment goes to LDS with the channels apart ([channel][matrix row], so
+// that every read of the loop is one address register and a constant), the
+// chunks' sums stay in registers, and for each expert of the tile the chunks
+// that hold one of its rows are multiplied, the rows scaled by their gates
+// (0 where a row is not the expert's).  So x is read once, out is written once
+// whatever top_k, and a row's sum runs over its experts in ascending order.
+// The next expert's weights are on their way while one's are in use.  A
+// wavefront owns 16 output channels.  ADJ runs the transposed maps on grad_out
+// and applies the gate after the product, which GG dots with x before that for
+// the gates' gradient.
+constexpr int kTile = 16;
+
 struct RowMap {
   int32_t src_off, dst_off;  // first columns in a row of src / dst
   int32_t K, N;              // channels summed over / produced
   int32_t V;                 // row length of the map's weights
   int32_t d, woff;
-  int32_t tile;              // rows of a tile, at most 32
-  int32_t ld_src, ld_dst;    // LDS elements between a tile's rows
-  int32_t matrix_rows;       // of a tile, at most
-  int32_t first;             // first block of this map
-  int32_t vec;               // bit 0 / 1: 16-byte aligned rows of src / dst; bit 2: of the weights along K
-  uint32_t inv_src, inv_dst; // ceil(2^32 / pieces of a src / dst segment), 0 for one piece
+  int32_t packed;            // bit 0: 16-byte pieces of src, bit 1: of dst, bit 2: of the weights along K
+  int32_t first;             // first share (a map's block of output channels) of this map
+};
+
+// LDS of a block (byte offsets)
+struct RowLds {
+  uint32_t tile, gates, mask, start, list, rows, graw, grow, esum, wsum, rsum, ents, total;
 };
 
 struct RowArgs {
   int64_t n_rows, ld_src, ld_dst, weight_numel;
   int32_t X, k, n_maps, waves;
+  int32_t tile;       // rows of a tile, at most kTile
+  int32_t n_tiles;
+  RowLds lds;
   RowMap map[kMaxMaps];
 };
 
-// LDS of a block (byte offsets), for the map that needs most.
-struct RowLds {
-  uint32_t src, acc, dot, rowsum, mask, start, list, rtab, rgate, rowid, graw, ents, total;
-};
-
-// Matrix rows of a tile, each expert's rounded up to 16.
-int matrix_rows(int tile, int X, int k, int d) { return tile * k * d + 15 * std::min(X, tile * k); }
-
-RowLds row_lds(const RowMap& m, int X, int k, int waves, bool gg, size_t size) {
-  RowLds L{};
-  uint32_t o = 0;
-  auto take = [&](size_t n, size_t each) {
-    const uint32_t at = o;
-    o = static_cast<uint32_t>((o + n * each + 15) / 16 * 16);
-    return at;
-  };
-  const size_t t = m.tile, r = matrix_rows(m.tile, X, k, m.d);
-  L.src = take(t * m.ld_src, size);
-  L.acc = take((t + 1) * m.ld_dst, size);  // the last row takes what the matrix rows past an expert's last one give
-  L.dot = take(gg ? (t + 1) * m.ld_dst : 0, size);
-  L.rowsum = take(gg ? (t * k * m.d + 1) * waves : 0, size);
-  L.mask = take(X, 4);
-  L.start = take(X, 4);
-  L.list = take(4 * (t * k + 1), 4);
-  L.rtab = take(r, 4);
-  L.rgate = take(r, size);
-  L.rowid = take(t, 8);
-  L.graw = take(t * k, size);
-  L.ents = take(t * k, 4);
-  L.total = o;
-  return L;
-}
+// Matrix rows of a tile are D runs of 16; a channel's row of them is padded to
+// 4 more than a multiple of 16, which puts the four channels that a matrix
+// instruction reads 16 banks apart.
+constexpr int pitch_of(int d) { return 16 * d + 4; }
 
 // Sum over the 16 lanes of a row of lanes, in all of them.
 template <int CTRL>
@@ -311,264 +293,356 @@ __device__ __forceinline__ T sum16(T v) {  // rotations by 8, 4, 2, 1
   return v + rotate16<0x121>(v);
 }
 
-// Visits the `pieces` pieces of each of `rows` rows, kBatch of them a thread at
-// a time: every load of a batch is issued before the first is waited for (one
-// after the other, a tile of 16 rows took 8 trips to memory).
-constexpr int kBatch = 8;
-
-template <class V, class Load, class Store>
-__device__ __forceinline__ void move_rows(int rows, int pieces, uint32_t inv, Load load, Store store) {
-  const int total = rows * pieces;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * blockDim.x) {
-    V v[kBatch];
-    int s[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = i0 + j * blockDim.x;
-      s[j] = inv != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), inv)) : i;
-      if (i < total) v[j] = load(s[j], i - s[j] * pieces);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = i0 + j * blockDim.x;
-      if (i < total) store(s[j], i - s[j] * pieces, v[j]);
-    }
-  }
+// A value the compiler takes for new: what is computed from it stays where it
+// is used (kept from one phase to the next, places in LDS took 60 registers).
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
-template <class T, int KS, bool ADJ, bool GG>
-__global__ __launch_bounds__(256) void k_rows(RowArgs a, RowLds L0, const T* __restrict__ src,
-                                              const T* __restrict__ weights, const int32_t* __restrict__ experts,
-                                              const T* __restrict__ gates, const int32_t* __restrict__ order,
-                                              T* __restrict__ dst, const T* __restrict__ other,
-                                              T* __restrict__ gate_part) {
-  extern __shared__ char lds[];
-  int mi = 0;
-  while (mi + 1 < a.n_maps && static_cast<int>(blockIdx.x) >= a.map[mi + 1].first) ++mi;
-  const RowMap m = a.map[mi];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, k = a.k, d = m.d;
-  const int64_t base = int64_t(static_cast<int>(blockIdx.x) - m.first) * m.tile;
-  const int rows = static_cast<int>(min<int64_t>(m.tile, a.n_rows - base));
-  T* const xs = reinterpret_cast<T*>(lds + L0.src);
-  T* const acc = reinterpret_cast<T*>(lds + L0.acc);
-  T* const dot = reinterpret_cast<T*>(lds + L0.dot);
-  T* const rowsum = reinterpret_cast<T*>(lds + L0.rowsum);
-  uint32_t* const mask = reinterpret_cast<uint32_t*>(lds + L0.mask);  // members of each expert, a bit per row
-  uint32_t* const start = reinterpret_cast<uint32_t*>(lds + L0.start);  // their first place << 16 | matrix row
-  int* const list = reinterpret_cast<int*>(lds + L0.list);  // the tile's experts: expert, first matrix row, rows, place
-  uint32_t* const rtab = reinterpret_cast<uint32_t*>(lds + L0.rtab);  // matrix row -> LDS places in dst << 16 | src
-  T* const rgate = reinterpret_cast<T*>(lds + L0.rgate);
-  int64_t* const rowid = reinterpret_cast<int64_t*>(lds + L0.rowid);
-  T* const graw = reinterpret_cast<T*>(lds + L0.graw);
-  int* const ents = reinterpret_cast<int*>(lds + L0.ents);
+// The tile's rows of a segment of n channels (CH at most), global <-> LDS:
+// element c of row s is [c / D][s D + c % D] there.  A wavefront takes whole
+// rows, several at a time where they are short, kBatch pieces in flight.
+constexpr int kBatch = 8;
 
-  // a thread's entry of the tile (tile * k <= blockDim), read once
-  const int n_entries = rows * k, my_s = tid / k;
-  int64_t my_at = 0;
-  int my_e = -1;
-  T my_g = 0;
-  if (tid < n_entries) {
-    const int64_t row = order != nullptr ? order[base + my_s] : base + my_s;
-    my_at = row * k + (tid - my_s * k);
-    const int e = experts[my_at];
-    my_e = e >= 0 && e < a.X ? e : -1;
-    if (my_e >= 0) my_g = gates[my_at];
-    if (tid == my_s * k) rowid[my_s] = row;
-    ents[tid] = my_e;
-    graw[tid] = my_g;
+template <class T, int D, int CH, int PER>
+struct TileMover {
+  static constexpr int kPieces = CH * D / PER;
+  static constexpr int lanes() {
+    int l = 1;
+    while (l < 64 && l < kPieces) l *= 2;
+    return l;
   }
-  for (int q = tid; q < a.X; q += blockDim.x) mask[q] = 0;
-  const int spare = m.tile * m.ld_dst;
-  for (int q = tid; q < m.matrix_rows; q += blockDim.x) {
-    rtab[q] = uint32_t(spare) << 16;
-    rgate[q] = T(0);
-  }
-  __syncthreads();
-  if (my_e >= 0) atomicOr(&mask[my_e], 1u << my_s);
+  static constexpr int kLanes = lanes(), kRows = 64 / kLanes, kSteps = (kPieces + 63) / 64;
+  static constexpr int P = pitch_of(D);
 
-  // the tile's rows
-  constexpr int kPer = 16 / sizeof(T);
-  const int len = m.K * d, olen = m.N * d;
-  auto stage = [&](const T* from, int64_t ld, int n, uint32_t inv, bool vec, T* to, int to_ld) {
-    if (vec)
-      move_rows<Pack<T>>(rows, n / kPer, inv,
-                         [&](int s, int c) { return *reinterpret_cast<const Pack<T>*>(from + rowid[s] * ld + c * kPer); },
-                         [&](int s, int c, const Pack<T>& p) {
+  // c / D as a 24-bit product (c < 64 D): 32-bit ones, which a division compiles to, run at a quarter of the rate
+  static __device__ __forceinline__ int place(int s, int c) {
+    return __mul24(__umul24(c, (65536 + D - 1) / D) >> 16, P - D) + __mul24(s, D) + c;
+  }
+
+  // (row, first element) of a lane's q-th piece; false where there is none
+  static __device__ __forceinline__ bool piece(int tid, int q, int rows, int pieces, int waves, int& s, int& c) {
+    const int lane = tid & 63;
+    s = (q / kSteps * waves + (tid >> 6)) * kRows + lane / kLanes;
+    c = q % kSteps * 64 + lane % kLanes;
+    const bool in = s < rows && c < pieces;
+    s = min(s, rows - 1);
+    c = min(c, pieces - 1) * PER;
+    return in;
+  }
+  static __device__ __forceinline__ int trips(int rows, int waves) {
+    return (rows + waves * kRows - 1) / (waves * kRows) * kSteps;
+  }
+
+  T v[kBatch][PER];
+
+  // a batch of pieces, from the q0-th on
+  __device__ __forceinline__ void issue(int q0, const T* from, const int64_t* start, int rows, int n, int waves) {
+    const int tid = fresh(threadIdx.x);
 #pragma unroll
-                           for (int q = 0; q < kPer; ++q) to[s * to_ld + c * kPer + q] = p.v[q];
-                         });
-    else
-      move_rows<T>(rows, n, inv, [&](int s, int c) { return from[rowid[s] * ld + c]; },
-                   [&](int s, int c, T v) { to[s * to_ld + c] = v; });
-  };
-  stage(src + m.src_off, a.ld_src, len, m.inv_src, m.vec & 1, xs, m.ld_src);
-  if (GG) stage(other + m.dst_off, a.ld_dst, olen, m.inv_dst, m.vec & 2, dot, m.ld_dst);
-  // channels up to the next multiple of 4 KS are summed over too: zero
-  const int padded = (m.K + 4 * KS - 1) / (4 * KS) * 4 * KS * d;
-  for (int s = w; s < rows && padded > len; s += a.waves)
-    for (int c = len + lane; c < padded; c += 64) xs[s * m.ld_src + c] = T(0);
-  for (int q = tid; q < rows * m.ld_dst; q += blockDim.x) acc[q] = T(0);
-  const int sums = m.tile * k * d + 1;  // a wavefront's sums of the gates' gradient, and a spare place
-  if (GG)
-    for (int q = tid; q < a.waves * sums; q += blockDim.x) rowsum[q] = T(0);
+    for (int j = 0; j < kBatch; ++j) {
+      int s, c;
+      piece(tid, q0 + j, rows, n * D / PER, waves, s, c);
+      const T* at = from + start[s] + c;
+      if constexpr (PER > 1) {
+        const Pack<T> p = *reinterpret_cast<const Pack<T>*>(at);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[j][e] = p.v[e];
+      } else {
+        v[j][0] = *at;
+      }
+    }
+  }
+  // puts the first batch, issued before, into LDS, and fetches what it left
+  __device__ __forceinline__ void finish(T* lds, const T* from, const int64_t* start, int rows, int n, int waves) {
+    for (int q0 = 0;;) {
+      const int tid = fresh(threadIdx.x);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        int s, c;
+        if (piece(tid, q0 + j, rows, n * D / PER, waves, s, c))
+#pragma unroll
+          for (int e = 0; e < PER; ++e) lds[place(s, c + e)] = v[j][e];
+      }
+      q0 += kBatch;
+      if (q0 >= trips(rows, waves)) break;
+      issue(q0, from, start, rows, n, waves);
+    }
+  }
+
+  static __device__ __forceinline__ void store(const T* lds, T* to, const int64_t* start, int rows, int n,
+                                               int waves) {
+    const int tid = fresh(threadIdx.x);
+    for (int q = 0; q < trips(rows, waves); ++q) {
+      int s, c;
+      if (!piece(tid, q, rows, n * D / PER, waves, s, c)) continue;
+      T* const at = to + start[s] + c;
+      if constexpr (PER > 1) {
+        Pack<T> p;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) p.v[e] = lds[place(s, c + e)];
+        *reinterpret_cast<Pack<T>*>(at) = p;
+      } else {
+        *at = lds[place(s, c)];
+      }
+    }
+  }
+};
+
+// One block's work on a map of components D, the rows' starts being in LDS.
+// KS: channels summed over in a pass / 4; VS, VD: 16-byte pieces of src / dst.
+template <class T, int D, int KS, bool ADJ, bool GG, bool VS, bool VD>
+__device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int share, int64_t base, int rows,
+                                         char* lds, const T* __restrict__ src, const T* __restrict__ weights,
+                                         const int32_t* __restrict__ experts, const T* __restrict__ gates,
+                                         const int32_t* __restrict__ order, T* __restrict__ dst,
+                                         const T* __restrict__ other, T* __restrict__ gate_part) {
+  constexpr int kPer = 16 / sizeof(T), CH = 4 * KS, P = pitch_of(D);
+  using Acc = typename Mfma<T>::Acc;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, k = a.k;
+  const int i16 = lane & 15, g4 = lane >> 4;
+  T* const xs = reinterpret_cast<T*>(lds + a.lds.tile);
+  T* const gtab = reinterpret_cast<T*>(lds + a.lds.gates);  // gate of each expert of the tile and row
+  uint32_t* const mask = reinterpret_cast<uint32_t*>(lds + a.lds.mask);  // members of each expert, a bit per row
+  int* const start = reinterpret_cast<int*>(lds + a.lds.start);          // each expert's place in the list
+  int* const list = reinterpret_cast<int*>(lds + a.lds.list);  // the tile's experts: expert, members' bits, members before
+  const int64_t* const src_row = reinterpret_cast<const int64_t*>(lds + a.lds.rows);
+  const int64_t* const dst_row = src_row + kTile;
+  T* const graw = reinterpret_cast<T*>(lds + a.lds.graw);
+  int* const ents = reinterpret_cast<int*>(lds + a.lds.ents);
+  T* const grow = reinterpret_cast<T*>(lds + a.lds.grow) + w * 16 * 9;  // a wavefront's gates of one expert's matrix rows
+  T* const esum = reinterpret_cast<T*>(lds + a.lds.esum);  // GG: entries' sums; each wavefront's; a wavefront's rows
+  T* const wsum = reinterpret_cast<T*>(lds + a.lds.wsum);
+  T* const rsum = reinterpret_cast<T*>(lds + a.lds.rsum) + w * 16 * 9;
+
+  // the rows are on their way while the tile's experts are listed
+  const int n_base = (share - m.first) * 16 * a.waves, n_here = min(16 * a.waves, m.N - n_base);
+  TileMover<T, D, CH, VS ? kPer : 1> mover;
+  TileMover<T, D, 64, VD ? kPer : 1> mover_dst;
+  const T* const src_from = src + m.src_off;
+  const T* const other_from = GG ? other + m.dst_off + n_base * D : nullptr;
+  if (GG) mover_dst.issue(0, other_from, dst_row, rows, n_here, a.waves);
+  mover.issue(0, src_from, src_row, rows, min(CH, m.K), a.waves);
+
+  const int n_entries = rows * k;
+  for (int q = tid; q < n_entries; q += blockDim.x)
+    if (ents[q] >= 0) atomicOr(&mask[ents[q]], 1u << (q / k));
   __syncthreads();
-  // experts present, ascending: places (members before) and matrix rows before, summed as one word
-  if (w == 0) {
-    int n_here = 0;
-    uint32_t before = 0;
+  if (w == 0) {  // experts present, ascending, and the members before each
+    int n_experts = 0, places = 0;
     for (int e0 = 0; e0 < a.X; e0 += 64) {
-      const uint32_t c = __popc(e0 + lane < a.X ? mask[e0 + lane] : 0);
-      const uint32_t mine = c << 16 | ((c * d + 15) & ~15u);
-      uint32_t s = mine;
+      const uint32_t mk = e0 + lane < a.X ? mask[e0 + lane] : 0;
+      const int c = __popc(mk);
+      int s = c;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t t = __shfl_up(s, o, 64);
+        const int t = __shfl_up(s, o, 64);
         if (lane >= o) s += t;
       }
-      const uint32_t at = before + s - mine;
       const uint64_t here = __ballot(c > 0);
       if (c > 0) {
-        int* const to = list + 4 * (n_here + __popcll(here & ((uint64_t(1) << lane) - 1)));
-        to[0] = e0 + lane;
-        to[1] = at & 0xFFFF;
-        to[2] = c * d;
-        to[3] = at >> 16;
+        const int j = n_experts + __popcll(here & ((uint64_t(1) << lane) - 1));
+        list[4 * j] = e0 + lane;
+        list[4 * j + 1] = static_cast<int>(mk);
+        list[4 * j + 2] = places + s - c;
+        start[e0 + lane] = j;
       }
-      if (e0 + lane < a.X) start[e0 + lane] = at;
-      before += __shfl(s, 63, 64);
-      n_here += __popcll(here);
+      places += __shfl(s, 63, 64);
+      n_experts += __popcll(here);
     }
-    if (lane == 0) list[4 * n_here] = -1;
+    if (lane == 0) list[4 * n_experts] = -1;
   }
   __syncthreads();
-  // members' gates (an expert that stands twice in a row: their sum) and matrix rows
-  int my_place = 0;
-  if (my_e >= 0) {
+  for (int q = tid; q < n_entries; q += blockDim.x) {
+    const int e = ents[q], s = q / k;
+    if (e < 0) continue;
+    T g = 0;  // of an expert that stands twice in a row: the sum
     bool leads = true;
-    T g = 0;
-    for (int b = 0; b < k; ++b) {
-      const int q = my_s * k + b;
-      if (ents[q] == my_e) {
-        leads = leads && q >= tid;
-        g += graw[q];
+    for (int b = s * k; b < s * k + k; ++b)
+      if (ents[b] == e) {
+        leads = leads && b >= q;
+        g += graw[b];
       }
-    }
-    const uint32_t at = start[my_e], nth = __popc(mask[my_e] & ((1u << my_s) - 1));
-    my_place = (at >> 16) + nth;
-    if (leads) {
-      const int r = (at & 0xFFFF) + nth * d;
-      for (int c = 0; c < d; ++c) {
-        rtab[r + c] = uint32_t(my_s * m.ld_dst + c) << 16 | uint32_t(my_s * m.ld_src + c);
-        rgate[r + c] = g;
-      }
-    }
+    if (leads) gtab[start[e] * kTile + s] = g;
   }
-  __syncthreads();
 
-  // each wavefront: 16 output channels, all experts of the tile, the next
-  // expert's weights on their way while one's are in use
-  const int i16 = lane & 15, g4 = lane >> 4;
-  T* const my_sums = GG ? rowsum + w * sums : nullptr;
-  for (int n0 = w * 16; n0 < m.N; n0 += a.waves * 16) {
-    const int col = min(n0 + i16, m.N - 1);  // a lane past the last channel fills a column that is not written
-    const int to = (n0 + i16) * d;
-    for (int k0 = 0; k0 < m.K; k0 += 4 * KS) {
-      const int kk = k0 + g4 * KS;  // lane's channels of the sum: kk .. kk + KS - 1
-      const bool full = k0 + 4 * KS <= m.K;
-      auto load_weights = [&](int e, T* b) {  // zero past the last channel of the sum
-        const T* wp = weights + e * a.weight_numel + m.woff;
-        if (ADJ) {
-          const T* row = wp + col * m.V;
-          if (KS >= kPer && full && (m.vec & 4)) {
+  const int col = min(n_base + 16 * w + i16, m.N - 1);  // past the last channel: a column that is not written
+  T mine[GG ? D : 1][4];                                // GG: this lane's x
+  if (GG) {
+    mover_dst.finish(xs, other_from, dst_row, rows, n_here, a.waves);
+    __syncthreads();
+    const bool col_in = n_base + 16 * w + i16 < m.N;
 #pragma unroll
-            for (int s = 0; s < KS; s += kPer) {
-              const Pack<T> p = *reinterpret_cast<const Pack<T>*>(row + kk + s);
+    for (int c = 0; c < (GG ? D : 1); ++c)
 #pragma unroll
-              for (int q = 0; q < kPer; ++q) b[s + q] = p.v[q];
-            }
-          } else {
+      for (int q = 0; q < 4; ++q)
+        mine[c][q] = col_in ? xs[(16 * w + i16) * P + 16 * c + Mfma<T>::row(g4, q)] : T(0);
+    __syncthreads();
+  }
+  Acc acc[D];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) b[s] = row[min(kk + s, m.K - 1)];
-          }
-        } else if (full) {
+  for (int c = 0; c < D; ++c) acc[c] = Acc{0, 0, 0, 0};
+  for (int k0 = 0; k0 < m.K; k0 += CH) {
+    const int k_here = min(CH, m.K - k0);
+    // lane's channels of the sum: 16 a + 4 g4 + b for its 4 a + b-th value; its place in the matrix is a part
+    // of its own (bytes) after a part common to the wavefront
+    const uint32_t mine_at = sizeof(T) * (ADJ ? col * m.V + 4 * g4 : 4 * g4 * m.V + col);
+    const bool full = k_here == CH;
+    auto load_weights = [&](int e, T (&b)[KS]) {
+      const T* const we = weights + m.woff + e * a.weight_numel + (ADJ ? int64_t(k0) : int64_t(k0) * m.V);
+      if (ADJ && full && (m.packed & 4)) {
 #pragma unroll
-          for (int s = 0; s < KS; ++s) b[s] = wp[(kk + s) * m.V + col];
-        } else {
+        for (int s = 0; s < KS; s += kPer) {
+          const Pack<T> p = *reinterpret_cast<const Pack<T>*>(reinterpret_cast<const char*>(we + s / 4 * 16 + s % 4) +
+                                                              mine_at);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) b[s] = wp[min(kk + s, m.K - 1) * m.V + col];
+          for (int q = 0; q < kPer; ++q) b[s + q] = p.v[q];
         }
-      };
-      T b[KS], next[KS];
-      int e = __builtin_amdgcn_readfirstlane(list[0]);
+      } else if (full) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int u = s / 4 * 16 + s % 4;
+          b[s] = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(we + (ADJ ? u : u * m.V)) + mine_at);
+        }
+      } else {
+        int last = k_here - 1;
+        asm volatile("" : "+v"(last));  // keeps the places below out of the registers around the loop
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int u = min(s / 4 * 16 + 4 * g4 + s % 4, last);
+          b[s] = we[ADJ ? col * m.V + u : u * m.V + col];
+        }
+      }
+    };
+    T b[KS], next[KS];
+    int e = __builtin_amdgcn_readfirstlane(list[0]);
+    if (e >= 0) load_weights(e, next);
+    if (k0 > 0) mover.issue(0, src_from + k0 * D, src_row, rows, k_here, a.waves);
+    mover.finish(xs, src_from + k0 * D, src_row, rows, k_here, a.waves);
+    for (int q = tid; q < (CH - k_here) * P; q += blockDim.x) xs[k_here * P + q] = T(0);
+    __syncthreads();
+    const T* const ap = xs + 4 * g4 * P + i16;
+    for (int j = 0; e >= 0; ++j) {
+      const int members = __builtin_amdgcn_readfirstlane(list[4 * j + 1]);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) b[s] = full || s / 4 * 16 + 4 * g4 + s % 4 < k_here ? next[s] : T(0);
+      e = __builtin_amdgcn_readfirstlane(list[4 * j + 4]);
       if (e >= 0) load_weights(e, next);
-      for (int j = 0; e >= 0; ++j) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) b[s] = full || kk + s < m.K ? next[s] : T(0);
-        e = __builtin_amdgcn_readfirstlane(list[4 * j + 4]);
-        if (e >= 0) load_weights(e, next);
-        const int r0 = __builtin_amdgcn_readfirstlane(list[4 * j + 1]);
-        const int n_rows = __builtin_amdgcn_readfirstlane(list[4 * j + 2]);
-        const int place = __builtin_amdgcn_readfirstlane(list[4 * j + 3]) * d;
-        for (int r = 0; r < n_rows; r += 16) {
-          const T* ap = xs + (rtab[r0 + r + i16] & 0xFFFF) + kk * d;
-          T av[KS];
+      for (int r = 0; r < 16 * D; r += 64)
+        if (r + lane < 16 * D) grow[r + lane] = gtab[j * kTile + (r + lane) / D];
 #pragma unroll
-          for (int s = 0; s < KS; ++s) av[s] = ap[s * d];
-          int at[4];
-          T gate[4], sofar[4], other_row[4];
+      for (int c = 0; c < D; ++c) {
+        constexpr auto bits = [](int chunk) {  // rows of the tile in the chunk
+          int v = 0;
+          for (int s = 16 * chunk / D; s <= (16 * chunk + 15) / D; ++s) v |= 1 << s;
+          return v;
+        };
+        if ((members & bits(c)) == 0) continue;
+        T av[KS];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int rr = r0 + r + Mfma<T>::row(g4, q);
-            at[q] = static_cast<int>(rtab[rr] >> 16) + to;
-            gate[q] = rgate[rr];
-          }
+        for (int s = 0; s < KS; ++s) av[s] = ap[(s / 4 * 16 + s % 4) * P + 16 * c];
+        if (!ADJ) {
+          const T g = grow[16 * c + i16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            sofar[q] = acc[at[q]];
-            if (GG) other_row[q] = dot[at[q]];
-          }
-          typename Mfma<T>::Acc prod = {0, 0, 0, 0};
+          for (int s = 0; s < KS; ++s) acc[c] = Mfma<T>::step(av[s] * g, b[s], acc[c]);
+        } else {
+          Acc prod = {0, 0, 0, 0};
 #pragma unroll
           for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[at[q]] = sofar[q] + gate[q] * prod[q];
-          if (GG) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int rr = r + Mfma<T>::row(g4, q);
-              const T v = sum16(n0 + i16 < m.N ? prod[q] * other_row[q] : T(0));
-              if (i16 == 0) my_sums[rr < n_rows ? place + rr : sums - 1] += v;
+          for (int q = 0; q < 4; ++q) {
+            const int r = 16 * c + Mfma<T>::row(g4, q);
+            acc[c][q] += grow[r] * prod[q];
+            if (GG) {
+              const T v = sum16(prod[q] * mine[GG ? c : 0][q]);
+              if (i16 == 0) rsum[r] = v;
             }
           }
         }
       }
-    }
-  }
-  __syncthreads();
-  if (dst != nullptr) {
-    T* const to = dst + m.dst_off;
-    if (m.vec & 2)
-      move_rows<Pack<T>>(rows, olen / kPer, m.inv_dst,
-                         [&](int s, int c) {
-                           Pack<T> p;
+      if (GG && lane < kTile && ((members >> lane) & 1)) {  // the expert's rows, each over its components
+        T v = 0;
 #pragma unroll
-                           for (int q = 0; q < kPer; ++q) p.v[q] = acc[s * m.ld_dst + c * kPer + q];
-                           return p;
-                         },
-                         [&](int s, int c, const Pack<T>& p) {
-                           *reinterpret_cast<Pack<T>*>(to + rowid[s] * a.ld_dst + c * kPer) = p;
-                         });
-    else
-      move_rows<T>(rows, olen, m.inv_dst, [&](int s, int c) { return acc[s * m.ld_dst + c]; },
-                   [&](int s, int c, T v) { to[rowid[s] * a.ld_dst + c] = v; });
+        for (int c = 0; c < D; ++c) v += rsum[lane * D + c];
+        wsum[w * kTile * k + list[4 * j + 2] + __popc(members & ((1 << lane) - 1))] = v;
+      }
+    }
+    __syncthreads();
+    if (GG)
+      for (int q = tid; q < n_entries; q += blockDim.x) {
+        if (ents[q] < 0) continue;
+        const int s = q / k, j = start[ents[q]];
+        const int place = list[4 * j + 2] + __popc(list[4 * j + 1] & ((1 << s) - 1));
+        T v = esum[q];
+        for (int ww = 0; ww < a.waves; ++ww) v += wsum[ww * kTile * k + place];
+        esum[q] = v;
+      }
   }
-  if (GG && tid < n_entries) {
-    T v = 0;
-    if (my_e >= 0)
-      for (int ww = 0; ww < a.waves; ++ww)
-        for (int c = 0; c < d; ++c) v += rowsum[ww * sums + my_place * d + c];
-    gate_part[mi * (a.n_rows * k) + my_at] = v;
+  if (dst != nullptr) {
+#pragma unroll
+    for (int c = 0; c < D; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) xs[(16 * w + i16) * P + 16 * c + Mfma<T>::row(g4, q)] = acc[c][q];
+    __syncthreads();
+    mover_dst.store(xs, dst + m.dst_off + n_base * D, dst_row, rows, n_here, a.waves);
   }
+  if (GG)
+    for (int q = tid; q < n_entries; q += blockDim.x)
+      gate_part[share * (a.n_rows * k) + (order != nullptr ? order[base + q / k] : base + q / k) * k + q % k] = esum[q];
+}
+
+template <class T, int KS, bool ADJ, bool GG>
+__global__ __launch_bounds__(256, sizeof(T) == 8 || GG ? 2 : (ADJ ? 3 : 4)) void k_rows(
+    RowArgs a, const T* __restrict__ src, const T* __restrict__ weights, const int32_t* __restrict__ experts,
+    const T* __restrict__ gates, const int32_t* __restrict__ order, T* __restrict__ dst, const T* __restrict__ other,
+    T* __restrict__ gate_part) {
+  extern __shared__ char lds[];
+  const int tid = threadIdx.x, k = a.k;
+  const int share = static_cast<int>(blockIdx.x) / a.n_tiles;
+  int mi = 0;
+  while (mi + 1 < a.n_maps && share >= a.map[mi + 1].first) ++mi;
+  const RowMap& m = a.map[mi];
+  const int64_t base = int64_t(static_cast<int>(blockIdx.x) - share * a.n_tiles) * a.tile;
+  const int rows = static_cast<int>(min<int64_t>(a.tile, a.n_rows - base));
+  // where the tile's rows start, its entries, and tables cleared
+  auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
+  int64_t* const src_row = reinterpret_cast<int64_t*>(lds + a.lds.rows);
+  if (tid < rows) {
+    const int64_t r = row_of(tid);
+    src_row[tid] = r * a.ld_src;
+    src_row[kTile + tid] = r * a.ld_dst;
+  }
+  for (int q = tid; q < rows * k; q += blockDim.x) {
+    const int64_t at = row_of(q / k) * k + q % k;
+    const int e = experts[at];
+    const bool live = e >= 0 && e < a.X;
+    reinterpret_cast<int*>(lds + a.lds.ents)[q] = live ? e : -1;
+    reinterpret_cast<T*>(lds + a.lds.graw)[q] = live ? gates[at] : T(0);
+    if (GG) reinterpret_cast<T*>(lds + a.lds.esum)[q] = T(0);
+  }
+  for (int q = tid; q < a.X; q += blockDim.x) reinterpret_cast<uint32_t*>(lds + a.lds.mask)[q] = 0;
+  for (int q = tid; q < rows * k * kTile; q += blockDim.x) reinterpret_cast<T*>(lds + a.lds.gates)[q] = T(0);
+  __syncthreads();
+#define TPCONV_MAP_ROWS(D)                                                                                         \
+  case D:                                                                                                          \
+    if ((m.packed & 3) == 3)                                                                                       \
+      map_rows<T, D, KS, ADJ, GG, true, true>(a, m, share, base, rows, lds, src, weights, experts, gates, order,   \
+                                              dst, other, gate_part);                                              \
+    else                                                                                                           \
+      map_rows<T, D, KS, ADJ, GG, false, false>(a, m, share, base, rows, lds, src, weights, experts, gates, order, \
+                                                dst, other, gate_part);                                            \
+    break;
+  switch (m.d) {
+    TPCONV_MAP_ROWS(1)
+    TPCONV_MAP_ROWS(3)
+    TPCONV_MAP_ROWS(5)
+    TPCONV_MAP_ROWS(7)
+    TPCONV_MAP_ROWS(9)
+    default: break;
+  }
+#undef TPCONV_MAP_ROWS
 }
 
 template <class T>
@@ -752,12 +826,12 @@ __global__ __launch_bounds__(256) void k_wgrad(WgradArgs a, const T* __restrict_
 }
 
 // Adds what the kernels above left in parts, in order: an expert's pieces
-// (blocks [0, X nw): nw blocks of 256 weights each) and the maps' shares of the
+// (blocks [0, X nw): nw blocks of 256 weights each) and the shares of the
 // gates' gradient (the blocks after them).
 template <class T>
 __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int n_groups, int64_t max_pieces,
                                               const int32_t* __restrict__ pieces, const T* __restrict__ part,
-                                              T* __restrict__ out, int64_t n_gates, int n_maps,
+                                              T* __restrict__ out, int64_t n_gates, int n_parts,
                                               const T* __restrict__ gate_part, T* __restrict__ gate_out) {
   __shared__ int lo[64], upto[64], list[256];
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -765,7 +839,7 @@ __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int 
     const int64_t q = int64_t(b - X * nw) * 256 + tid;
     if (q >= n_gates) return;
     T s = 0;
-    for (int p = 0; p < n_maps; ++p) s += gate_part[p * n_gates + q];
+    for (int p = 0; p < n_parts; ++p) s += gate_part[p * n_gates + q];
     gate_out[q] = s;
     return;
   }
@@ -811,23 +885,25 @@ __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <class T, int KS, bool ADJ, bool GG>
-hipError_t rows_ks(const RowArgs& a, const RowLds& L, int64_t blocks, const T* src, const T* weights,
-                   const int32_t* experts, const T* gates, const int32_t* order, T* dst, const T* other, T* part,
-                   hipStream_t s) {
+hipError_t rows_ks(const RowArgs& a, unsigned blocks, const T* src, const T* weights, const int32_t* experts,
+                   const T* gates, const int32_t* order, T* dst, const T* other, T* part, hipStream_t s) {
   auto* const f = k_rows<T, KS, ADJ, GG>;
-  if (L.total > 64 * 1024) {  // above the default limit of dynamic LDS
-    const hipError_t he = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
-                                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
+  if (a.lds.total > 64 * 1024) {  // above the default limit of dynamic LDS
+    const hipError_t he =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(a.lds.total));
     if (he != hipSuccess) return he;
   }
-  hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * a.waves), L.total, s, a, L, src, weights, experts, gates, order, dst,
+  hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * a.waves), a.lds.total, s, a, src, weights, experts, gates, order, dst,
                      other, part);
   return hipGetLastError();
 }
 
+// n_parts: into how many partial sums the gates' gradient went, one for each
+// block of output channels of each map.
 template <class T, bool ADJ, bool GG>
 hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, const int32_t* experts, const T* gates,
-                const int32_t* order, T* dst, const T* other, T* part, hipStream_t s) {
+                const int32_t* order, T* dst, const T* other, T* part, T* gate_grad, int& n_parts, hipStream_t s) {
   RowArgs a{};
   a.n_rows = n;
   a.ld_src = ADJ ? p.dim_out : p.dim_in;
@@ -837,7 +913,7 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
   a.k = p.top_k;
   a.n_maps = static_cast<int32_t>(p.maps.size());
   const int per = 16 / static_cast<int>(sizeof(T));
-  int maxK = 0, maxN = 0;
+  int maxK = 0, maxN = 0, maxD = 0;
   for (int q = 0; q < a.n_maps; ++q) {
     const ExpertMap& e = p.maps[q];
     RowMap& m = a.map[q];
@@ -848,69 +924,61 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
     m.V = e.mul_out;
     m.d = e.d;
     m.woff = e.woff;
-    const bool vs = aligned16(src) && a.ld_src % per == 0 && m.src_off % per == 0 && (m.K * m.d) % per == 0;
-    const bool vd = (dst == nullptr || aligned16(dst)) && (!GG || aligned16(other)) && a.ld_dst % per == 0 &&
+    const bool ps = aligned16(src) && a.ld_src % per == 0 && m.src_off % per == 0 && (m.K * m.d) % per == 0;
+    const bool pd = (dst == nullptr || aligned16(dst)) && (!GG || aligned16(other)) && a.ld_dst % per == 0 &&
                     m.dst_off % per == 0 && (m.N * m.d) % per == 0;
-    const bool vw = aligned16(weights) && a.weight_numel % per == 0 && m.woff % per == 0 && m.V % per == 0;
-    m.vec = (vs ? 1 : 0) | (vd ? 2 : 0) | (vw ? 4 : 0);
+    const bool pw = aligned16(weights) && a.weight_numel % per == 0 && m.woff % per == 0 && m.V % per == 0;
+    m.packed = (ps ? 1 : 0) | (pd ? 2 : 0) | (pw ? 4 : 0);
     maxK = std::max(maxK, m.K);
     maxN = std::max(maxN, m.N);
+    maxD = std::max(maxD, m.d);
   }
-  const int KS = maxK <= 16 ? 4 : (maxK <= 32 ? 8 : 16);
-  a.waves = std::min(4, (maxN + 15) / 16);
-  // Tile: as many rows (32 at most: a bit each) as leave LDS for 8 wavefronts
-  // on a CU, 20 KiB for each of the block's; a thread for each entry, one row
-  // at least.  With few rows
-  // the tiles are made smaller, to have two blocks for each of the 256 CUs.
   std::sort(a.map, a.map + a.n_maps, [](const RowMap& x, const RowMap& y) {
     return int64_t(x.K) * x.N * x.d > int64_t(y.K) * y.N * y.d;  // long maps first
   });
-  uint32_t region[sizeof(RowLds) / 4] = {};
-  const int64_t spread = std::max<int64_t>(1, n * a.n_maps / 512);
-  int64_t blocks = 0;
+  const int KS = maxK <= 16 ? 4 : (maxK <= 32 ? 8 : 16);
+  a.waves = std::min(4, (maxN + 15) / 16);
+  // With few rows the tiles are made smaller, to have two wavefronts for each
+  // of the 1024 SIMDs.
+  n_parts = 0;
   for (int q = 0; q < a.n_maps; ++q) {
-    RowMap& m = a.map[q];
-    // rows in LDS start d (rounded up to 4) banks apart, modulo the 64 banks
-    auto pitch = [&](int channels) {
-      const int want = (m.d + 3) / 4 * 4, full = channels * m.d;
-      return full + ((want - full) % 64 + 64) % 64;
-    };
-    m.ld_src = pitch((m.K + 4 * KS - 1) / (4 * KS) * 4 * KS);
-    m.ld_dst = pitch((m.N + 15) / 16 * 16);
-    auto inverse = [](int pieces) { return pieces > 1 ? uint32_t((0xFFFFFFFFull + pieces) / pieces) : 0u; };
-    m.inv_src = inverse(m.K * m.d / (m.vec & 1 ? per : 1));
-    m.inv_dst = inverse(m.N * m.d / (m.vec & 2 ? per : 1));
-    RowLds one{};
-    for (m.tile = std::min(32, 64 * a.waves / a.k); m.tile > 1; --m.tile) {
-      one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
-      if (m.tile <= spread && one.total <= 20480u * a.waves) break;
-    }
-    one = row_lds(m, a.X, a.k, a.waves, GG, sizeof(T));
-    m.matrix_rows = matrix_rows(m.tile, a.X, a.k, m.d);
-    m.first = static_cast<int32_t>(blocks);
-    blocks += (n + m.tile - 1) / m.tile;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    // one launch for all maps: each region as large as the map that needs most
-    for (size_t f = 0; f < sizeof(RowLds) / 4; ++f) {
-      const uint32_t* const from = reinterpret_cast<const uint32_t*>(&one) + f;
-      region[f] = std::max(region[f], f > 0 ? from[0] - from[-1] : 0u);
-    }
+    a.map[q].first = n_parts;
+    n_parts += (a.map[q].N + 16 * a.waves - 1) / (16 * a.waves);
   }
-  RowLds L{};  // the regions' sizes, to offsets
-  for (size_t f = 1; f < sizeof(RowLds) / 4; ++f) {
-    uint32_t* const at = reinterpret_cast<uint32_t*>(&L) + f;
-    at[0] = at[-1] + region[f];
-  }
-  if (L.total > 160 * 1024) return hipErrorInvalidValue;
+  a.tile = static_cast<int32_t>(std::min<int64_t>(kTile, std::max<int64_t>(1, n * n_parts * a.waves / 2048)));
+  const int64_t tiles = (n + a.tile - 1) / a.tile;
+  if (tiles * n_parts > INT32_MAX) return hipErrorInvalidValue;
+  a.n_tiles = static_cast<int32_t>(tiles);
+  uint32_t o = 0;
+  auto take = [&](size_t count, size_t each) {
+    const uint32_t at = o;
+    o = static_cast<uint32_t>((o + count * each + 15) / 16 * 16);
+    return at;
+  };
+  const size_t entries = size_t(a.tile) * a.k, size = sizeof(T);
+  a.lds.tile = take(std::max(4 * KS, 16 * a.waves) * pitch_of(maxD), size);
+  a.lds.gates = take(entries * kTile, size);
+  a.lds.mask = take(a.X, 4);
+  a.lds.start = take(a.X, 4);
+  a.lds.list = take(4 * (entries + 1), 4);
+  a.lds.rows = take(2 * kTile, 8);
+  a.lds.graw = take(entries, size);
+  a.lds.grow = take(16 * 9 * a.waves, size);
+  a.lds.esum = take(GG ? entries : 0, size);
+  a.lds.wsum = take(GG ? size_t(kTile) * a.k * a.waves : 0, size);
+  a.lds.rsum = take(GG ? 16 * 9 * a.waves : 0, size);
+  a.lds.ents = take(entries, 4);
+  a.lds.total = o;
+  if (a.lds.total > 160 * 1024) return hipErrorInvalidValue;
+  const unsigned blocks = static_cast<unsigned>(tiles * n_parts);
+  T* const gg = n_parts == 1 ? gate_grad : part;
   for (const ColumnRun& r : ADJ ? p.bare_in : p.bare_out)
     if (dst != nullptr)
       hipLaunchKernelGGL(k_zero_columns<T>, dim3(blocks_for(n * r.len, 256)), dim3(256), 0, s, n, a.ld_dst, r.off,
                          r.len, dst);
-  switch (KS) {
-    case 4: return rows_ks<T, 4, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
-    case 8: return rows_ks<T, 8, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
-    default: return rows_ks<T, 16, ADJ, GG>(a, L, blocks, src, weights, experts, gates, order, dst, other, part, s);
-  }
+  if (KS == 4) return rows_ks<T, 4, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
+  if (KS == 8) return rows_ks<T, 8, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
+  return rows_ks<T, 16, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
 }
 
 const int32_t* order_in(const Experts& p, int64_t n, const void* layout) {
@@ -929,7 +997,9 @@ BackwardSpace backward_space(const Experts& p, int64_t n) {
   const size_t size = p.f64 ? 8 : 4;
   const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
   BackwardSpace w{};
-  w.parts = align_up(p.maps.size() * n * p.top_k * size);
+  size_t shares = 0;  // as rows() counts them, with the fewest wavefronts a map's channels can get
+  for (const ExpertMap& m : p.maps) shares += (m.mul_in + 15) / 16;
+  w.parts = align_up(shares * n * p.top_k * size);
   w.total = std::max<size_t>(256, w.parts + align_up(L.n_groups * L.max_pieces * p.weight_numel * size));
   return w;
 }
@@ -946,21 +1016,24 @@ template <class T>
 hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates,
                     const void* layout, const T* grad, T* gx, T* gw, T* gg, void* ws, hipStream_t s) {
   const int32_t* order = order_in(p, n, layout);
-  const int64_t n_gates = gg != nullptr ? n * p.top_k : 0;
+  int64_t n_gates = gg != nullptr ? n * p.top_k : 0;
   const int n_maps = static_cast<int>(p.maps.size()), X = p.n_experts;
+  int n_parts = 1;
   const BackwardSpace space = backward_space(p, n);
   T* const gate_part = static_cast<T*>(ws);
   hipError_t he = hipSuccess;
   if (n_gates > 0)
-    he = rows<T, true, true>(p, n, grad, weights, experts, gates, order, gx, x, gate_part, s);
+    he = rows<T, true, true>(p, n, grad, weights, experts, gates, order, gx, x, gate_part, gg, n_parts, s);
   else if (n > 0 && gx != nullptr)
-    he = rows<T, true, false>(p, n, grad, weights, experts, gates, order, gx, nullptr, nullptr, s);
+    he = rows<T, true, false>(p, n, grad, weights, experts, gates, order, gx, nullptr, nullptr, nullptr,
+                             n_parts, s);
   if (he != hipSuccess) return he;
+  if (n_parts == 1) n_gates = 0;  // they are whole
   const int64_t gate_blocks = (n_gates + 255) / 256;
   if (gw == nullptr) {
     if (gate_blocks > 0)
       hipLaunchKernelGGL(k_join<T>, dim3(static_cast<unsigned>(gate_blocks)), dim3(256), 0, s, 0, 0, p.weight_numel, 0,
-                         int64_t(0), nullptr, nullptr, nullptr, n_gates, n_maps, gate_part, gg);
+                         int64_t(0), nullptr, nullptr, nullptr, n_gates, n_parts, gate_part, gg);
     return hipGetLastError();
   }
   const LayoutShape L = layout_shape(n, X, p.top_k);
@@ -1020,7 +1093,7 @@ hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, c
   if (nw > 0 || gate_blocks > 0)
     hipLaunchKernelGGL(k_join<T>, dim3(static_cast<unsigned>(int64_t(X) * nw + gate_blocks)), dim3(256), 0, s, X, nw,
                        p.weight_numel, n > 0 ? static_cast<int>(L.n_groups) : 0, L.max_pieces, pcs, parts, gw, n_gates,
-                       n_maps, gate_part, gg);
+                       n_parts, gate_part, gg);
   return hipGetLastError();
 }
 
@@ -1048,13 +1121,14 @@ hipError_t launch_experts_forward(const Experts& p, int64_t n, const void* x, co
                                   const int32_t* experts, const void* gates, const void* layout, void* out,
                                   hipStream_t s) {
   const int32_t* order = order_in(p, n, layout);
+  int n_parts;
   if (p.f64)
     return rows<double, false, false>(p, n, static_cast<const double*>(x), static_cast<const double*>(weights),
                                       experts, static_cast<const double*>(gates), order, static_cast<double*>(out),
-                                      nullptr, nullptr, s);
+                                      nullptr, nullptr, nullptr, n_parts, s);
   return rows<float, false, false>(p, n, static_cast<const float*>(x), static_cast<const float*>(weights), experts,
                                    static_cast<const float*>(gates), order, static_cast<float*>(out), nullptr,
-                                   nullptr, s);
+                                   nullptr, nullptr, n_parts, s);
 }
 
 hipError_t launch_experts_backward(const Experts& p, int64_t n, const void* x, const void* weights,
