@@ -136,53 +136,76 @@ __device__ int scan_counters(int* c, int n, int* wave_sums) {
 // * H / X), H = min(X, 4096 / X); rows without experts last.  Rows of one bin
 // come in no fixed order (an integer atomic hands out the places): a row's
 // results do not depend on its neighbours.  Entries are ranked by counting in
-// order, so theirs is fixed.  Latency bound: 28000 rows are 14 blocks.
+// order, so theirs is fixed.  Latency bound, so the group's experts are read
+// once, into LDS, where they fit.
+constexpr int kStaged = 16384;
+
 __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group,
                                                  const int32_t* __restrict__ experts, int32_t* __restrict__ order,
                                                  int32_t* __restrict__ entries, int32_t* __restrict__ first,
                                                  int32_t* __restrict__ pieces) {
   __shared__ int bins[kMaxBins + 1];
   __shared__ int wave_sums[16];
+  __shared__ uint16_t staged[kStaged];
   const int64_t r0 = blockIdx.x * group;
   const int rows = static_cast<int>(min(group, n - r0));
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, nw = blockDim.x >> 6;
   const int32_t* ex = experts + r0 * k;
+  const int total = rows * k;
+  const bool in_lds = total <= kStaged;
+  auto clean = [&](int e) { return e >= 0 && e < X ? e : X; };  // X: none
+  if (in_lds)
+    for (int q0 = tid; q0 < total; q0 += 8 * blockDim.x) {
+      int e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = ex[min(q0 + j * int(blockDim.x), total - 1)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (q0 + j * int(blockDim.x) < total) staged[q0 + j * blockDim.x] = static_cast<uint16_t>(clean(e[j]));
+    }
+  auto expert = [&](int q) { return in_lds ? int(staged[q]) : clean(ex[q]); };
 
   auto bin_of = [&](int r) {
     int lo = X, hi = X;
     for (int a = 0; a < k; ++a) {
-      const int e = ex[int64_t(r) * k + a];
-      if (e < 0 || e >= X) continue;
-      if (e < lo) {
-        hi = lo;
-        lo = e;
-      } else if (e > lo && e < hi) {
-        hi = e;
-      }
+      const int e = expert(r * k + a);
+      hi = e < lo ? lo : (e > lo && e < hi ? e : hi);
+      lo = min(lo, e);
     }
     if (lo == X) return X * H;
-    if (hi == X) hi = lo;
-    return lo * H + hi * H / X;
+    return lo * H + (hi == X ? lo : hi) * H / X;
   };
   for (int q = tid; q <= X * H; q += blockDim.x) bins[q] = 0;
   __syncthreads();
-  for (int r = tid; r < rows; r += blockDim.x) atomicAdd(&bins[bin_of(r)], 1);
+  constexpr int kKept = 2;  // rows of a thread whose bins are kept (all of them in a group of 2048)
+  int kept[kKept];
+#pragma unroll
+  for (int j = 0; j < kKept; ++j) {
+    const int r = tid + j * blockDim.x;
+    kept[j] = r < rows ? bin_of(r) : 0;
+    if (r < rows) atomicAdd(&bins[kept[j]], 1);
+  }
+  for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x) atomicAdd(&bins[bin_of(r)], 1);
   __syncthreads();
   scan_counters(bins, X * H + 1, wave_sums);
-  for (int r = tid; r < rows; r += blockDim.x)
+#pragma unroll
+  for (int j = 0; j < kKept; ++j) {
+    const int r = tid + j * blockDim.x;
+    if (r < rows) order[r0 + atomicAdd(&bins[kept[j]], 1)] = static_cast<int32_t>(r0 + r);
+  }
+  for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x)
     order[r0 + atomicAdd(&bins[bin_of(r)], 1)] = static_cast<int32_t>(r0 + r);
   __syncthreads();
 
   // entries by expert: each wavefront counts, then places, its own run of them;
   // counters [expert][wavefront], scanned in that order
-  const int total = rows * k;
   const int run = ((total + nw - 1) / nw + 63) / 64 * 64;
   const int q0 = w * run, q1 = min(total, q0 + run);
   for (int q = tid; q < X * nw; q += blockDim.x) bins[q] = 0;
   __syncthreads();
   for (int q = q0 + lane; q < q1; q += 64) {
-    const int e = ex[q];
-    if (e >= 0 && e < X) atomicAdd(&bins[e * nw + w], 1);
+    const int e = expert(q);
+    if (e < X) atomicAdd(&bins[e * nw + w], 1);
   }
   __syncthreads();
   const int placed = scan_counters(bins, X * nw, wave_sums);
@@ -203,8 +226,8 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
   }
   __syncthreads();
   for (int q = q0; q < q1; q += 64) {
-    const int e = q + lane < q1 ? ex[q + lane] : -1;
-    const bool live = e >= 0 && e < X;
+    const int e = q + lane < q1 ? expert(q + lane) : X;
+    const bool live = e < X;
     uint64_t peers = __ballot(live);  // lanes of this pass with the same expert
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
@@ -238,13 +261,14 @@ __global__ void k_load(int X, int64_t n_groups, const int32_t* __restrict__ firs
 // The segment goes to LDS with the channels apart ([channel][matrix row], so
 // that every read of the loop is one address register and a constant), the
 // chunks' sums stay in registers, and for each expert of the tile the chunks
-// that hold one of its rows are multiplied, the rows scaled by their gates
-// (0 where a row is not the expert's).  So x is read once, out is written once
+// that hold one of its rows are multiplied and added times the rows' gates (0
+// where a row is not the expert's; 4 multiplications for a chunk, where gates
+// on the rows would take 16, which compete with the fp32 matrix instructions
+// for the vector units).  So x is read once, out is written once
 // whatever top_k, and a row's sum runs over its experts in ascending order.
 // The next expert's weights are on their way while one's are in use.  A
-// wavefront owns 16 output channels.  ADJ runs the transposed maps on grad_out
-// and applies the gate after the product, which GG dots with x before that for
-// the gates' gradient.
+// wavefront owns 16 output channels.  ADJ runs the transposed maps on
+// grad_out; GG also dots the products with x for the gates' gradient.
 constexpr int kTile = 16;
 
 struct RowMap {
@@ -337,14 +361,20 @@ struct TileMover {
 
   T v[kBatch][PER];
 
-  // a batch of pieces, from the q0-th on
-  __device__ __forceinline__ void issue(int q0, const T* from, const int64_t* start, int rows, int n, int waves) {
+  // a batch of pieces, from the q0-th on; start(s): where row s of the tile starts
+  template <class Start>
+  __device__ __forceinline__ void issue(int q0, const T* from, Start start, int rows, int n, int waves) {
     const int tid = fresh(threadIdx.x);
+    int64_t row[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       int s, c;
       piece(tid, q0 + j, rows, n * D / PER, waves, s, c);
-      const T* at = from + start[s] + c;
+      row[j] = start(s) + c;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const T* at = from + row[j];
       if constexpr (PER > 1) {
         const Pack<T> p = *reinterpret_cast<const Pack<T>*>(at);
 #pragma unroll
@@ -355,7 +385,8 @@ struct TileMover {
     }
   }
   // puts the first batch, issued before, into LDS, and fetches what it left
-  __device__ __forceinline__ void finish(T* lds, const T* from, const int64_t* start, int rows, int n, int waves) {
+  template <class Start>
+  __device__ __forceinline__ void finish(T* lds, const T* from, Start start, int rows, int n, int waves) {
     for (int q0 = 0;;) {
       const int tid = fresh(threadIdx.x);
 #pragma unroll
@@ -371,13 +402,13 @@ struct TileMover {
     }
   }
 
-  static __device__ __forceinline__ void store(const T* lds, T* to, const int64_t* start, int rows, int n,
-                                               int waves) {
+  template <class Start>
+  static __device__ __forceinline__ void store(const T* lds, T* to, Start start, int rows, int n, int waves) {
     const int tid = fresh(threadIdx.x);
     for (int q = 0; q < trips(rows, waves); ++q) {
       int s, c;
       if (!piece(tid, q, rows, n * D / PER, waves, s, c)) continue;
-      T* const at = to + start[s] + c;
+      T* const at = to + start(s) + c;
       if constexpr (PER > 1) {
         Pack<T> p;
 #pragma unroll
@@ -407,8 +438,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   uint32_t* const mask = reinterpret_cast<uint32_t*>(lds + a.lds.mask);  // members of each expert, a bit per row
   int* const start = reinterpret_cast<int*>(lds + a.lds.start);          // each expert's place in the list
   int* const list = reinterpret_cast<int*>(lds + a.lds.list);  // the tile's experts: expert, members' bits, members before
-  const int64_t* const src_row = reinterpret_cast<const int64_t*>(lds + a.lds.rows);
-  const int64_t* const dst_row = src_row + kTile;
+  int* const rowid = reinterpret_cast<int*>(lds + a.lds.rows);
   T* const graw = reinterpret_cast<T*>(lds + a.lds.graw);
   int* const ents = reinterpret_cast<int*>(lds + a.lds.ents);
   T* const grow = reinterpret_cast<T*>(lds + a.lds.grow) + w * 16 * 9;  // a wavefront's gates of one expert's matrix rows
@@ -416,18 +446,47 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   T* const wsum = reinterpret_cast<T*>(lds + a.lds.wsum);
   T* const rsum = reinterpret_cast<T*>(lds + a.lds.rsum) + w * 16 * 9;
 
-  // the rows are on their way while the tile's experts are listed
+  // The tile's entries, then its rows, are on their way while its experts are
+  // listed: one trip to memory for the row numbers, one for all that they name.
   const int n_base = (share - m.first) * 16 * a.waves, n_here = min(16 * a.waves, m.N - n_base);
+  const int n_entries = rows * k;
+  auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
+  auto src_row = [&](int s) { return rowid[s] * a.ld_src; };
+  auto dst_row = [&](int s) { return rowid[s] * a.ld_dst; };
+  const int q0 = min(tid, n_entries - 1), s0 = q0 / k;
+  const int64_t row0 = row_of(s0), at0 = row0 * k + (q0 - s0 * k);
+  const int e0 = experts[at0];
+  const T g0 = gates[at0];
   TileMover<T, D, CH, VS ? kPer : 1> mover;
   TileMover<T, D, 64, VD ? kPer : 1> mover_dst;
   const T* const src_from = src + m.src_off;
   const T* const other_from = GG ? other + m.dst_off + n_base * D : nullptr;
-  if (GG) mover_dst.issue(0, other_from, dst_row, rows, n_here, a.waves);
-  mover.issue(0, src_from, src_row, rows, min(CH, m.K), a.waves);
+  auto first = [&](auto row) {
+    if (GG) mover_dst.issue(0, other_from, [&](int s) { return row(s) * a.ld_dst; }, rows, n_here, a.waves);
+    mover.issue(0, src_from, [&](int s) { return row(s) * a.ld_src; }, rows, min(CH, m.K), a.waves);
+  };
+  if (order != nullptr)
+    first([&](int s) -> int64_t { return order[base + s]; });
+  else
+    first([&](int s) -> int64_t { return base + s; });
 
-  const int n_entries = rows * k;
-  for (int q = tid; q < n_entries; q += blockDim.x)
-    if (ents[q] >= 0) atomicOr(&mask[ents[q]], 1u << (q / k));
+  for (int q = tid; q < a.X; q += blockDim.x) mask[q] = 0;
+  for (int q = tid; q < n_entries * kTile; q += blockDim.x) gtab[q] = T(0);
+  __syncthreads();
+  auto note = [&](int q, int s, int64_t row, int e, T g) {
+    const bool live = e >= 0 && e < a.X;
+    ents[q] = live ? e : -1;
+    graw[q] = live ? g : T(0);
+    if (GG) esum[q] = T(0);
+    if (live) atomicOr(&mask[e], 1u << s);
+    if (q == s * k) rowid[s] = static_cast<int>(row);
+  };
+  if (tid < n_entries) note(q0, s0, row0, e0, g0);
+  for (int q = tid + blockDim.x; q < n_entries; q += blockDim.x) {
+    const int s = q / k;
+    const int64_t row = row_of(s), at = row * k + (q - s * k);
+    note(q, s, row, experts[at], gates[at]);
+  }
   __syncthreads();
   if (w == 0) {  // experts present, ascending, and the members before each
     int n_experts = 0, places = 0;
@@ -543,22 +602,16 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
         T av[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) av[s] = ap[(s / 4 * 16 + s % 4) * P + 16 * c];
-        if (!ADJ) {
-          const T g = grow[16 * c + i16];
+        Acc prod = {0, 0, 0, 0};
 #pragma unroll
-          for (int s = 0; s < KS; ++s) acc[c] = Mfma<T>::step(av[s] * g, b[s], acc[c]);
-        } else {
-          Acc prod = {0, 0, 0, 0};
+        for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = 16 * c + Mfma<T>::row(g4, q);
-            acc[c][q] += grow[r] * prod[q];
-            if (GG) {
-              const T v = sum16(prod[q] * mine[GG ? c : 0][q]);
-              if (i16 == 0) rsum[r] = v;
-            }
+        for (int q = 0; q < 4; ++q) {
+          const int r = 16 * c + Mfma<T>::row(g4, q);
+          acc[c][q] += grow[r] * prod[q];
+          if (GG) {
+            const T v = sum16(prod[q] * mine[GG ? c : 0][q]);
+            if (i16 == 0) rsum[r] = v;
           }
         }
       }
@@ -590,7 +643,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   }
   if (GG)
     for (int q = tid; q < n_entries; q += blockDim.x)
-      gate_part[share * (a.n_rows * k) + (order != nullptr ? order[base + q / k] : base + q / k) * k + q % k] = esum[q];
+      gate_part[share * (a.n_rows * k) + int64_t(rowid[q / k]) * k + q % k] = esum[q];
 }
 
 template <class T, int KS, bool ADJ, bool GG>
@@ -599,32 +652,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 8 || GG ? 2 : (ADJ ? 3 : 4)) void
     const T* __restrict__ gates, const int32_t* __restrict__ order, T* __restrict__ dst, const T* __restrict__ other,
     T* __restrict__ gate_part) {
   extern __shared__ char lds[];
-  const int tid = threadIdx.x, k = a.k;
   const int share = static_cast<int>(blockIdx.x) / a.n_tiles;
   int mi = 0;
   while (mi + 1 < a.n_maps && share >= a.map[mi + 1].first) ++mi;
   const RowMap& m = a.map[mi];
   const int64_t base = int64_t(static_cast<int>(blockIdx.x) - share * a.n_tiles) * a.tile;
   const int rows = static_cast<int>(min<int64_t>(a.tile, a.n_rows - base));
-  // where the tile's rows start, its entries, and tables cleared
-  auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
-  int64_t* const src_row = reinterpret_cast<int64_t*>(lds + a.lds.rows);
-  if (tid < rows) {
-    const int64_t r = row_of(tid);
-    src_row[tid] = r * a.ld_src;
-    src_row[kTile + tid] = r * a.ld_dst;
-  }
-  for (int q = tid; q < rows * k; q += blockDim.x) {
-    const int64_t at = row_of(q / k) * k + q % k;
-    const int e = experts[at];
-    const bool live = e >= 0 && e < a.X;
-    reinterpret_cast<int*>(lds + a.lds.ents)[q] = live ? e : -1;
-    reinterpret_cast<T*>(lds + a.lds.graw)[q] = live ? gates[at] : T(0);
-    if (GG) reinterpret_cast<T*>(lds + a.lds.esum)[q] = T(0);
-  }
-  for (int q = tid; q < a.X; q += blockDim.x) reinterpret_cast<uint32_t*>(lds + a.lds.mask)[q] = 0;
-  for (int q = tid; q < rows * k * kTile; q += blockDim.x) reinterpret_cast<T*>(lds + a.lds.gates)[q] = T(0);
-  __syncthreads();
 #define TPCONV_MAP_ROWS(D)                                                                                         \
   case D:                                                                                                          \
     if ((m.packed & 3) == 3)                                                                                       \
@@ -961,7 +994,7 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
   a.lds.mask = take(a.X, 4);
   a.lds.start = take(a.X, 4);
   a.lds.list = take(4 * (entries + 1), 4);
-  a.lds.rows = take(2 * kTile, 8);
+  a.lds.rows = take(kTile, 4);
   a.lds.graw = take(entries, size);
   a.lds.grow = take(16 * 9 * a.waves, size);
   a.lds.esum = take(GG ? entries : 0, size);
