@@ -29,9 +29,10 @@ __device__ __forceinline__ Words philox(uint64_t block, uint64_t offset, uint64_
   return Words{{c0, c1, c2, c3}};
 }
 
-// One thread per element.
+// One thread per element, its draw computed for it alone: for rows whose
+// column table does not fit LDS.
 template <class T>
-__global__ void k_dropout(DropArgs a, const T* x, const T* residual, T* out) {
+__global__ void k_dropout_wide(DropArgs a, const T* x, const T* residual, T* out) {
   const T scale = static_cast<T>(a.scale);
   const int64_t total = a.n_rows * a.dim, step = int64_t(gridDim.x) * blockDim.x;
   for (int64_t q = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; q < total; q += step) {
@@ -46,19 +47,122 @@ __global__ void k_dropout(DropArgs a, const T* x, const T* residual, T* out) {
   }
 }
 
+// Memory bound: a block takes tiles of rows, draws the tile's channels (four
+// to a generator call) into LDS, a byte each, and streams the tile's pieces of
+// 16 bytes past them; a table in LDS says which channel a column belongs to.
+// The next kAhead pieces are loaded while the draws are made.
+constexpr int kThreads = 256, kAhead = 4;
+constexpr int kTableColumns = 16384, kTileBytes = 16384;
+
+template <class T, bool VEC, bool RES>
+__global__ __launch_bounds__(kThreads) void k_dropout(DropArgs a, int tile, uint32_t inv, const T* x,
+                                                      const T* residual, T* out) {
+  constexpr int kPer = VEC ? 16 / sizeof(T) : 1;
+  struct alignas(kPer * sizeof(T)) Piece {
+    T v[kPer];
+  };
+  extern __shared__ uint16_t channel_of[];  // [dim], then a byte for each channel of the tile
+  const int dim = static_cast<int>(a.dim), channels = static_cast<int>(a.channels);
+  uint8_t* const keep = reinterpret_cast<uint8_t*>(channel_of + (dim + 7) / 8 * 8);
+  const int tid = threadIdx.x;
+  for (int s = 0; s < a.n_segs; ++s)
+    for (int c = a.seg[s].off + tid; c < a.seg[s].end; c += kThreads)
+      channel_of[c] = static_cast<uint16_t>(a.seg[s].channel + (c - a.seg[s].off) / a.seg[s].d);
+  const T scale = static_cast<T>(a.scale);
+  const int pieces = dim / kPer;
+  for (int64_t i0 = int64_t(blockIdx.x) * tile; i0 < a.n_rows; i0 += int64_t(gridDim.x) * tile) {
+    const int rows = static_cast<int>(min<int64_t>(tile, a.n_rows - i0)), total = rows * pieces;
+    const Piece* const xp = reinterpret_cast<const Piece*>(x + i0 * dim);
+    const Piece* const rp = reinterpret_cast<const Piece*>(residual + (RES ? i0 * dim : 0));
+    Piece* const op = reinterpret_cast<Piece*>(out + i0 * dim);
+    Piece vx[kAhead], vr[kAhead];
+    auto load = [&](int q0) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int q = min(q0 + j * kThreads, total - 1);
+        vx[j] = xp[q];
+        if (RES) vr[j] = rp[q];
+      }
+    };
+    load(tid);
+    __syncthreads();  // the last tile's draws are no longer read
+    const int64_t c0 = i0 * channels;
+    const int n = rows * channels, lead = static_cast<int>(c0 & 3);  // channels of the first call that are not ours
+    for (int g = tid; g * 4 < n + lead; g += kThreads) {
+      const Words w = philox((uint64_t(c0) >> 2) + g, a.offset, a.seed);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = g * 4 + j - lead;
+        if (c >= 0 && c < n) keep[c] = w.w[j] >= a.threshold;
+      }
+    }
+    __syncthreads();
+    for (int q0 = tid; q0 < total; q0 += kAhead * kThreads) {
+      if (q0 != tid) load(q0);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int q = q0 + j * kThreads;
+        if (q >= total) continue;
+        const int row = inv != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(q), inv)) : q;
+        const uint16_t* const ch = channel_of + (q - row * pieces) * kPer;
+        const uint8_t* const kept = keep + row * channels;
+        Piece p;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const T base = RES ? vr[j].v[e] : T(0);
+          p.v[e] = kept[ch[e]] ? base + scale * vx[j].v[e] : base;
+        }
+        op[q] = p;
+      }
+    }
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <class T>
+hipError_t dropout(const DropArgs& a, const T* x, const T* residual, T* out, hipStream_t s) {
+  constexpr int kPer = 16 / sizeof(T);
+  if (a.dim > kTableColumns) {
+    const int64_t g = (a.n_rows * a.dim + 255) / 256;
+    hipLaunchKernelGGL(k_dropout_wide<T>, dim3(static_cast<unsigned>(g > 65536 ? 65536 : g)), dim3(256), 0, s, a, x,
+                       residual, out);
+    return hipGetLastError();
+  }
+  const bool vec = a.dim % kPer == 0 && aligned16(x) && aligned16(residual) && aligned16(out);
+  const int pieces = static_cast<int>(a.dim) / (vec ? kPer : 1);
+  // a tile: as many rows as make 16 KiB of x, one at least; fewer where that leaves CUs without a tile
+  int64_t tile = kTileBytes / (a.dim * int64_t(sizeof(T)));
+  tile = tile < 1 ? 1 : tile;
+  while (tile > 1 && (a.n_rows + tile - 1) / tile < 512) tile = (tile + 1) / 2;
+  int64_t blocks = (a.n_rows + tile - 1) / tile;
+  blocks = blocks < 2048 ? blocks : 2048;  // 8 blocks for each CU, the table built once for all of a block's tiles
+  const uint32_t inv = pieces > 1 ? uint32_t((0xFFFFFFFFull + pieces) / pieces) : 0u;
+  const size_t lds = (a.dim + 7) / 8 * 16 + tile * a.channels;
+  const dim3 grid(static_cast<unsigned>(blocks));
+#define TPCONV_DROP(V, R)                                                                                         \
+  hipLaunchKernelGGL((k_dropout<T, V, R>), grid, dim3(kThreads), lds, s, a, static_cast<int>(tile), inv, x, residual, \
+                     out)
+  if (vec && residual != nullptr)
+    TPCONV_DROP(true, true);
+  else if (vec)
+    TPCONV_DROP(true, false);
+  else if (residual != nullptr)
+    TPCONV_DROP(false, true);
+  else
+    TPCONV_DROP(false, false);
+#undef TPCONV_DROP
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_dropout(bool f64, const DropArgs& a, const void* x, const void* residual, void* out,
                           hipStream_t s) {
-  const int64_t g = (a.n_rows * a.dim + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(g > 65536 ? 65536 : g));
-  if (f64)
-    hipLaunchKernelGGL(k_dropout<double>, grid, dim3(256), 0, s, a, static_cast<const double*>(x),
-                       static_cast<const double*>(residual), static_cast<double*>(out));
-  else
-    hipLaunchKernelGGL(k_dropout<float>, grid, dim3(256), 0, s, a, static_cast<const float*>(x),
-                       static_cast<const float*>(residual), static_cast<float*>(out));
-  return hipGetLastError();
+  return f64 ? dropout(a, static_cast<const double*>(x), static_cast<const double*>(residual),
+                       static_cast<double*>(out), s)
+             : dropout(a, static_cast<const float*>(x), static_cast<const float*>(residual), static_cast<float*>(out),
+                       s);
 }
 
 }  // namespace tpconv
