@@ -24,7 +24,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from .tpconv import F32, F64, _check, _lib, _need, _on_launch_stream, _ptr, _stream_handle
+from .tpconv import F32, F64, _check, _lib, _on_launch_stream
+from .tpconv import _need as _explain
 
 NODE_EXPORTS = ("tpconv_embedding_forward", "tpconv_embedding_workspace_bytes", "tpconv_embedding_backward",
                 "tpconv_route_forward", "tpconv_route_backward", "tpconv_experts_plan", "tpconv_experts_query",
@@ -79,6 +80,24 @@ def _declare():
 
 
 _declare()
+
+
+# These calls are short enough for their checks to show: the common case of
+# each is a few attribute reads, and pointers go to ctypes as integers.
+def _need(t, shape, dtype, name):
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _explain(t, shape, dtype, name)
+    return t
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _code(t: torch.Tensor, name: str) -> int:
