@@ -1,11 +1,13 @@
 // node_route.hip -- routing of rows to experts: scores, groups, top_k, gates,
 // and the gradient of the gates with respect to the logits.
 //
-// 2^LG lanes hold a row, VPL logits each (expert v * 2^LG + lane), so a row
-// is read once, coalesced, and several short rows share a wavefront.  The
-// reductions over a row run on the vector units (DPP and lane swaps); one
-// round of the selection is a maximum over the row, a ballot of the lanes that
-// hold it, and the lowest of them: no sort, and ties are settled exactly.
+// 8 or 16 lanes hold a row, VPL logits each (expert v * lanes + lane), so a row
+// is read once and 8 or 4 rows share a wavefront.  (A whole wavefront to a row
+// of 128 took 125 us for 131072 rows: the steps across lanes, the group
+// search and the gates then serve one row.)  The reductions over a row run on
+// the vector units (DPP); one round of the selection is a maximum over the
+// row's keys, as ordered whole numbers, and a minimum over the indices that
+// hold it: no sort, and ties are settled exactly.
 #include <hip/hip_runtime.h>
 
 #include "node_internal.hpp"
@@ -35,17 +37,16 @@ __device__ __forceinline__ T sigmoid(T z) {
 // ------------------------------------------------- reductions over 2^LG lanes
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
 // v of the lane across: by 1, 2, 4, 8 (the last two mirror, which is the same
-// once the lanes below agree), 16, 32
+// once the lanes below agree)
 template <int STEP>
 __device__ __forceinline__ uint32_t across(uint32_t v) {
   if constexpr (STEP == 0) return dpp<0xB1>(v);
   if constexpr (STEP == 1) return dpp<0x4E>(v);
   if constexpr (STEP == 2) return dpp<0x141>(v);
-  if constexpr (STEP == 3) return dpp<0x140>(v);
-  return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 1 << STEP, 64));
+  return dpp<0x140>(v);
 }
 template <int STEP>
 __device__ __forceinline__ float across(float v) {
@@ -55,6 +56,11 @@ template <int STEP>
 __device__ __forceinline__ double across(double v) {
   return __hiloint2double(static_cast<int>(across<STEP>(static_cast<uint32_t>(__double2hiint(v)))),
                           static_cast<int>(across<STEP>(static_cast<uint32_t>(__double2loint(v)))));
+}
+
+template <int STEP>
+__device__ __forceinline__ uint64_t across(uint64_t v) {
+  return uint64_t(across<STEP>(static_cast<uint32_t>(v >> 32))) << 32 | across<STEP>(static_cast<uint32_t>(v));
 }
 
 struct Max {
@@ -71,21 +77,36 @@ struct Sum {
 };
 template <int LG, class Op, class T>
 __device__ __forceinline__ T reduce(T v, Op op) {
+  static_assert(LG <= 4, "rows of 16 lanes at most");
   if constexpr (LG > 0) v = op(v, across<0>(v));
   if constexpr (LG > 1) v = op(v, across<1>(v));
   if constexpr (LG > 2) v = op(v, across<2>(v));
   if constexpr (LG > 3) v = op(v, across<3>(v));
-  if constexpr (LG > 4) v = op(v, across<4>(v));
-  if constexpr (LG > 5) v = op(v, across<5>(v));
   return v;
 }
 
-// lanes of this row for which `on` holds, the row's first lane at bit 0
-template <int LG>
-__device__ __forceinline__ uint64_t row_ballot(bool on) {
-  const uint64_t m = __ballot(on);
-  if constexpr (LG == 6) return m;
-  return (m >> (threadIdx.x & 63 & ~((1 << LG) - 1))) & ((uint64_t(1) << (1 << LG)) - 1);
+// v of lane `from` of this row
+template <int LG, class T>
+__device__ __forceinline__ T of_lane(T v, int from) {
+  return __shfl(v, (threadIdx.x & 63 & ~((1 << LG) - 1)) + from, 64);
+}
+
+// Scores as whole numbers in the same order; 0 is below every score.
+__device__ __forceinline__ uint32_t ordered(float s) {
+  const uint32_t b = __float_as_uint(s + 0.0f);  // one zero
+  return (b >> 31) != 0 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t ordered(double s) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
+  return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
+}
+
+// Makes a wavefront's LDS writes visible to its own reads (a row never leaves
+// its wavefront).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // maximum and sum of exponentials of a row's softmax (masked entries add
@@ -109,10 +130,19 @@ template <class T, int LG>
 __device__ __forceinline__ T gate_of(const RouteArgs& a, T z, bool has, T top, T sum) {
   constexpr int L = LG < 3 ? LG : 3;
   if (a.renorm) {
-    const T l = a.sigmoid ? log_sigmoid(z) : z;
-    const bool number = has && l == l;
-    const T m = reduce<L>(number ? l : -inf<T>(), Max{});
-    const T e = has ? exp(l - m) : T(0);
+    T e;
+    // sigmoids far from underflow are divided as they are, others through their logarithms
+    bool plain = false;
+    if (a.sigmoid) {
+      e = has ? sigmoid(z) : T(0);
+      plain = __all(!has || e > T(1e-30));
+    }
+    if (!plain) {
+      const T l = a.sigmoid ? log_sigmoid(z) : z;
+      const bool number = has && l == l;
+      const T m = reduce<L>(number ? l : -inf<T>(), Max{});
+      e = has ? exp(l - m) : T(0);
+    }
     const T total = reduce<L>(e, Sum{});
     return has ? e / total : T(0);
   }
@@ -121,28 +151,35 @@ __device__ __forceinline__ T gate_of(const RouteArgs& a, T z, bool has, T top, T
 
 constexpr int kThreads = 256;
 
-// Rows of a wavefront: 64 >> LG.  BY_SCORE: the keys are scores (there is a
-// bias, or a group's two best are summed); otherwise the logits themselves,
-// which have the same order.
+// BY_SCORE: the keys are scores (there is a bias, or a group's two best are
+// summed); otherwise the logits themselves, which have the same order.
 template <class T, int LG, int VPL, bool BY_SCORE>
 __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __restrict__ logits,
                                                     const T* __restrict__ bias, int32_t* __restrict__ experts,
                                                     T* __restrict__ gates) {
-  constexpr int P = 1 << LG, kRows = kThreads / P;
-  __shared__ T keys[BY_SCORE ? kRows * P * VPL : 1];  // rows' keys, for the groups
-  __shared__ T best[BY_SCORE ? kRows * P : 1];
+  constexpr int P = 1 << LG, kRows = kThreads / P, X_MAX = P * VPL;
+  using Key = decltype(ordered(T(0)));
+  __shared__ T rows[kRows][X_MAX + 4];  // a row's scores, then its logits; rows start 4 banks apart
+  __shared__ T groups[BY_SCORE ? kRows : 1][BY_SCORE ? 64 : 1];
   const int sub = threadIdx.x & (P - 1), in_block = threadIdx.x >> LG;
+  T* const row = rows[in_block];
+  T* const group = groups[BY_SCORE ? in_block : 0];
+  const int per = a.X / a.groups;
   const int64_t step = int64_t(gridDim.x) * kRows;
+  T ahead[VPL];  // the next row's logits
+  auto load = [&](int64_t i0) {
+    const T* const zr = logits + min(i0 + in_block, a.n_rows - 1) * a.X;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) ahead[v] = zr[min(v * P + sub, a.X - 1)];
+  };
+  load(int64_t(blockIdx.x) * kRows);
   for (int64_t i0 = int64_t(blockIdx.x) * kRows; i0 < a.n_rows; i0 += step) {
     const int64_t i = min(i0 + in_block, a.n_rows - 1);  // lanes past the end redo the last row and write nothing
     const bool live = i0 + in_block < a.n_rows;
-    const T* const zr = logits + i * a.X;
-    T z[VPL], key[VPL];
+    T z[VPL], score[VPL];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int e = v * P + sub;
-      z[v] = e < a.X ? zr[e] : -inf<T>();
-    }
+    for (int v = 0; v < VPL; ++v) z[v] = v * P + sub < a.X ? ahead[v] : -inf<T>();
+    load(i0 + step);
     T top = 0, sum = 1;
     if (!a.sigmoid) softmax_stats<T, LG>(z, top, sum);
     const T inv = T(1) / sum;
@@ -152,62 +189,73 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
       T s = z[v];
       if (BY_SCORE) {
         s = a.sigmoid ? sigmoid(z[v]) : exp(z[v] - top) * inv;
-        if (bias != nullptr) s += bias[e < a.X ? e : 0];
+        if (bias != nullptr) s += bias[min(e, a.X - 1)];
       } else if (!a.sigmoid && sum != sum) {
         s = sum;  // a NaN row orders by index
       }
       const T low = lowest(T(0));
       s = s >= low ? s : low;  // NaN (and -inf from the bias) last of the unmasked
-      key[v] = z[v] == -inf<T>() ? -inf<T>() : s;
+      score[v] = z[v] == -inf<T>() ? -inf<T>() : s;
     }
+    uint32_t out_of_group = 0;  // bit v: the group of expert v * P + sub is not chosen
     if (BY_SCORE && a.top_groups < a.groups) {
-      T* const row = keys + in_block * (P * VPL);
-      T* const score = best + in_block * P;
-      __syncthreads();
+      wave_sync();
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) row[v * P + sub] = key[v];
-      __syncthreads();
-      const int per = a.X / a.groups;
-      T k1 = -inf<T>(), k2 = -inf<T>();
-      if (sub < a.groups)
-        for (int e = sub * per; e < (sub + 1) * per; ++e) {
+      for (int v = 0; v < VPL; ++v) row[v * P + sub] = score[v];
+      wave_sync();
+      for (int g = sub; g < a.groups; g += P) {
+        T k1 = -inf<T>(), k2 = -inf<T>();
+        for (int e = g * per; e < (g + 1) * per; ++e) {
           const T k = row[e];
           k2 = k > k1 ? k1 : (k > k2 ? k : k2);
           k1 = k > k1 ? k : k1;
         }
-      const T mine = k2 > -inf<T>() ? k1 + k2 : k1;
-      score[sub] = mine;
-      __syncthreads();
-      int rank = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const T other = score[g];
-        rank += other > mine || (other == mine && g < sub);
+        group[g] = k2 > -inf<T>() ? k1 + k2 : k1;
       }
-      const uint64_t inside = row_ballot<LG>(sub < a.groups && rank < a.top_groups && mine > -inf<T>());
+      wave_sync();
+      uint64_t chosen = 0;  // of this lane's groups, then of all of the row's
+      for (int g = sub; g < a.groups; g += P) {
+        const T mine = group[g];
+        int rank = 0;
+        for (int o = 0; o < a.groups; ++o) {
+          const T other = group[o];
+          rank += other > mine || (other == mine && o < g);
+        }
+        if (rank < a.top_groups && mine > -inf<T>()) chosen |= uint64_t(1) << g;
+      }
+      chosen = reduce<LG>(chosen, [](uint64_t x, uint64_t y) { return x | y; });
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
-        if (!((inside >> ((v * P + sub) / per & 63)) & 1)) key[v] = -inf<T>();
+        if (!((chosen >> ((v * P + sub) / per & 63)) & 1)) out_of_group |= 1u << v;
     }
+    Key key[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      key[v] = score[v] == -inf<T>() || ((out_of_group >> v) & 1) ? Key(0) : ordered(score[v]);
     // the next in the order (key descending, index ascending), top_k times
     int pick = -1;
     for (int j = 0; j < a.k; ++j) {
-      T m = key[0];
+      Key most = key[0];
+      int e = sub;
 #pragma unroll
-      for (int v = 1; v < VPL; ++v) m = key[v] > m ? key[v] : m;
-      m = reduce<LG>(m, Max{});
-      int e = -1;
-#pragma unroll
-      for (int v = VPL - 1; v >= 0; --v) {
-        const uint64_t have = row_ballot<LG>(key[v] == m && m > -inf<T>());
-        if (have != 0) e = v * P + __ffsll(static_cast<unsigned long long>(have)) - 1;
+      for (int v = 1; v < VPL; ++v) {
+        e = key[v] > most ? v * P + sub : e;
+        most = key[v] > most ? key[v] : most;
       }
+      const Key m = reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
+      e = static_cast<int>(reduce<LG>(static_cast<uint32_t>(most == m ? e : X_MAX),
+                                      [](uint32_t x, uint32_t y) { return x < y ? x : y; }));
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
-        if (e == v * P + sub) key[v] = -inf<T>();
-      if (sub == j) pick = e;
+        if (e == v * P + sub) key[v] = 0;
+      if (sub == j) pick = m != 0 ? e : -1;
     }
     const bool has = sub < a.k && pick >= 0;
-    T w = gate_of<T, LG>(a, has ? zr[pick] : T(0), has, top, sum);
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) row[v * P + sub] = z[v];
+    wave_sync();
+    T w = gate_of<T, LG>(a, has ? row[pick] : T(0), has, top, sum);
     if (!a.sigmoid && has && sum != sum) w = sum;  // NaN in, NaN out
     if (live && sub < a.k) {
       experts[i * a.k + sub] = pick;
@@ -222,24 +270,33 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a, const T* _
                                                          const T* __restrict__ grad, T* __restrict__ out) {
   constexpr int P = 1 << LG, kRows = kThreads / P, L = LG < 3 ? LG : 3;
   const int sub = threadIdx.x & (P - 1), in_block = threadIdx.x >> LG;
-  const int first = threadIdx.x & 63 & ~(P - 1);  // the row's first lane
   const int64_t step = int64_t(gridDim.x) * kRows;
   const T scale = static_cast<T>(a.scale);
-  for (int64_t i0 = int64_t(blockIdx.x) * kRows; i0 < a.n_rows; i0 += step) {
-    const int64_t i = min(i0 + in_block, a.n_rows - 1);
+  // lane j: the j-th chosen expert, its logit and the gradient of its gate,
+  // the expert two rows ahead and the others one
+  auto row_at = [&](int64_t i0) { return min(i0 + in_block, a.n_rows - 1); };
+  auto expert = [&](int64_t i0) {
+    const int e = experts[row_at(i0) * a.k + min(sub, a.k - 1)];
+    return sub < a.k && e >= 0 && e < a.X ? e : -1;
+  };
+  const int64_t begin = int64_t(blockIdx.x) * kRows;
+  int pick1 = expert(begin), pick2 = expert(begin + step);
+  T g1, z1;
+  auto load = [&](int64_t i0, int pick) {
+    const int64_t i = row_at(i0);
+    g1 = grad[i * a.k + min(sub, a.k - 1)];
+    z1 = logits[i * a.X + max(pick, 0)];
+  };
+  load(begin, pick1);
+  for (int64_t i0 = begin; i0 < a.n_rows; i0 += step) {
+    const int64_t i = row_at(i0);
     const bool live = i0 + in_block < a.n_rows;
     const T* const zr = logits + i * a.X;
-    // lane j: the j-th chosen expert, its logit and the gradient of its gate.
-    int pick = -1;
-    T g = 0, zp = 0;
-    if (sub < a.k) {
-      const int e = experts[i * a.k + sub];
-      if (e >= 0 && e < a.X) {
-        pick = e;
-        g = grad[i * a.k + sub];
-        zp = zr[e];
-      }
-    }
+    const int pick = pick1;
+    const T g = pick >= 0 ? g1 : T(0), zp = pick >= 0 ? z1 : T(0);
+    pick1 = pick2;
+    load(i0 + step, pick1);
+    pick2 = expert(i0 + 2 * step);
     T top = 0, sum = 1;
     T z[VPL];
     if (!a.renorm && !a.sigmoid) {
@@ -250,20 +307,21 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a, const T* _
     const T w = gate_of<T, LG>(a, zp, pick >= 0, top, sum);
     const T inner = reduce<L>(g * w, Sum{});
     // what lane j's expert gets
-    T d = a.renorm ? w * (g - __shfl(inner, first, 64)) : w * g;
+    const T all = of_lane<LG>(inner, 0);
+    T d = a.renorm ? w * (g - all) : w * g;
     if (a.sigmoid) d *= sigmoid(-zp);
     T dz[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) dz[v] = T(0);
     for (int j = 0; j < a.k; ++j) {
-      const int e = __shfl(pick, first + j, 64);
-      const T t = __shfl(d, first + j, 64);
+      const int e = of_lane<LG>(pick, j);
+      const T t = of_lane<LG>(d, j);
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
         if (e == v * P + sub) dz[v] += t;
     }
     if (!a.renorm && !a.sigmoid) {
-      const T all = __shfl(inner, first, 64), inv = T(1) / sum;
+      const T inv = T(1) / sum;
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
         if (!(z[v] == -inf<T>())) dz[v] -= exp(z[v] - top) * inv * all;
@@ -285,15 +343,15 @@ template <class F>
 hipError_t with_shape(int X, F f) {
   if (X <= 8) return f(Shape<3, 1>{});  // 8 lanes at least: a place for each of top_k
   if (X <= 16) return f(Shape<4, 1>{});
-  if (X <= 32) return f(Shape<5, 1>{});
-  if (X <= 64) return f(Shape<6, 1>{});
-  if (X <= 128) return f(Shape<6, 2>{});
-  return f(Shape<6, 4>{});
+  if (X <= 32) return f(Shape<4, 2>{});
+  if (X <= 64) return f(Shape<4, 4>{});
+  if (X <= 128) return f(Shape<4, 8>{});
+  return f(Shape<4, 16>{});
 }
 
 dim3 grid_of(int64_t n_rows, int lg) {
   const int64_t rows = kThreads >> lg, g = (n_rows + rows - 1) / rows;
-  return dim3(static_cast<unsigned>(g < 4096 ? g : 4096));  // 16 blocks' wavefronts a SIMD, then rows in turn
+  return dim3(static_cast<unsigned>(g < 4096 ? g : 4096));  // 16 wavefronts for each SIMD, then rows in turn
 }
 
 template <class T>
