@@ -52,9 +52,10 @@ int blocks_for(int64_t n, int block) {
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // ------------------------------------------------------------------ layout
-// Rows are taken in groups of kGroup (or n / 64 when that is more, so that
-// there are at most 64 groups); each group is sorted by itself, which needs
-// no exchange between blocks: one launch whatever the size.
+// Rows are taken in groups of kGroup, fewer where top_k makes more than twice
+// as many entries of them (or of n / 64 when that is more: at most 64 groups);
+// each group is sorted by itself, which needs no exchange between blocks: one
+// launch whatever the size.
 //   order    the group's rows by the pair (smallest, next) of their experts, so
 //            that a tile of consecutive rows meets few experts
 //   entries  the group's entries (row * top_k + place) by expert, entries of an
@@ -74,7 +75,7 @@ struct LayoutShape {
 
 LayoutShape layout_shape(int64_t n, int X, int k) {
   LayoutShape L{};
-  L.group = std::max<int64_t>(kGroup, (n + 63) / 64);
+  L.group = std::max<int64_t>(std::min<int64_t>(kGroup, 2 * kGroup / k), (n + 63) / 64);
   L.n_groups = std::max<int64_t>(1, (n + L.group - 1) / L.group);
   const int64_t most = std::min(L.group, std::max<int64_t>(n, 1)) * k;
   L.max_pieces = most / kPiece + X;
@@ -132,12 +133,12 @@ __device__ int scan_counters(int* c, int n, int* wave_sums) {
   return total;
 }
 
-// One block per group.  Bins of the row order: (smallest expert) * H + (next
+// Two blocks per group.  Bins of the row order: (smallest expert) * H + (next
 // * H / X), H = min(X, 4096 / X); rows without experts last.  Rows of one bin
 // come in no fixed order (an integer atomic hands out the places): a row's
 // results do not depend on its neighbours.  Entries are ranked by counting in
 // order, so theirs is fixed.  Latency bound, so the group's experts are read
-// once, into LDS, where they fit.
+// once, into LDS, where they fit, and the two sorts run in blocks of their own.
 constexpr int kStaged = 16384;
 
 __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group,
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
   __shared__ int bins[kMaxBins + 1];
   __shared__ int wave_sums[16];
   __shared__ uint16_t staged[kStaged];
-  const int64_t r0 = blockIdx.x * group;
+  const int64_t grp = blockIdx.x >> 1, r0 = grp * group;
   const int rows = static_cast<int>(min(group, n - r0));
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, nw = blockDim.x >> 6;
   const int32_t* ex = experts + r0 * k;
@@ -165,37 +166,39 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
     }
   auto expert = [&](int q) { return in_lds ? int(staged[q]) : clean(ex[q]); };
 
-  auto bin_of = [&](int r) {
-    int lo = X, hi = X;
-    for (int a = 0; a < k; ++a) {
-      const int e = expert(r * k + a);
-      hi = e < lo ? lo : (e > lo && e < hi ? e : hi);
-      lo = min(lo, e);
+  if ((blockIdx.x & 1) == 0) {
+    auto bin_of = [&](int r) {
+      int lo = X, hi = X;
+      for (int a = 0; a < k; ++a) {
+        const int e = expert(r * k + a);
+        hi = e < lo ? lo : (e > lo && e < hi ? e : hi);
+        lo = min(lo, e);
+      }
+      if (lo == X) return X * H;
+      return lo * H + (hi == X ? lo : hi) * H / X;
+    };
+    for (int q = tid; q <= X * H; q += blockDim.x) bins[q] = 0;
+    __syncthreads();
+    constexpr int kKept = 2;  // rows of a thread whose bins are kept (all of them in a group of 2048)
+    int kept[kKept];
+#pragma unroll
+    for (int j = 0; j < kKept; ++j) {
+      const int r = tid + j * blockDim.x;
+      kept[j] = r < rows ? bin_of(r) : 0;
+      if (r < rows) atomicAdd(&bins[kept[j]], 1);
     }
-    if (lo == X) return X * H;
-    return lo * H + (hi == X ? lo : hi) * H / X;
-  };
-  for (int q = tid; q <= X * H; q += blockDim.x) bins[q] = 0;
-  __syncthreads();
-  constexpr int kKept = 2;  // rows of a thread whose bins are kept (all of them in a group of 2048)
-  int kept[kKept];
+    for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x) atomicAdd(&bins[bin_of(r)], 1);
+    __syncthreads();
+    scan_counters(bins, X * H + 1, wave_sums);
 #pragma unroll
-  for (int j = 0; j < kKept; ++j) {
-    const int r = tid + j * blockDim.x;
-    kept[j] = r < rows ? bin_of(r) : 0;
-    if (r < rows) atomicAdd(&bins[kept[j]], 1);
+    for (int j = 0; j < kKept; ++j) {
+      const int r = tid + j * blockDim.x;
+      if (r < rows) order[r0 + atomicAdd(&bins[kept[j]], 1)] = static_cast<int32_t>(r0 + r);
+    }
+    for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x)
+      order[r0 + atomicAdd(&bins[bin_of(r)], 1)] = static_cast<int32_t>(r0 + r);
+    return;
   }
-  for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x) atomicAdd(&bins[bin_of(r)], 1);
-  __syncthreads();
-  scan_counters(bins, X * H + 1, wave_sums);
-#pragma unroll
-  for (int j = 0; j < kKept; ++j) {
-    const int r = tid + j * blockDim.x;
-    if (r < rows) order[r0 + atomicAdd(&bins[kept[j]], 1)] = static_cast<int32_t>(r0 + r);
-  }
-  for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x)
-    order[r0 + atomicAdd(&bins[bin_of(r)], 1)] = static_cast<int32_t>(r0 + r);
-  __syncthreads();
 
   // entries by expert: each wavefront counts, then places, its own run of them;
   // counters [expert][wavefront], scanned in that order
@@ -209,8 +212,8 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
   }
   __syncthreads();
   const int placed = scan_counters(bins, X * nw, wave_sums);
-  int32_t* const fst = first + blockIdx.x * int64_t(X + 1);
-  int32_t* const pcs = pieces + blockIdx.x * int64_t(X + 1);
+  int32_t* const fst = first + grp * (X + 1);
+  int32_t* const pcs = pieces + grp * (X + 1);
   int mine = 0;  // X <= 256 <= blockDim
   if (tid < X) {
     const int at = bins[tid * nw], end = tid + 1 < X ? bins[(tid + 1) * nw] : placed;
@@ -299,22 +302,26 @@ struct RowArgs {
 // instruction reads 16 banks apart.
 constexpr int pitch_of(int d) { return 16 * d + 4; }
 
-// Sum over the 16 lanes of a row of lanes, in all of them.
+// Four values of each of the 16 lanes of a row of lanes, each summed over the
+// lanes: lane q of every four holds the q-th sum.  The first two steps halve
+// the values while they add (11 additions and selections for 16).
 template <int CTRL>
-__device__ __forceinline__ float rotate16(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+__device__ __forceinline__ float moved(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 template <int CTRL>
-__device__ __forceinline__ double rotate16(double v) {
-  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
-                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, false));
+__device__ __forceinline__ double moved(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true));
 }
 template <class T>
-__device__ __forceinline__ T sum16(T v) {  // rotations by 8, 4, 2, 1
-  v += rotate16<0x128>(v);
-  v += rotate16<0x124>(v);
-  v += rotate16<0x122>(v);
-  return v + rotate16<0x121>(v);
+__device__ __forceinline__ T sums16(const T (&v)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const T a = (odd ? v[1] : v[0]) + moved<0xB1>(odd ? v[0] : v[1]);  // with the lane next to it
+  const T b = (odd ? v[3] : v[2]) + moved<0xB1>(odd ? v[2] : v[3]);
+  T s = (high ? b : a) + moved<0x4E>(high ? a : b);  // with the pair next to it
+  s += moved<0x124>(s);                              // and the other fours: rotations by 4 and 8
+  return s + moved<0x128>(s);
 }
 
 // A value the compiler takes for new: what is computed from it stays where it
@@ -606,13 +613,13 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
 #pragma unroll
         for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 16 * c + Mfma<T>::row(g4, q);
-          acc[c][q] += grow[r] * prod[q];
-          if (GG) {
-            const T v = sum16(prod[q] * mine[GG ? c : 0][q]);
-            if (i16 == 0) rsum[r] = v;
-          }
+        for (int q = 0; q < 4; ++q) acc[c][q] += grow[16 * c + Mfma<T>::row(g4, q)] * prod[q];
+        if (GG) {
+          T v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = prod[q] * mine[GG ? c : 0][q];
+          const T s = sums16(v, i16);
+          if (i16 < 4) rsum[16 * c + Mfma<T>::row(g4, i16)] = s;
         }
       }
       if (GG && lane < kTile && ((members >> lane) & 1)) {  // the expert's rows, each over its components
@@ -1143,8 +1150,9 @@ hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* exp
   char* const at = static_cast<char*>(layout);
   auto ints = [&](size_t off) { return reinterpret_cast<int32_t*>(at + off); };
   const int H = std::min(X, kMaxBins / X);
-  const int threads = std::min(L.group, n) > 1024 ? 1024 : 256;
-  hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(L.n_groups)), dim3(threads), 0, s, n, X, p.top_k, H,
+  const int threads = std::min(L.group, n) * p.top_k > 1024 ? 1024 : 256;
+  hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(2 * L.n_groups)), dim3(threads), 0, s, n, X, p.top_k,
+                     H,
                      L.group, experts, ints(L.order), ints(L.entries), ints(L.first), ints(L.pieces));
   if (load != nullptr) hipLaunchKernelGGL(k_load, dim3(1), dim3(256), 0, s, X, L.n_groups, ints(L.first), load);
   return hipGetLastError();
