@@ -654,7 +654,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
 }
 
 template <class T, int KS, bool ADJ, bool GG>
-__global__ __launch_bounds__(256, sizeof(T) == 8 || GG ? 2 : (ADJ ? 3 : 4)) void k_rows(
+__global__ __launch_bounds__(256, sizeof(T) == 8 ? 2 : (ADJ ? 3 : 4)) void k_rows(
     RowArgs a, const T* __restrict__ src, const T* __restrict__ weights, const int32_t* __restrict__ experts,
     const T* __restrict__ gates, const int32_t* __restrict__ order, T* __restrict__ dst, const T* __restrict__ other,
     T* __restrict__ gate_part) {
