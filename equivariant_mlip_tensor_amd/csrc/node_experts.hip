@@ -58,6 +58,8 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 // launch whatever the size.
 //   order    the group's rows by the pair (smallest, next) of their experts, so
 //            that a tile of consecutive rows meets few experts
+//   listed   the rows' experts in that order (a tile's are then one run, known
+//            without its row numbers)
 //   entries  the group's entries (row * top_k + place) by expert, entries of an
 //            expert in ascending order (the sums over them are taken in it)
 //   first    [group][X + 1] where each expert's entries start in `entries`,
@@ -70,7 +72,7 @@ constexpr int kPiece = 128;
 struct LayoutShape {
   int64_t group, n_groups;
   int64_t max_pieces;  // pieces of a group, at most
-  size_t order, entries, first, pieces, total;
+  size_t order, listed, entries, first, pieces, total;
 };
 
 LayoutShape layout_shape(int64_t n, int X, int k) {
@@ -86,6 +88,7 @@ LayoutShape layout_shape(int64_t n, int X, int k) {
     return at;
   };
   L.order = take(n);
+  L.listed = take(n * k);
   L.entries = take(n * k);
   L.first = take(L.n_groups * (X + 1));
   L.pieces = take(L.n_groups * (X + 1));
@@ -143,7 +146,7 @@ constexpr int kStaged = 16384;
 
 __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group,
                                                  const int32_t* __restrict__ experts, int32_t* __restrict__ order,
-                                                 int32_t* __restrict__ entries, int32_t* __restrict__ first,
+                                                 int32_t* __restrict__ listed, int32_t* __restrict__ entries, int32_t* __restrict__ first,
                                                  int32_t* __restrict__ pieces) {
   __shared__ int bins[kMaxBins + 1];
   __shared__ int wave_sums[16];
@@ -177,6 +180,10 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
       if (lo == X) return X * H;
       return lo * H + (hi == X ? lo : hi) * H / X;
     };
+    auto put = [&](int r, int at) {
+      order[r0 + at] = static_cast<int32_t>(r0 + r);
+      for (int a = 0; a < k; ++a) listed[(r0 + at) * k + a] = expert(r * k + a);
+    };
     for (int q = tid; q <= X * H; q += blockDim.x) bins[q] = 0;
     __syncthreads();
     constexpr int kKept = 2;  // rows of a thread whose bins are kept (all of them in a group of 2048)
@@ -193,10 +200,9 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
 #pragma unroll
     for (int j = 0; j < kKept; ++j) {
       const int r = tid + j * blockDim.x;
-      if (r < rows) order[r0 + atomicAdd(&bins[kept[j]], 1)] = static_cast<int32_t>(r0 + r);
+      if (r < rows) put(r, atomicAdd(&bins[kept[j]], 1));
     }
-    for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x)
-      order[r0 + atomicAdd(&bins[bin_of(r)], 1)] = static_cast<int32_t>(r0 + r);
+    for (int r = tid + kKept * blockDim.x; r < rows; r += blockDim.x) put(r, atomicAdd(&bins[bin_of(r)], 1));
     return;
   }
 
@@ -280,7 +286,6 @@ struct RowMap {
   int32_t V;                 // row length of the map's weights
   int32_t d, woff;
   int32_t packed;            // bit 0: 16-byte pieces of src, bit 1: of dst, bit 2: of the weights along K
-  int32_t first;             // first share (a map's block of output channels) of this map
 };
 
 // LDS of a block (byte offsets)
@@ -289,6 +294,7 @@ struct RowLds {
 };
 
 struct RowArgs {
+  int32_t first[kMaxMaps];  // first share (a map's block of output channels) of each map, INT32_MAX past the last map
   int64_t n_rows, ld_src, ld_dst, weight_numel;
   int32_t X, k, n_maps, waves;
   int32_t tile;       // rows of a tile, at most kTile
@@ -429,9 +435,10 @@ struct TileMover {
 };
 
 // One block's work on a map of components D, the rows' starts being in LDS.
-// KS: channels summed over in a pass / 4; VS, VD: 16-byte pieces of src / dst.
+// KS: channels summed over in a pass / 4; VS, VD: 16-byte pieces of src / dst;
+// experts: in the rows' order here.
 template <class T, int D, int KS, bool ADJ, bool GG, bool VS, bool VD>
-__device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int share, int64_t base, int rows,
+__device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int share, int n_base, int64_t base, int rows,
                                          char* lds, const T* __restrict__ src, const T* __restrict__ weights,
                                          const int32_t* __restrict__ experts, const T* __restrict__ gates,
                                          const int32_t* __restrict__ order, T* __restrict__ dst,
@@ -455,15 +462,15 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
 
   // The tile's entries, then its rows, are on their way while its experts are
   // listed: one trip to memory for the row numbers, one for all that they name.
-  const int n_base = (share - m.first) * 16 * a.waves, n_here = min(16 * a.waves, m.N - n_base);
+  const int n_here = min(16 * a.waves, m.N - n_base);
   const int n_entries = rows * k;
   auto row_of = [&](int s) -> int64_t { return order != nullptr ? order[base + s] : base + s; };
   auto src_row = [&](int s) { return rowid[s] * a.ld_src; };
   auto dst_row = [&](int s) { return rowid[s] * a.ld_dst; };
   const int q0 = min(tid, n_entries - 1), s0 = q0 / k;
-  const int64_t row0 = row_of(s0), at0 = row0 * k + (q0 - s0 * k);
-  const int e0 = experts[at0];
-  const T g0 = gates[at0];
+  const int e0 = experts[base * k + q0];
+  const int64_t row0 = row_of(s0);
+  const T g0 = gates[row0 * k + (q0 - s0 * k)];
   TileMover<T, D, CH, VS ? kPer : 1> mover;
   TileMover<T, D, 64, VD ? kPer : 1> mover_dst;
   const T* const src_from = src + m.src_off;
@@ -491,8 +498,8 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   if (tid < n_entries) note(q0, s0, row0, e0, g0);
   for (int q = tid + blockDim.x; q < n_entries; q += blockDim.x) {
     const int s = q / k;
-    const int64_t row = row_of(s), at = row * k + (q - s * k);
-    note(q, s, row, experts[at], gates[at]);
+    const int64_t row = row_of(s);
+    note(q, s, row, experts[base * k + q], gates[row * k + (q - s * k)]);
   }
   __syncthreads();
   if (w == 0) {  // experts present, ascending, and the members before each
@@ -661,18 +668,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 8 ? 2 : (ADJ ? 3 : 4)) void k_row
   extern __shared__ char lds[];
   const int share = static_cast<int>(blockIdx.x) / a.n_tiles;
   int mi = 0;
-  while (mi + 1 < a.n_maps && share >= a.map[mi + 1].first) ++mi;
+#pragma unroll
+  for (int q = 1; q < kMaxMaps; ++q) mi += share >= a.first[q];
   const RowMap& m = a.map[mi];
   const int64_t base = int64_t(static_cast<int>(blockIdx.x) - share * a.n_tiles) * a.tile;
   const int rows = static_cast<int>(min<int64_t>(a.tile, a.n_rows - base));
+  const int n_base = (share - a.first[mi]) * 16 * a.waves;
 #define TPCONV_MAP_ROWS(D)                                                                                         \
   case D:                                                                                                          \
     if ((m.packed & 3) == 3)                                                                                       \
-      map_rows<T, D, KS, ADJ, GG, true, true>(a, m, share, base, rows, lds, src, weights, experts, gates, order,   \
-                                              dst, other, gate_part);                                              \
+      map_rows<T, D, KS, ADJ, GG, true, true>(a, m, share, n_base, base, rows, lds, src, weights, experts, gates,  \
+                                              order, dst, other, gate_part);                                       \
     else                                                                                                           \
-      map_rows<T, D, KS, ADJ, GG, false, false>(a, m, share, base, rows, lds, src, weights, experts, gates, order, \
-                                                dst, other, gate_part);                                            \
+      map_rows<T, D, KS, ADJ, GG, false, false>(a, m, share, n_base, base, rows, lds, src, weights, experts,        \
+                                                gates, order, dst, other, gate_part);                              \
     break;
   switch (m.d) {
     TPCONV_MAP_ROWS(1)
@@ -939,11 +948,23 @@ hipError_t rows_ks(const RowArgs& a, unsigned blocks, const T* src, const T* wei
   return hipGetLastError();
 }
 
+// The rows' order and their experts in it; both NULL without a layout.
+struct RowOrder {
+  const int32_t *order = nullptr, *listed = nullptr;
+};
+
+RowOrder order_in(const Experts& p, int64_t n, const void* layout) {
+  if (layout == nullptr) return {};
+  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
+  const char* const at = static_cast<const char*>(layout);
+  return {reinterpret_cast<const int32_t*>(at + L.order), reinterpret_cast<const int32_t*>(at + L.listed)};
+}
+
 // n_parts: into how many partial sums the gates' gradient went, one for each
 // block of output channels of each map.
 template <class T, bool ADJ, bool GG>
 hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, const int32_t* experts, const T* gates,
-                const int32_t* order, T* dst, const T* other, T* part, T* gate_grad, int& n_parts, hipStream_t s) {
+                const RowOrder& layout, T* dst, const T* other, T* part, T* gate_grad, int& n_parts, hipStream_t s) {
   RowArgs a{};
   a.n_rows = n;
   a.ld_src = ADJ ? p.dim_out : p.dim_in;
@@ -981,8 +1002,9 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
   // With few rows the tiles are made smaller, to have two wavefronts for each
   // of the 1024 SIMDs.
   n_parts = 0;
+  std::fill(a.first, a.first + kMaxMaps, INT32_MAX);
   for (int q = 0; q < a.n_maps; ++q) {
-    a.map[q].first = n_parts;
+    a.first[q] = n_parts;
     n_parts += (a.map[q].N + 16 * a.waves - 1) / (16 * a.waves);
   }
   a.tile = static_cast<int32_t>(std::min<int64_t>(kTile, std::max<int64_t>(1, n * n_parts * a.waves / 2048)));
@@ -1016,15 +1038,11 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
     if (dst != nullptr)
       hipLaunchKernelGGL(k_zero_columns<T>, dim3(blocks_for(n * r.len, 256)), dim3(256), 0, s, n, a.ld_dst, r.off,
                          r.len, dst);
+  const int32_t* const order = layout.order;
+  if (layout.listed != nullptr) experts = layout.listed;
   if (KS == 4) return rows_ks<T, 4, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
   if (KS == 8) return rows_ks<T, 8, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
   return rows_ks<T, 16, ADJ, GG>(a, blocks, src, weights, experts, gates, order, dst, other, gg, s);
-}
-
-const int32_t* order_in(const Experts& p, int64_t n, const void* layout) {
-  if (layout == nullptr) return nullptr;
-  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
-  return reinterpret_cast<const int32_t*>(static_cast<const char*>(layout) + L.order);
 }
 
 // Workspace of the backward: the maps' shares of the gates' gradient, then the
@@ -1055,7 +1073,7 @@ hipError_t wgrad_launch(const WgradArgs& a, int64_t blocks, const T* x, const T*
 template <class T>
 hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, const int32_t* experts, const T* gates,
                     const void* layout, const T* grad, T* gx, T* gw, T* gg, void* ws, hipStream_t s) {
-  const int32_t* order = order_in(p, n, layout);
+  const RowOrder order = order_in(p, n, layout);
   int64_t n_gates = gg != nullptr ? n * p.top_k : 0;
   const int n_maps = static_cast<int>(p.maps.size()), X = p.n_experts;
   int n_parts = 1;
@@ -1153,7 +1171,7 @@ hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* exp
   const int threads = std::min(L.group, n) * p.top_k > 1024 ? 1024 : 256;
   hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(2 * L.n_groups)), dim3(threads), 0, s, n, X, p.top_k,
                      H,
-                     L.group, experts, ints(L.order), ints(L.entries), ints(L.first), ints(L.pieces));
+                     L.group, experts, ints(L.order), ints(L.listed), ints(L.entries), ints(L.first), ints(L.pieces));
   if (load != nullptr) hipLaunchKernelGGL(k_load, dim3(1), dim3(256), 0, s, X, L.n_groups, ints(L.first), load);
   return hipGetLastError();
 }
@@ -1161,7 +1179,7 @@ hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* exp
 hipError_t launch_experts_forward(const Experts& p, int64_t n, const void* x, const void* weights,
                                   const int32_t* experts, const void* gates, const void* layout, void* out,
                                   hipStream_t s) {
-  const int32_t* order = order_in(p, n, layout);
+  const RowOrder order = order_in(p, n, layout);
   int n_parts;
   if (p.f64)
     return rows<double, false, false>(p, n, static_cast<const double*>(x), static_cast<const double*>(weights),
