@@ -28,10 +28,15 @@ __device__ __forceinline__ T log_sigmoid(T z) {
   return (z < T(0) ? z : T(0)) - log1p(exp(z < T(0) ? z : -z));
 }
 
+// a / b for 1 <= b: the reciprocal instruction is good to a unit in the last
+// place, a tenth of a division's cost
+__device__ __forceinline__ float over(float a, float b) { return a * __builtin_amdgcn_rcpf(b); }
+__device__ __forceinline__ double over(double a, double b) { return a / b; }
+
 template <class T>
 __device__ __forceinline__ T sigmoid(T z) {
   const T e = exp(z < T(0) ? z : -z);
-  return (z < T(0) ? e : T(1)) / (T(1) + e);
+  return over(z < T(0) ? e : T(1), T(1) + e);
 }
 
 // ------------------------------------------------- reductions over 2^LG lanes
@@ -173,6 +178,15 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
     for (int v = 0; v < VPL; ++v) ahead[v] = zr[min(v * P + sub, a.X - 1)];
   };
   load(int64_t(blockIdx.x) * kRows);
+  T shift[BY_SCORE ? VPL : 1];     // the experts' biases
+  int group_of[BY_SCORE ? VPL : 1];
+  if (BY_SCORE)
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = min(v * P + sub, a.X - 1);
+      shift[v] = bias != nullptr ? bias[e] : T(0);
+      group_of[v] = e / per;
+    }
   for (int64_t i0 = int64_t(blockIdx.x) * kRows; i0 < a.n_rows; i0 += step) {
     const int64_t i = min(i0 + in_block, a.n_rows - 1);  // lanes past the end redo the last row and write nothing
     const bool live = i0 + in_block < a.n_rows;
@@ -185,11 +199,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
     const T inv = T(1) / sum;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int e = v * P + sub;
       T s = z[v];
       if (BY_SCORE) {
-        s = a.sigmoid ? sigmoid(z[v]) : exp(z[v] - top) * inv;
-        if (bias != nullptr) s += bias[min(e, a.X - 1)];
+        s = (a.sigmoid ? sigmoid(z[v]) : exp(z[v] - top) * inv) + shift[BY_SCORE ? v : 0];
       } else if (!a.sigmoid && sum != sum) {
         s = sum;  // a NaN row orders by index
       }
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
       chosen = reduce<LG>(chosen, [](uint64_t x, uint64_t y) { return x | y; });
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
-        if (!((chosen >> ((v * P + sub) / per & 63)) & 1)) out_of_group |= 1u << v;
+        if (!((chosen >> group_of[BY_SCORE ? v : 0]) & 1)) out_of_group |= 1u << v;
     }
     Key key[VPL];
 #pragma unroll
@@ -236,15 +248,13 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
     int pick = -1;
     for (int j = 0; j < a.k; ++j) {
       Key most = key[0];
-      int e = sub;
 #pragma unroll
-      for (int v = 1; v < VPL; ++v) {
-        e = key[v] > most ? v * P + sub : e;
-        most = key[v] > most ? key[v] : most;
-      }
+      for (int v = 1; v < VPL; ++v) most = key[v] > most ? key[v] : most;
       const Key m = reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
-      e = static_cast<int>(reduce<LG>(static_cast<uint32_t>(most == m ? e : X_MAX),
-                                      [](uint32_t x, uint32_t y) { return x < y ? x : y; }));
+      uint32_t at = X_MAX;
+#pragma unroll
+      for (int v = VPL - 1; v >= 0; --v) at = key[v] == m ? v * P + sub : at;
+      const int e = static_cast<int>(reduce<LG>(at, [](uint32_t x, uint32_t y) { return x < y ? x : y; }));
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
         if (e == v * P + sub) key[v] = 0;

@@ -136,7 +136,7 @@ def tpconv_embedding_forward(types, table, scale: float = 1.0, out=None, stream=
     _need(types, (n,), torch.int32, "types")
     _need(table, (n_types, dim), dt, "table")
     if out is None:
-        out = torch.empty((n, dim), dtype=dt, device=table.device)
+        out = table.new_empty((n, dim))
     stride = _rows_view(out, n, dim, dt, "out")
     _check(_lib.tpconv_embedding_forward(code, n, n_types, dim, _ptr(types), _ptr(table), float(scale), _ptr(out),
                                          stride, _stream_handle(stream)))
@@ -155,7 +155,7 @@ def tpconv_embedding_backward(types, grad_out, n_types: int, scale: float = 1.0,
     _need(types, (n,), torch.int32, "types")
     stride = _rows_view(grad_out, n, dim, dt, "grad_out")
     if grad_table is None:
-        grad_table = torch.empty((n_types, dim), dtype=dt, device=grad_out.device)
+        grad_table = grad_out.new_empty((n_types, dim))
     _need(grad_table, (n_types, dim), dt, "grad_table")
     if workspace is None:
         need = int(_lib.tpconv_embedding_workspace_bytes(code, n, n_types, dim))
@@ -200,7 +200,7 @@ def tpconv_route_forward(config: RouteConfig, logits, bias=None, experts=None, g
     if experts is None:
         experts = torch.empty(shape, dtype=torch.int32, device=dev)
     if gates is None:
-        gates = torch.empty(shape, dtype=dt, device=dev)
+        gates = logits.new_empty(shape)
     _need(experts, shape, torch.int32, "experts")
     _need(gates, shape, dt, "gates")
     _check(_lib.tpconv_route_forward(code, n, config._ref, _ptr(logits), _ptr(bias), _ptr(experts), _ptr(gates),
@@ -320,7 +320,7 @@ def tpconv_experts_forward(plan: ExpertsPlan, x, weights, experts, gates, layout
     _need(experts, (n, k), torch.int32, "experts")
     _need(gates, (n, k), dt, "gates")
     if out is None:
-        out = torch.empty((n, plan.dim_out), dtype=dt, device=x.device)
+        out = x.new_empty((n, plan.dim_out))
     _need(out, (n, plan.dim_out), dt, "out")
     _check(_lib.tpconv_experts_forward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(experts), _ptr(gates),
                                        _layout_of(plan, n, layout), _ptr(out), _stream_handle(stream)))
