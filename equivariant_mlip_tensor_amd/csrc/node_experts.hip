@@ -64,23 +64,28 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 //            expert in ascending order (the sums over them are taken in it)
 //   first    [group][X + 1] where each expert's entries start in `entries`,
 //            relative to the group's first
-//   piece    [group][X + 1] the same in pieces of at most kPiece entries
+//   pieces   [group][X + 1] the same in pieces of at most `piece` entries
 constexpr int64_t kGroup = 2048;
 constexpr int kMaxBins = 4096;
-constexpr int kPiece = 128;
+constexpr int kPiece = 128, kLeastPiece = 32;
 
 struct LayoutShape {
   int64_t group, n_groups;
+  int32_t piece;       // entries of a piece, at most
   int64_t max_pieces;  // pieces of a group, at most
   size_t order, listed, entries, first, pieces, total;
 };
 
-LayoutShape layout_shape(int64_t n, int X, int k) {
+LayoutShape layout_shape(const Experts& p, int64_t n) {
+  const int X = p.n_experts, k = p.top_k;
   LayoutShape L{};
+  // pieces of all maps for 4 blocks a CU; longer ones (fewer sums to add) where there are entries enough
+  L.piece = kLeastPiece;
+  while (L.piece < kPiece && n * k * int64_t(p.maps.size()) > int64_t(1024) * L.piece) L.piece *= 2;
   L.group = std::max<int64_t>(std::min<int64_t>(kGroup, 2 * kGroup / k), (n + 63) / 64);
   L.n_groups = std::max<int64_t>(1, (n + L.group - 1) / L.group);
   const int64_t most = std::min(L.group, std::max<int64_t>(n, 1)) * k;
-  L.max_pieces = most / kPiece + X;
+  L.max_pieces = most / L.piece + X;
   size_t o = 0;
   auto take = [&](int64_t ints) {
     const size_t at = o;
@@ -144,7 +149,7 @@ __device__ int scan_counters(int* c, int n, int* wave_sums) {
 // once, into LDS, where they fit, and the two sorts run in blocks of their own.
 constexpr int kStaged = 16384;
 
-__global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group,
+__global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group, int piece,
                                                  const int32_t* __restrict__ experts, int32_t* __restrict__ order,
                                                  int32_t* __restrict__ listed, int32_t* __restrict__ entries, int32_t* __restrict__ first,
                                                  int32_t* __restrict__ pieces) {
@@ -224,7 +229,7 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
   if (tid < X) {
     const int at = bins[tid * nw], end = tid + 1 < X ? bins[(tid + 1) * nw] : placed;
     fst[tid] = at;
-    mine = static_cast<int>((end - at + kPiece - 1) / kPiece);
+    mine = static_cast<int>((end - at + piece - 1) / piece);
   }
   int n_pieces;
   const int before = block_exclusive(mine, wave_sums, n_pieces);
@@ -704,7 +709,7 @@ __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t
 // ------------------------------------------------------- weights' gradient
 // grad_M_e = sum over e's entries and components of x (gate G)^T: a matrix
 // product whose inner dimension is the (entry, component) pairs of an expert.
-// A block takes one piece (at most kPiece entries of one expert and group), one
+// A block takes one piece (at most 128 entries of one expert and group), one
 // map and one S x S tile of it.  Stages of a few entries are gathered into LDS
 // with the components split out ([component row][channel]), while the next
 // stage's loads are in flight in registers; 4 wavefronts share the tile (S =
@@ -722,7 +727,7 @@ struct WgradArgs {
   int64_t dim_in, dim_out, weight_numel;
   int64_t max_pieces, group;
   int64_t slots;  // pieces of all groups, at most
-  int32_t X, k, n_maps;
+  int32_t X, k, n_maps, piece;
   int32_t direct;  // every expert has one piece at most: straight into grad_weights, zeros for those without
   WgradMap map[kMaxMaps];
 };
@@ -772,8 +777,8 @@ __global__ __launch_bounds__(256) void k_wgrad(WgradArgs a, const T* __restrict_
     }
     __syncthreads();
     e = found[0];
-    from = fst[e] + found[1] * kPiece;
-    count = min(kPiece, fst[e + 1] - from);
+    from = fst[e] + found[1] * a.piece;
+    count = min(a.piece, fst[e + 1] - from);
   }
   if (tid < count) {
     const int64_t q = entries[grp * a.group * a.k + from + tid];
@@ -955,7 +960,7 @@ struct RowOrder {
 
 RowOrder order_in(const Experts& p, int64_t n, const void* layout) {
   if (layout == nullptr) return {};
-  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
+  const LayoutShape L = layout_shape(p, n);
   const char* const at = static_cast<const char*>(layout);
   return {reinterpret_cast<const int32_t*>(at + L.order), reinterpret_cast<const int32_t*>(at + L.listed)};
 }
@@ -1053,7 +1058,7 @@ struct BackwardSpace {
 
 BackwardSpace backward_space(const Experts& p, int64_t n) {
   const size_t size = p.f64 ? 8 : 4;
-  const LayoutShape L = layout_shape(n, p.n_experts, p.top_k);
+  const LayoutShape L = layout_shape(p, n);
   BackwardSpace w{};
   size_t shares = 0;  // as rows() counts them, with the fewest wavefronts a map's channels can get
   for (const ExpertMap& m : p.maps) shares += (m.mul_in + 15) / 16;
@@ -1094,7 +1099,7 @@ hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, c
                          int64_t(0), nullptr, nullptr, nullptr, n_gates, n_parts, gate_part, gg);
     return hipGetLastError();
   }
-  const LayoutShape L = layout_shape(n, X, p.top_k);
+  const LayoutShape L = layout_shape(p, n);
   const char* const at = static_cast<const char*>(layout);
   auto ints = [&](size_t off) { return n > 0 ? reinterpret_cast<const int32_t*>(at + off) : nullptr; };
   WgradArgs a{};
@@ -1107,7 +1112,8 @@ hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, c
   a.k = p.top_k;
   a.n_maps = n_maps;
   // with at most a piece's entries in all, an expert's one piece is its sum
-  a.direct = n * p.top_k <= kPiece;
+  a.piece = L.piece;
+  a.direct = n * p.top_k <= L.piece;
   a.slots = a.direct ? X : L.n_groups * L.max_pieces;
   const int per = 16 / static_cast<int>(sizeof(T));
   bool vec = aligned16(x) && aligned16(grad) && p.dim_in % per == 0 && p.dim_out % per == 0;
@@ -1157,21 +1163,21 @@ hipError_t backward(const Experts& p, int64_t n, const T* x, const T* weights, c
 
 }  // namespace
 
-size_t experts_layout_bytes(const Experts& p, int64_t n) { return layout_shape(n, p.n_experts, p.top_k).total; }
+size_t experts_layout_bytes(const Experts& p, int64_t n) { return layout_shape(p, n).total; }
 
 size_t experts_workspace(const Experts& p, int64_t n) { return backward_space(p, n).total; }
 
 hipError_t launch_experts_layout(const Experts& p, int64_t n, const int32_t* experts, void* layout, int32_t* load,
                                  hipStream_t s) {
   const int X = p.n_experts;
-  const LayoutShape L = layout_shape(n, X, p.top_k);
+  const LayoutShape L = layout_shape(p, n);
   char* const at = static_cast<char*>(layout);
   auto ints = [&](size_t off) { return reinterpret_cast<int32_t*>(at + off); };
   const int H = std::min(X, kMaxBins / X);
   const int threads = std::min(L.group, n) * p.top_k > 1024 ? 1024 : 256;
   hipLaunchKernelGGL(k_layout, dim3(static_cast<unsigned>(2 * L.n_groups)), dim3(threads), 0, s, n, X, p.top_k,
                      H,
-                     L.group, experts, ints(L.order), ints(L.listed), ints(L.entries), ints(L.first), ints(L.pieces));
+                     L.group, L.piece, experts, ints(L.order), ints(L.listed), ints(L.entries), ints(L.first), ints(L.pieces));
   if (load != nullptr) hipLaunchKernelGGL(k_load, dim3(1), dim3(256), 0, s, X, L.n_groups, ints(L.first), load);
   return hipGetLastError();
 }
