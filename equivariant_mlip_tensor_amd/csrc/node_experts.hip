@@ -625,7 +625,10 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
 #pragma unroll
         for (int s = 0; s < KS; ++s) prod = Mfma<T>::step(av[s], b[s], prod);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[c][q] += grow[16 * c + Mfma<T>::row(g4, q)] * prod[q];
+        for (int q = 0; q < 4; ++q) {  // a row that is not the expert's takes nothing, infinities and NaN included
+          const T g = grow[16 * c + Mfma<T>::row(g4, q)];
+          acc[c][q] = fma(g, g != T(0) ? prod[q] : T(0), acc[c][q]);
+        }
         if (GG) {
           T v[4];
 #pragma unroll

@@ -122,7 +122,9 @@ tpconv_status tpconv_route_backward(tpconv_dtype dtype, int64_t n_rows, const tp
  * maps in the order of irreps_in's segments.  An output segment without a
  * partner is zero, and so is a row without experts.  experts entries outside
  * [0, n_experts) are skipped (their gate is not read into any sum and their
- * gate gradient is 0); an expert that stands twice counts twice. */
+ * gate gradient is 0); an expert that stands twice counts twice.  Infinities
+ * and NaN in an expert's weights reach the rows that have it with a gate other
+ * than 0, and no others. */
 #define TPCONV_MAX_EXPERT_MUL 256
 
 typedef struct tpconv_experts_s* tpconv_experts_t;

@@ -344,6 +344,40 @@ def test_experts_nan_stays_in_its_row(node):
     assert torch.isfinite(gg).all(1).cpu().numpy().sum() == n - 2
 
 
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("irr", ["9x0e+8x1o", "32x0e+20x2e", "64x3o+40x4e"])
+def test_experts_infinities_of_other_experts_stay_out(node, dt, irr):
+    """Weights that are infinite, NaN or overflow reach the rows of their expert alone."""
+    import torch
+    rng = np.random.default_rng(11)
+    n, X, k = 100, 6, 2
+    experts, gates = routing_of(rng, n, X, k, 0.1)
+    gates[5] = 0.0
+    experts[5] = [2, 3]                                    # gates of 0: nothing of them either
+    plan = node.tpconv_experts_plan(irr, irr, X, k, dt)
+    x, G = (rng.standard_normal((n, plan.dim_in)).astype(NP[dt]) for _ in range(2))
+    w = rng.standard_normal((X, plan.weight_numel)).astype(NP[dt])
+    big = np.sqrt(np.finfo(NP[dt]).max)
+    x *= big / 64                                          # products with the third's weights overflow, others do not
+    G *= big / 64
+    bad = w.copy()
+    bad[2, ::3], bad[2, 1::3], bad[3] = np.nan, np.inf, bad[3] * big * 64
+    others = ~np.isin(experts, [2, 3]).any(1) | (gates == 0).all(1)
+    assert 20 < others.sum() < 80
+    x, e, g, G = dev(x), dev(experts), dev(gates.astype(NP[dt])), dev(G)
+    layout = node.tpconv_experts_layout(plan, e)
+    for lay in (layout, None):
+        for need in ((True, False, True), (True, False, False)):
+            clean, dirty = ((node.tpconv_experts_forward(plan, x, dev(v), e, g, lay),
+                             *node.tpconv_experts_backward(plan, x, dev(v), e, g, G, lay, need=need))
+                            for v in (w, bad))
+            assert torch.equal(clean[0][others], dirty[0][others]) and torch.equal(clean[1][others], dirty[1][others])
+            assert not torch.isfinite(dirty[0][~others]).any(1).all()
+            if need[2]:
+                rows = torch.from_numpy(~np.isin(experts, [2, 3])).cuda()
+                assert torch.equal(clean[3][rows], dirty[3][rows])
+
+
 def test_experts_gradient_against_differences(node):
     rng = np.random.default_rng(12)
     irr_in, irr_out, X, k, n = "5x0e+4x1o+2x2e", "3x0e+6x1o+2x2e", 4, 2, 50
