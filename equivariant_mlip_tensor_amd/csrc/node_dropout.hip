@@ -30,7 +30,8 @@ __device__ __forceinline__ Words philox(uint64_t block, uint64_t offset, uint64_
 }
 
 // One thread per element, its draw computed for it alone: for rows whose
-// column table does not fit LDS.
+// column table does not fit LDS (above 16384 columns; the generator then runs
+// four times a block of draws, or 2l+1 times that).
 template <class T>
 __global__ void k_dropout_wide(DropArgs a, const T* x, const T* residual, T* out) {
   const T scale = static_cast<T>(a.scale);
@@ -50,7 +51,9 @@ __global__ void k_dropout_wide(DropArgs a, const T* x, const T* residual, T* out
 // Memory bound: a block takes tiles of rows, draws the tile's channels (four
 // to a generator call) into LDS, a byte each, and streams the tile's pieces of
 // 16 bytes past them; a table in LDS says which channel a column belongs to.
-// The next kAhead pieces are loaded while the draws are made.
+// The next kAhead pieces are loaded while the draws are made.  28000 fp32 rows
+// of 1024 columns: 67 us with a residual (344 MB, 5.1 TB/s), 40 us without (229
+// MB, 5.7 TB/s), at the rate of a copy; 1024 rows of 288: 4 us (latency).
 constexpr int kThreads = 256, kAhead = 4;
 constexpr int kTableColumns = 16384, kTileBytes = 16384;
 
@@ -129,9 +132,11 @@ hipError_t dropout(const DropArgs& a, const T* x, const T* residual, T* out, hip
                        residual, out);
     return hipGetLastError();
   }
+  // 28000 rows of 1024 columns: 67 us by 16 bytes, 79 by single elements
   const bool vec = a.dim % kPer == 0 && aligned16(x) && aligned16(residual) && aligned16(out);
   const int pieces = static_cast<int>(a.dim) / (vec ? kPer : 1);
-  // a tile: as many rows as make 16 KiB of x, one at least; fewer where that leaves CUs without a tile
+  // a tile: as many rows as make 16 KiB of x, one at least; fewer where that leaves CUs without a tile (1024 rows of
+  // 288: 4.2 us, with whole tiles 4.5)
   int64_t tile = kTileBytes / (a.dim * int64_t(sizeof(T)));
   tile = tile < 1 ? 1 : tile;
   while (tile > 1 && (a.n_rows + tile - 1) / tile < 512) tile = (tile + 1) / 2;
