@@ -473,7 +473,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   int* const rowid = reinterpret_cast<int*>(lds + a.lds.rows);
   T* const graw = reinterpret_cast<T*>(lds + a.lds.graw);
   int* const ents = reinterpret_cast<int*>(lds + a.lds.ents);
-  T* const grow = reinterpret_cast<T*>(lds + a.lds.grow) + w * 16 * 9;  // a wavefront's gates of an expert's matrix rows
+  T* const grow = reinterpret_cast<T*>(lds + a.lds.grow) + w * 16 * 9;  // a wavefront's: gates of an expert's rows
   T* const esum = reinterpret_cast<T*>(lds + a.lds.esum);  // GG: entries' sums; each wavefront's; a wavefront's rows
   T* const wsum = reinterpret_cast<T*>(lds + a.lds.wsum);
   T* const rsum = reinterpret_cast<T*>(lds + a.lds.rsum) + w * 16 * 9;
