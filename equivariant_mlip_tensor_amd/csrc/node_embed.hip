@@ -50,8 +50,8 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a, int lg, const T* __r
 }
 
 // ------------------------------------------------------------------- backward
-// Each block sorts its rows' types (a bitonic sort in LDS of type * rows +
-// row, so that rows of a type stay in order) and sums its runs of equal types.
+// Each block sorts its rows by type (rows of a type stay in order) and sums its
+// runs of equal types.
 // The sorted rows are cut into equal slices, one for each group of lanes that
 // holds a row; a group sums its slice run by run.  A run that lies in one
 // slice is written by its group; the parts of one that crosses slices go
@@ -60,11 +60,12 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a, int lg, const T* __r
 // list in `runs`; the second kernel adds each type's sums over the blocks, in
 // order.  (A walk over all atoms by each type's own threads reads the types as
 // often as there are types: 41 ms at 250001 rows.)  250001 fp32 rows of 128, 97
-// types: 48 us, 2.7 TB/s, the sort of a block not being covered by the loads of
-// another at two blocks a CU; 28000 rows of 64, 5 types: 12.3 us, of which the
-// sort and its barriers are most; 16 fp64 rows in one block: 5.8 us.
+// types: 38 us, 3.4 TB/s: each block's sort, then its reads, in turn (blocks of
+// half the length: 37 us and 3.4 more for the join); 28000 rows of 64, 5 types:
+// 9.2 us (latency); 16 fp64 rows in one block: 5.8 us.
 constexpr int kRows = 1024;  // rows of a block, at most
 constexpr int kThreads = 512;
+constexpr int kCounters = 4096;  // of the sort by counting: 16 KiB of LDS, four blocks still share a CU's
 
 struct EmbedSpace {
   int64_t rows, blocks;  // rows of a block
@@ -74,7 +75,7 @@ struct EmbedSpace {
 EmbedSpace embed_space(int64_t n, int64_t n_types, int64_t dim, size_t size) {
   EmbedSpace s{};
   // Blocks for the 256 CUs first, then long blocks: the longer, the fewer sums are left to add.  28000 rows:
-  // sums and join 17.6 us, with 1024 rows a block 26; 250001 rows: 56, with 64 rows a block 106.
+  // sums and join 14.6 us, with 64 rows a block 17.7; 250001 rows: 45, with 512 rows a block 48.
   s.rows = 64;
   while (s.rows < kRows && s.rows * 256 < n) s.rows *= 2;
   s.blocks = (n + s.rows - 1) / s.rows;
@@ -83,6 +84,64 @@ EmbedSpace embed_space(int64_t n, int64_t n_types, int64_t dim, size_t size) {
   s.part = o;
   s.total = std::max<size_t>(256, o + align_up(size * s.blocks * most * dim));
   return s;
+}
+
+// The block's rows by type, rows of a type in their order: put(place, type,
+// row).  Each wavefront counts the types of its own run of rows, lanes of a type
+// found by a ballot for each of its bits, in counters [type][wavefront]; their
+// running sums are the places.
+template <class Put>
+__device__ __forceinline__ void sort_by_counting(const EmbedArgs& a, int64_t r0, int rows, int waves, int* count,
+                                                 int* sums, Put put) {
+  constexpr int kRounds = kRows / kThreads;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int none = static_cast<int>(a.n_types), n = (none + 1) * waves, bits = 32 - __clz(none);
+  const int rounds = (rows + kThreads - 1) / kThreads;
+  for (int q = tid; q < n; q += kThreads) count[q] = 0;
+  int type[kRounds], place[kRounds];
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    const int q = (w * rounds + j) * 64 + lane;
+    const int t = a.types[r0 + min(q, rows - 1)];
+    type[j] = j < rounds && q < rows ? (t >= 0 && t < none ? t : none) : -1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    uint64_t peers = __ballot(type[j] >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t on = __ballot((type[j] >> b) & 1);
+      peers &= (type[j] >> b) & 1 ? on : ~on;
+    }
+    const int rank = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    int base = 0;
+    if (type[j] >= 0 && rank == 0) base = atomicAdd(&count[type[j] * waves + w], __popcll(peers));
+    place[j] = __shfl(base, type[j] >= 0 ? __ffsll(static_cast<unsigned long long>(peers)) - 1 : 0, 64) + rank;
+  }
+  __syncthreads();
+  const int per = (n + kThreads - 1) / kThreads, q0 = min(n, tid * per), q1 = min(n, q0 + per);
+  int mine = 0;
+  for (int q = q0; q < q1; ++q) mine += count[q];
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int t = __shfl_up(before, o, 64);
+    if (lane >= o) before += t;
+  }
+  if (lane == 63) sums[w] = before;
+  __syncthreads();
+  before -= mine;
+  for (int q = 0; q < w; ++q) before += sums[q];
+  for (int q = q0; q < q1; ++q) {
+    const int c = count[q];
+    count[q] = before;
+    before += c;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j)
+    if (type[j] >= 0) put(count[type[j] * waves + w] + place[j], type[j], (w * rounds + j) * 64 + lane);
+  __syncthreads();
 }
 
 // A group's columns: kCols pieces a lane at a time, 16 bytes or one element.
@@ -95,31 +154,39 @@ __global__ __launch_bounds__(kThreads) void k_embed_runs(EmbedArgs a, int lg, in
   __shared__ uint64_t key[kRows];
   __shared__ int run_of[kRows];  // sorted row -> its run
   __shared__ int sums[kThreads / 64];
+  __shared__ int count[kCounters];
   extern __shared__ char lds[];
   T* const head = reinterpret_cast<T*>(lds);  // a group's part of the run its slice starts in
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t r0 = int64_t(blockIdx.x) * block_rows;
   const int rows = static_cast<int>(min<int64_t>(block_rows, a.n_rows - r0));
-  int size = 2;
-  while (size < rows) size *= 2;
-  for (int q = tid; q < size; q += kThreads) {
-    const int64_t t = q < rows ? a.types[r0 + q] : -1;
-    // types outside the table after all others
-    key[q] = (t >= 0 && t < a.n_types ? uint64_t(t) : uint64_t(1) << 40) << 10 | uint64_t(q);
-  }
-  __syncthreads();
-  for (int k = 2; k <= size; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int q = tid; q < size / 2; q += kThreads) {
-        const int lo = 2 * q - (q & (j - 1)), hi = lo + j;
-        const uint64_t x = key[lo], y = key[hi];
-        if ((x > y) == ((lo & k) == 0)) {
-          key[lo] = y;
-          key[hi] = x;
+  // types outside the table come after all others
+  auto key_of = [&](int64_t t, int q) {
+    return (t >= 0 && t < a.n_types ? uint64_t(t) : uint64_t(1) << 40) << 10 | uint64_t(q);
+  };
+  // by counting where the counters fit (1024 rows: up to 511 types), else by a bitonic sort of the keys, which
+  // takes any types: 250001 rows of 128 and 97 types in 38 us, by the other 48; 28000 rows of 64 in 9.2 and 12.4
+  const int waves = (min(rows, kThreads) + 63) / 64;  // wavefronts with rows
+  if ((a.n_types + 1) * waves <= kCounters) {
+    sort_by_counting(a, r0, rows, waves, count, sums, [&](int at, int t, int q) { key[at] = key_of(t, q); });
+  } else {
+    int size = 2;
+    while (size < rows) size *= 2;
+    for (int q = tid; q < size; q += kThreads) key[q] = key_of(q < rows ? a.types[r0 + q] : -1, q);
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        for (int q = tid; q < size / 2; q += kThreads) {
+          const int lo = 2 * q - (q & (j - 1)), hi = lo + j;
+          const uint64_t x = key[lo], y = key[hi];
+          if ((x > y) == ((lo & k) == 0)) {
+            key[lo] = y;
+            key[hi] = x;
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
-    }
+  }
   // number the runs: 4 sorted rows a thread
   constexpr int kEach = kRows / kThreads;
   int starts[kEach], mine = 0;
@@ -328,7 +395,7 @@ hipError_t backward(const EmbedArgs& a, const T* grad, T* grad_table, void* ws, 
   // one block and a small table: no sums left to add (16 fp64 rows: 5.8 us, by way of the workspace 6.0 + 3.2)
   T* const table = space.blocks == 1 && a.n_types * a.dim <= 16384 ? grad_table : nullptr;
   if (a.n_rows > 0) {
-    // 16 bytes a lane: 250001 rows of 128 in 48 us, one element a lane 58
+    // 16 bytes a lane where all rows allow it, for the same reason as above
     const bool vec = aligned16(grad) && a.dim % kPer == 0 && a.stride % kPer == 0;
     const int lg = lanes_for(vec ? a.dim / kPer : a.dim, 9);
     const dim3 grid(static_cast<unsigned>(space.blocks));

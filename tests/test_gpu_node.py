@@ -96,6 +96,19 @@ def test_embedding_sorted_reversed_and_uniform_types(node):
         within(got, on.embedding_backward(t, grad, types), bound, "grad_table")
 
 
+@pytest.mark.parametrize("types", [1, 40, 511, 512, 700])
+def test_embedding_gradient_of_many_rows(node, types):
+    """The longest blocks, with as many types as are sorted by counting and more."""
+    rng = np.random.default_rng(types)
+    n, dim = 140001, 3
+    t = rng.integers(-1, types + 1, n).astype(np.int32)
+    grad = rng.standard_normal((n, dim)).astype(np.float32)
+    got = node.tpconv_embedding_backward(dev(t), dev(grad), types)
+    count = np.bincount(t[(t >= 0) & (t < types)], minlength=types)[:, None]
+    bound = (count + 6) * EPS["f32"] * on.embedding_backward(t, np.abs(grad), types)
+    within(got, on.embedding_backward(t, grad, types), bound, "grad_table")
+
+
 # -------------------------------------------------------------------- routing
 def config(node, **kw):
     return node.RouteConfig(**kw), dict(score=kw.get("score", "softmax"), renormalise=kw.get("renormalise", True),
