@@ -7,13 +7,13 @@
 // search and the gates then serve one row.)  The reductions over a row run on
 // the vector units (DPP); one round of the selection is a maximum over the
 // row's keys, as ordered whole numbers, and a minimum over the indices that
-// hold it: no sort, and ties are settled exactly.  The forward is bound by the
-// vector instructions of those rounds, the gradient by its reads of single
-// logits and gates, each of which waits for the expert's number: 131072 fp32
-// rows of 128 experts in 8 groups, 6 chosen, take 54 us and 21 us (1000
-// vector instructions for four rows: a fourth in the groups' search, a fourth
-// in the rounds; 67 MB of logits read, 67 MB of their gradient written: 13 us each at the rate of a
-// copy); 28000 rows of 16 experts take 4.5 us and 5.3 us.
+// hold it: no sort, and ties are settled exactly.  The forward is bound by its
+// vector instructions, the gradient by its reads of single logits and gates,
+// each of which waits for the expert's number: 131072 fp32 rows of 128 experts
+// in 8 groups, 6 chosen, take 54 us (1000 instructions for four rows, a fourth
+// of them in the groups' search and a fourth in the rounds) and 21 us; 67 MB of
+// logits read and 67 MB of their gradient written are 13 us each at the rate of
+// a copy.  28000 rows of 16 experts take 4.5 us and 5.3 us.
 #include <hip/hip_runtime.h>
 
 #include "node_internal.hpp"
