@@ -4,6 +4,7 @@
 
 #include <algorithm>
 
+#include "node_device.hpp"
 #include "node_internal.hpp"
 
 namespace tpconv {
@@ -117,6 +118,7 @@ __device__ __forceinline__ void sort_by_counting(const EmbedArgs& a, int64_t r0,
     int base = 0;
     if (type[j] >= 0 && rank == 0) base = atomicAdd(&count[type[j] * waves + w], __popcll(peers));
     place[j] = __shfl(base, type[j] >= 0 ? __ffsll(static_cast<unsigned long long>(peers)) - 1 : 0, 64) + rank;
+    wave_sync();  // the next round's rows take the places after these
   }
   __syncthreads();
   const int per = (n + kThreads - 1) / kThreads, q0 = min(n, tid * per), q1 = min(n, q0 + per);

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 
+#include "node_device.hpp"
 #include "node_internal.hpp"
 
 namespace tpconv {
@@ -258,6 +259,7 @@ __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H,
       base = __shfl(base, __ffsll(static_cast<unsigned long long>(peers)) - 1, 64);
       entries[r0 * k + base + rank] = static_cast<int32_t>(r0 * k + q + lane);
     }
+    wave_sync();  // the next pass's entries take the places after these
   }
 }
 
@@ -620,9 +622,11 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
       for (int s = 0; s < KS; ++s) b[s] = full || s / 4 * 16 + 4 * g4 + s % 4 < k_here ? next[s] : T(0);
       e = __builtin_amdgcn_readfirstlane(list[4 * j + 4]);
       if (e >= 0) load_weights(e, next);
+      wave_sync();  // the last expert's gates and sums are read
 #pragma unroll
       for (int r = 0; r < 16 * D; r += 64)
         if (r + lane < 16 * D) grow[r + lane] = gtab[j * kTile + (r + lane) / D];
+      wave_sync();
 #pragma unroll
       for (int c = 0; c < D; ++c) {
         constexpr auto bits = [](int chunk) {  // rows of the tile in the chunk
@@ -650,6 +654,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
           if (i16 < 4) rsum[16 * c + Mfma<T>::row(g4, i16)] = s;
         }
       }
+      if (GG) wave_sync();
       if (GG && lane < kTile && ((members >> lane) & 1)) {  // the expert's rows, each over its components
         T v = 0;
 #pragma unroll

@@ -16,6 +16,7 @@
 // a copy.  28000 rows of 16 experts take 4.5 us and 5.3 us.
 #include <hip/hip_runtime.h>
 
+#include "node_device.hpp"
 #include "node_internal.hpp"
 
 namespace tpconv {
@@ -110,14 +111,6 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 __device__ __forceinline__ uint64_t ordered(double s) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
   return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
-}
-
-// Makes a wavefront's LDS writes visible to its own reads (a row never leaves
-// its wavefront).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // maximum and sum of exponentials of a row's softmax (masked entries add
