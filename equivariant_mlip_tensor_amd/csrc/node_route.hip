@@ -222,7 +222,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
           k2 = fmax(k2, fmin(k1, k));
           k1 = fmax(k1, k);
         }
-        group[g] = k2 > -inf<T>() ? k1 + k2 : k1;
+        // NaN (here the lowest value) and the two keys' sum stay numbers: the group is not one that is all masked
+        const T least = lowest(T(0)) / 2;
+        group[g] = k1 == -inf<T>() ? k1 : fmax(k1, least) + (k2 == -inf<T>() ? T(0) : fmax(k2, least));
       }
       wave_sync();
       for (int g = sub; g < a.groups; g += P) {

@@ -76,7 +76,9 @@ tpconv_status tpconv_embedding_backward(tpconv_dtype dtype, int64_t n_rows, int6
  * over the chosen), formed from the logits so that scores which all underflow
  * still give gates that sum to scale.  The bias moves the selection only.
  * A NaN logit (with softmax also +inf) orders below every number but before
- * the masked ones and makes the gates it enters NaN. */
+ * the masked ones and makes the gates it enters NaN; NaN keys go by their
+ * index.  In a group's key, NaN and a key below half the type's lowest value
+ * count as that half, so a group is dropped for its rank alone. */
 #define TPCONV_MAX_EXPERTS 256
 #define TPCONV_MAX_TOP_K 8
 

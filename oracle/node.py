@@ -62,27 +62,32 @@ def scores(z, kind):
 
 
 def keys(z, bias, kind):
+    """Selection keys: scores plus bias, -inf for a masked expert, NaN where the score is."""
     s = scores(z, kind)
     return np.where(np.isneginf(z), -np.inf, s + (0.0 if bias is None else np.asarray(bias, np.float64)))
 
 
-def group_keys(key, n_groups):
+def group_keys(key, n_groups, low=np.finfo(np.float64).min / 2):
+    """The sum of a group's two largest unmasked keys; `low` for NaN and for what is below it."""
     out = []
     for g in np.split(key, n_groups):
-        best = np.sort(g[~np.isneginf(g)])[::-1][:2]
+        live = g[~np.isneginf(g)]
+        best = np.sort(np.where(live >= low, live, low))[::-1][:2]
         out.append(best.sum() if len(best) else -np.inf)
     return np.array(out)
 
 
-def choose(z, bias, cfg):
-    """Chosen experts of one row, in order (fewer than top_k when the rest is masked)."""
+def choose(z, bias, cfg, low=np.finfo(np.float64).min / 2):
+    """Chosen experts of one row, in order (fewer than top_k when the rest is masked): by descending key, then by
+    index; NaN keys after all others."""
     key = keys(z, bias, cfg["score"])
     if cfg["n_groups"] > 1:
-        order = np.argsort(-group_keys(key, cfg["n_groups"]), kind="stable")[:cfg["top_groups"]]
+        order = np.argsort(-group_keys(key, cfg["n_groups"], low), kind="stable")[:cfg["top_groups"]]
         inside = np.repeat(np.isin(np.arange(cfg["n_groups"]), order), len(z) // cfg["n_groups"])
         key = np.where(inside, key, -np.inf)
-    order = np.argsort(-key, kind="stable")[:cfg["top_k"]]
-    return [int(e) for e in order if not np.isneginf(key[e])]
+    live = [e for e in range(len(z)) if not np.isneginf(key[e])]
+    live.sort(key=lambda e: (1, 0.0, e) if np.isnan(key[e]) else (0, -key[e], e))
+    return live[:cfg["top_k"]]
 
 
 def log_scores(z, kind):
@@ -94,6 +99,8 @@ def gates_of(z, picked, cfg):
     if not picked:
         return np.zeros(0)
     if cfg["renormalise"]:
+        if cfg["score"] == "softmax" and np.isnan(scores(z, "softmax")).any():
+            return np.full(len(picked), np.nan)                # NaN or +inf among the logits
         l = log_scores(z[picked], cfg["score"])
         w = np.exp(l - l.max())
         return cfg["scale"] * w / w.sum()
@@ -102,10 +109,11 @@ def gates_of(z, picked, cfg):
 
 def route_forward(logits, bias, cfg):
     z = np.asarray(logits, np.float64)
+    low = float(np.finfo(np.asarray(logits).dtype).min) / 2
     experts = np.full((len(z), cfg["top_k"]), -1, np.int32)
     gates = np.zeros((len(z), cfg["top_k"]))
     for i in range(len(z)):
-        picked = choose(z[i], bias, cfg)
+        picked = choose(z[i], bias, cfg, low)
         experts[i, :len(picked)] = picked
         gates[i, :len(picked)] = gates_of(z[i], picked, cfg)
     return experts, gates

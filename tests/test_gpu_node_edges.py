@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 
 from oracle import node as on
-from test_gpu_node import EPS, NP, check_experts, config, dev, node, within  # noqa: F401  (node is a fixture)
+from test_gpu_node import EPS, NP, check_experts, config, dev, node, separated, within  # noqa: F401  (node is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,54 @@ def test_experts_many_experts_in_a_tile(node, dt, irr):  # noqa: F811
     for _ in range(3):
         again = check_experts(node, dt, irr, irr, X, experts, gates)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+# -------------------------------------------------------------------- routing
+def same(got, want, tol, what):
+    """Within tol of |want|; NaN exactly where the definition has NaN."""
+    got = got.cpu().numpy().astype(np.float64)
+    nan = np.isnan(want)
+    assert np.array_equal(np.isnan(got), nan), (what, got, want)
+    assert (np.abs(got - want)[~nan] <= (tol * np.abs(want))[~nan]).all(), (what, got, want)
+
+
+# twice the logits' size and 32 units for exp and log1p, X for the sums (as in test_gpu_node.py); logits below 8
+def gate_tol(X, dt):
+    return (X + 2 * 8 + 32) * EPS[dt]
+
+
+def put_not_numbers(rng, z, per):
+    """NaN, +inf and -inf in all constellations of a row and of a group of `per`."""
+    X, nan, inf = z.shape[1], np.nan, np.inf
+    z[0, X // 2] = nan                                          # one NaN
+    z[1] = nan                                                  # all of a row
+    z[2, :per] = nan                                            # all of a group
+    z[3, 0] = inf
+    z[4] = -inf                                                 # a padding row
+    z[5, :-1], z[5, -1] = -inf, nan                             # NaN is all that is not masked
+    z[6, ::2], z[6, 1::2] = nan, -inf
+    z[7, rng.random(X) < 0.5] = nan
+    z[8, :per], z[8, per - 1] = -inf, nan                       # a group with one NaN alone
+    z[9, rng.random(X) < 0.3], z[9, 0] = -inf, nan
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("X,G,T,k", [(8, 1, 1, 3), (12, 4, 2, 3), (24, 6, 3, 5), (64, 8, 2, 4), (100, 50, 9, 8),
+                                     (256, 64, 5, 8), (7, 7, 3, 3)])
+def test_routing_of_not_numbers(node, dt, score, renorm, X, G, T, k):  # noqa: F811
+    """NaN keys come after every number and before the masked experts, in groups as without, and their gates are
+    NaN: a row of a router that has diverged is never taken for a padding row."""
+    log(f"[node] routing of NaN {dt} {score} renorm={renorm} X={X} groups={G}/{T} k={k}")
+    rng = np.random.default_rng([X, G])
+    cfg, ocfg = config(node, n_experts=X, top_k=k, score=score, renormalise=renorm, n_groups=G, top_groups=T)
+    for bias in (None, (0.1 * rng.standard_normal(X)).astype(NP[dt])):
+        z = separated(rng, 40, X, bias, ocfg, dt, 0.05)
+        put_not_numbers(rng, z, X // G)
+        experts, gates = node.tpconv_route_forward(cfg, dev(z), None if bias is None else dev(bias))
+        want_e, want_g = on.route_forward(z, bias, ocfg)
+        assert np.array_equal(experts.cpu().numpy(), want_e)
+        same(gates, want_g, gate_tol(X, dt), "gates")
+        assert (want_e[1] >= 0).all() and np.isnan(want_g[1]).all()
+        assert (want_e[5, 0], want_e[4, 0]) == (X - 1, -1)

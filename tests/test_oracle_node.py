@@ -124,6 +124,23 @@ def test_route_selection_brute_force_ties_and_masks():
     assert on.choose(np.full(9, -np.inf), None, cfg) == []
 
 
+def test_route_nan_comes_after_numbers_and_before_masks():
+    nan, inf = np.nan, np.inf
+    cfg = dict(score="sigmoid", renormalise=True, n_groups=3, top_groups=2, top_k=4, scale=1.0)
+    z = np.array([[nan, nan, 1.0, 2.0, nan, -inf],              # groups: NaN twice; two numbers; NaN alone
+                  [nan, nan, nan, nan, nan, nan],
+                  [-inf, -inf, nan, -inf, -inf, -inf],
+                  [3.0, nan, -inf, -inf, 1.0, 2.0]])
+    experts, gates = on.route_forward(z, None, cfg)
+    assert experts.tolist() == [[3, 2, 4, -1], [0, 1, 2, 3], [2, -1, -1, -1], [0, 5, 4, 1]]
+    assert np.isnan(gates[:, 0]).all() and (gates[2, 1:] == 0).all()
+    # softmax: every score of such a row is NaN, and so are its gates, chosen from what is not masked
+    experts, gates = on.route_forward(z, None, dict(cfg, score="softmax"))
+    assert experts[3].tolist()[:2] == [0, 1] and np.isnan(gates[experts >= 0]).all()
+    assert on.route_forward(np.array([[inf, 0.0, 1.0, 2.0]]), None, dict(cfg, n_groups=1, score="softmax",
+                                                                         top_k=2))[0].tolist() == [[0, 1]]
+
+
 def test_renormalised_gates_sum_to_scale_where_scores_underflow():
     for kind in ("softmax", "sigmoid"):
         cfg = dict(score=kind, renormalise=True, n_groups=1, top_groups=1, top_k=2, scale=3.0)
