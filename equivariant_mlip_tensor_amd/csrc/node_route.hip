@@ -206,8 +206,9 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
         s = sum;  // a NaN row orders by index
       }
       const T low = lowest(T(0));
-      s = s >= low ? s : low;  // NaN (and -inf from the bias) last of the unmasked
-      score[v] = z[v] == -inf<T>() ? -inf<T>() : s;
+      s = s >= low ? s : low;  // NaN last of the unmasked
+      const bool masked = z[v] == -inf<T>() || (BY_SCORE && shift[BY_SCORE ? v : 0] == -inf<T>());
+      score[v] = masked ? -inf<T>() : s;
     }
     uint32_t out_of_group = 0;  // bit v: the group of expert v * P + sub is not chosen
     if (BY_SCORE && a.top_groups < a.groups) {

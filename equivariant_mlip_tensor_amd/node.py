@@ -188,7 +188,7 @@ class RouteConfig:
 def tpconv_route_forward(config: RouteConfig, logits, bias=None, experts=None, gates=None,
                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(experts int32 [n, top_k], gates [n, top_k]) for logits [n, n_experts]; bias [n_experts] moves the selection
-    only.  Masked experts have logit -inf; places without an expert get -1 and gate 0."""
+    only.  Masked experts have logit or bias -inf; places without an expert get -1 and gate 0."""
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     n, dt, dev = logits.shape[0], logits.dtype, logits.device

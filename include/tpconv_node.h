@@ -65,7 +65,8 @@ tpconv_status tpconv_embedding_backward(tpconv_dtype dtype, int64_t n_rows, int6
 
 /* ---------------------------------------------------------------- routing --
  * For each row: scores s = softmax(logits) or sigmoid(logits); selection keys
- * s + bias; experts with logit -inf are masked and never chosen.  With
+ * s + bias; experts with logit -inf or bias -inf are masked and never chosen
+ * (a bias leaves scores and gates as they are, -inf too).  With
  * n_groups > 1 the experts form n_groups equal runs: a group's key is the sum
  * of its two largest unmasked keys (of the one it has, if it has one), and
  * only the top_groups groups with the largest keys stay.  The top_k largest

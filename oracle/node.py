@@ -62,9 +62,10 @@ def scores(z, kind):
 
 
 def keys(z, bias, kind):
-    """Selection keys: scores plus bias, -inf for a masked expert, NaN where the score is."""
-    s = scores(z, kind)
-    return np.where(np.isneginf(z), -np.inf, s + (0.0 if bias is None else np.asarray(bias, np.float64)))
+    """Selection keys: scores plus bias, -inf for a masked expert (logit or bias -inf), NaN where the score is."""
+    s, b = scores(z, kind), np.zeros(len(z)) if bias is None else np.asarray(bias, np.float64)
+    masked = np.isneginf(z) | np.isneginf(b)
+    return np.where(masked, -np.inf, s + np.where(masked, 0.0, b))
 
 
 def group_keys(key, n_groups, low=np.finfo(np.float64).min / 2):

@@ -89,3 +89,30 @@ def test_routing_of_not_numbers(node, dt, score, renorm, X, G, T, k):  # noqa: F
         same(gates, want_g, gate_tol(X, dt), "gates")
         assert (want_e[1] >= 0).all() and np.isnan(want_g[1]).all()
         assert (want_e[5, 0], want_e[4, 0]) == (X - 1, -1)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("X,G,T,k", [(8, 1, 1, 3), (12, 4, 2, 3), (24, 6, 3, 5), (64, 8, 2, 4), (256, 64, 5, 8)])
+def test_routing_with_infinite_and_lowest_biases(node, dt, score, X, G, T, k):  # noqa: F811
+    """A bias of -inf masks its expert; the type's lowest value puts it last, and its group behind the others'."""
+    log(f"[node] routing biases {dt} {score} X={X} groups={G}/{T} k={k}")
+    rng = np.random.default_rng([X, G, 1])
+    cfg, ocfg = config(node, n_experts=X, top_k=k, score=score, n_groups=G, top_groups=T)
+    per, low = X // G, np.finfo(NP[dt]).min
+    masks = [np.zeros(X) for _ in range(6)]
+    masks[0][: X - 2] = -np.inf                                 # fewer than top_k left
+    masks[1][::2] = -np.inf
+    masks[2][:per] = -np.inf                                    # a whole group
+    masks[3][:] = -np.inf                                       # nothing left
+    masks[4][:per], masks[4][-1] = low, low                     # a group put last, and one expert of another
+    masks[5][0], masks[5][X // 2] = np.inf, -np.inf
+    for bias in masks:
+        bias = bias.astype(NP[dt])
+        z = separated(rng, 20, X, np.where(bias == low, -np.inf, bias), ocfg, dt, 0.2)
+        z[4] = np.nan
+        experts, gates = node.tpconv_route_forward(cfg, dev(z), dev(bias))
+        want_e, want_g = on.route_forward(z, bias, ocfg)
+        assert np.array_equal(experts.cpu().numpy(), want_e), bias
+        same(gates, want_g, gate_tol(X, dt), "gates")
+        assert not np.isneginf(bias[want_e[want_e >= 0]]).any()

@@ -141,6 +141,21 @@ def test_route_nan_comes_after_numbers_and_before_masks():
                                                                          top_k=2))[0].tolist() == [[0, 1]]
 
 
+def test_route_bias_of_minus_infinity_masks():
+    """As if the expert's logit were -inf, but for the softmax's sum."""
+    rng = np.random.default_rng(6)
+    for score, groups in itertools.product(("softmax", "sigmoid"), (1, 3)):
+        cfg = dict(score=score, renormalise=True, n_groups=groups, top_groups=min(2, groups), top_k=3, scale=1.0)
+        z = rng.standard_normal((20, 9))
+        bias = np.where(rng.random(9) < 0.4, -np.inf, 0.0)
+        z[0, 0] = np.nan
+        experts, gates = on.route_forward(z, bias, cfg)
+        e, g = on.route_forward(np.where(np.isneginf(bias), -np.inf, z)[1:], None, cfg)
+        assert (experts[1:] == e).all()
+        np.testing.assert_allclose(gates[1:], g, rtol=1e-14)
+        assert not np.isneginf(bias[experts[experts >= 0]]).any()
+
+
 def test_renormalised_gates_sum_to_scale_where_scores_underflow():
     for kind in ("softmax", "sigmoid"):
         cfg = dict(score=kind, renormalise=True, n_groups=1, top_groups=1, top_k=2, scale=3.0)
