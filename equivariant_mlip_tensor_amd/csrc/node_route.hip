@@ -16,6 +16,8 @@
 // a copy.  28000 rows of 16 experts take 4.5 us and 5.3 us.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "node_device.hpp"
 #include "node_internal.hpp"
 
@@ -103,7 +105,8 @@ __device__ __forceinline__ T of_lane(T v, int from) {
   return __shfl(v, (threadIdx.x & 63 & ~((1 << LG) - 1)) + from, 64);
 }
 
-// Scores as whole numbers in the same order; 0 is below every score.
+// Scores as whole numbers in the same order; 0 (none) and 1 (NaN) are below
+// every score.
 __device__ __forceinline__ uint32_t ordered(float s) {
   const uint32_t b = __float_as_uint(s + 0.0f);  // one zero
   return (b >> 31) != 0 ? ~b : b | 0x80000000u;
@@ -155,21 +158,28 @@ __device__ __forceinline__ T gate_of(const RouteArgs& a, T z, bool has, T top, T
 
 constexpr int kThreads = 256;
 
-// BY_SCORE: the keys are scores (there is a bias, or a group's two best are
-// summed); otherwise the logits themselves, which have the same order: 28000
-// rows of 16 in 4.6 us, by scores 5.4.
+// BY_SCORE: scores are formed (there is a bias to add, or a group's two best are
+// summed); 28000 rows of 16 take 4.6 us without, 5.4 with.  Without a bias the
+// keys are the logits, which have the scores' order and tell apart scores that
+// round to one number (0 or 1); with one, equal keys go by the logits, so that a
+// bias of zeros chooses the same.  fp32 rows of up to 128 are held to 96
+// registers, five wavefronts a SIMD: 131072 rows of 128 in groups in 56 us, with
+// two registers more and four wavefronts in 58.
 template <class T, int LG, int VPL, bool BY_SCORE>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __restrict__ logits,
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void k_route(
+    RouteArgs a, const T* __restrict__ logits,
                                                     const T* __restrict__ bias, int32_t* __restrict__ experts,
                                                     T* __restrict__ gates) {
   constexpr int P = 1 << LG, kRows = kThreads / P, X_MAX = P * VPL;
   using Key = decltype(ordered(T(0)));
+  constexpr Key kNaN = 1;
   __shared__ T rows[kRows][X_MAX + 4];  // a row's scores, then its logits; rows start 4 banks apart
   __shared__ T groups[BY_SCORE ? kRows : 1][BY_SCORE ? 136 : 1];  // a row's groups' scores, then 1 for the chosen; 8 banks apart
   const int sub = threadIdx.x & (P - 1), in_block = threadIdx.x >> LG;
   T* const row = rows[in_block];
   T* const group = groups[BY_SCORE ? in_block : 0];
   const int per = a.X / a.groups;
+  const bool by_bias = BY_SCORE && bias != nullptr;
   const int64_t step = int64_t(gridDim.x) * kRows;
   T ahead[VPL];  // the next row's logits
   auto load = [&](int64_t i0) {
@@ -205,8 +215,6 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
       } else if (!a.sigmoid && sum != sum) {
         s = sum;  // a NaN row orders by index
       }
-      const T low = lowest(T(0));
-      s = s >= low ? s : low;  // NaN last of the unmasked
       const bool masked = z[v] == -inf<T>() || (BY_SCORE && shift[BY_SCORE ? v : 0] == -inf<T>());
       score[v] = masked ? -inf<T>() : s;
     }
@@ -214,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
     if (BY_SCORE && a.top_groups < a.groups) {
       wave_sync();
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) row[v * P + sub] = score[v];
+      for (int v = 0; v < VPL; ++v) row[v * P + sub] = score[v] == score[v] ? score[v] : lowest(T(0));
       wave_sync();
       for (int g = sub; g < a.groups; g += P) {
         T k1 = -inf<T>(), k2 = -inf<T>();
@@ -244,29 +252,67 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a, const T* __rest
     }
     Key key[VPL];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-      key[v] = score[v] == -inf<T>() || ((out_of_group >> v) & 1) ? Key(0) : ordered(score[v]);
-    // the next in the order (key descending, index ascending), top_k times
+    for (int v = 0; v < VPL; ++v) {
+      const Key number = ordered(by_bias ? score[v] : z[v]), live = score[v] == score[v] ? number : kNaN;
+      const bool out = score[v] == -inf<T>() || ((out_of_group >> v) & 1) != 0;
+      key[v] = out ? Key(0) : live;
+    }
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) row[v * P + sub] = z[v];  // out of the registers during the rounds
+    wave_sync();
+    // the next in the order (key descending, then index ascending or, with LOGITS, logit descending and index
+    // ascending), top_k times; lane j keeps the j-th and its key
     int pick = -1;
-    for (int j = 0; j < a.k; ++j) {
+    Key picked = 0;
+    auto largest = [&] {
       Key most = key[0];
 #pragma unroll
       for (int v = 1; v < VPL; ++v) most = key[v] > most ? key[v] : most;
-      const Key m = reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
-      uint32_t at = X_MAX;
+      return reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
+    };
+    auto choose = [&](auto LOGITS) {
+      for (int j = 0; j < a.k; ++j) {
+        const Key m = largest();
+        T best = -inf<T>();
+        if constexpr (LOGITS) {
 #pragma unroll
-      for (int v = VPL - 1; v >= 0; --v) at = key[v] == m ? v * P + sub : at;
-      const int e = static_cast<int>(reduce<LG>(at, [](uint32_t x, uint32_t y) { return x < y ? x : y; }));
+          for (int v = 0; v < VPL; ++v) {
+            const T l = row[v * P + sub];
+            best = key[v] == m && l > best ? l : best;
+          }
+          best = reduce<LG>(best, Max{});
+        }
+        uint32_t at = X_MAX;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        if (e == v * P + sub) key[v] = 0;
-      if (sub == j) pick = m != 0 ? e : -1;
+        for (int v = VPL - 1; v >= 0; --v)
+          at = key[v] == m && (!LOGITS || m <= kNaN || row[v * P + sub] == best) ? v * P + sub : at;
+        const int e = static_cast<int>(reduce<LG>(at, [](uint32_t x, uint32_t y) { return x < y ? x : y; }));
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+          if (e == v * P + sub) key[v] = 0;
+        pick = sub == j ? (m != 0 ? e : -1) : pick;
+        picked = sub == j ? m : picked;
+      }
+    };
+    choose(std::false_type{});
+    if (by_bias) {
+      // equal keys, rare, stand side by side, the last chosen's perhaps among those left: then the rounds are made
+      // again with the logits (131072 rows of 128 in groups: 56 us; with a check in each round 60)
+      const Key before = of_lane<LG>(picked, max(sub - 1, 0)), left = largest();
+      const bool equal = (sub > 0 && sub < a.k && picked == before) || (sub == a.k - 1 && picked == left);
+      if (__any(equal && picked > kNaN)) {
+        for (int j = 0; j < a.k; ++j) {
+          const int e = of_lane<LG>(pick, j);
+          const Key m = of_lane<LG>(picked, j);
+#pragma unroll
+          for (int v = 0; v < VPL; ++v)
+            if (e == v * P + sub) key[v] = m;
+        }
+        choose(std::true_type{});
+      }
     }
     const bool has = sub < a.k && pick >= 0;
-    wave_sync();
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) row[v * P + sub] = z[v];
-    wave_sync();
     T w = gate_of<T, LG>(a, has ? row[pick] : T(0), has, top, sum);
     if (!a.sigmoid && has && sum != sum) w = sum;  // NaN in, NaN out
     if (live && sub < a.k) {

@@ -70,8 +70,9 @@ tpconv_status tpconv_embedding_backward(tpconv_dtype dtype, int64_t n_rows, int6
  * n_groups > 1 the experts form n_groups equal runs: a group's key is the sum
  * of its two largest unmasked keys (of the one it has, if it has one), and
  * only the top_groups groups with the largest keys stay.  The top_k largest
- * keys are chosen, in descending order.  Ties go to the lowest index, of
- * groups and of experts.  A row with fewer than top_k experts left (all masked:
+ * keys are chosen, in descending order.  Experts whose keys are equal in the
+ * data type (scores that round to 0 or 1) go by their logits, the larger first;
+ * what ties in these too, and groups that tie, go to the lowest index.  A row with fewer than top_k experts left (all masked:
  * a padding atom) gets index -1 and gate 0 in its last places.
  * Gates: scale * s of the chosen, or, with renormalise, scale * s / (sum of s
  * over the chosen), formed from the logits so that scores which all underflow

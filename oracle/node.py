@@ -79,15 +79,15 @@ def group_keys(key, n_groups, low=np.finfo(np.float64).min / 2):
 
 
 def choose(z, bias, cfg, low=np.finfo(np.float64).min / 2):
-    """Chosen experts of one row, in order (fewer than top_k when the rest is masked): by descending key, then by
-    index; NaN keys after all others."""
+    """Chosen experts of one row, in order (fewer than top_k when the rest is masked): by descending key, equal keys
+    by descending logit, then by index; NaN keys after all others, by index."""
     key = keys(z, bias, cfg["score"])
     if cfg["n_groups"] > 1:
         order = np.argsort(-group_keys(key, cfg["n_groups"], low), kind="stable")[:cfg["top_groups"]]
         inside = np.repeat(np.isin(np.arange(cfg["n_groups"]), order), len(z) // cfg["n_groups"])
         key = np.where(inside, key, -np.inf)
     live = [e for e in range(len(z)) if not np.isneginf(key[e])]
-    live.sort(key=lambda e: (1, 0.0, e) if np.isnan(key[e]) else (0, -key[e], e))
+    live.sort(key=lambda e: (1, 0.0, 0.0, e) if np.isnan(key[e]) else (0, -key[e], -z[e], e))
     return live[:cfg["top_k"]]
 
 

@@ -116,3 +116,43 @@ def test_routing_with_infinite_and_lowest_biases(node, dt, score, X, G, T, k):  
         assert np.array_equal(experts.cpu().numpy(), want_e), bias
         same(gates, want_g, gate_tol(X, dt), "gates")
         assert not np.isneginf(bias[want_e[want_e >= 0]]).any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("X,k", [(6, 2), (8, 4), (16, 3), (50, 8), (256, 8)])
+def test_routing_of_saturated_scores_goes_by_the_logits(node, dt, score, X, k):  # noqa: F811
+    """Scores that round to 1 or to 0 are told apart by their logits, with a bias of zeros as without one."""
+    rng = np.random.default_rng([X, k])
+    cfg, ocfg = config(node, n_experts=X, top_k=k, score=score, scale=3.0)
+    z = np.zeros((40, X))
+    z[0] = -5000.0
+    z[0, X // 2] += 1.0                                         # all underflow as sigmoids
+    z[1] = 60.0 + rng.permutation(X)                            # all 1 as sigmoids
+    z[2] = -3000.0 - rng.permutation(X)
+    z[3] = np.where(rng.random(X) < 0.5, 1.0, -1.0) * (1000.0 + rng.permutation(X))
+    z[4] = np.where(np.arange(X) < X // 2, 70.0, 71.0)          # ties of logits as well: the lowest index
+    z[5] = np.finfo(NP[dt]).min
+    z[6], z[6, 1:] = np.finfo(NP[dt]).min, -4000.0 - rng.permutation(X - 1)
+    z[7:] = 2000.0 * rng.integers(-2, 3, (33, X)) + rng.integers(0, 5, (33, X))
+    z[8:, 0] = -np.inf
+    z = z.astype(NP[dt])
+    zero = np.zeros(X, NP[dt])
+    want_e, want_g = on.route_forward(z, None, ocfg)
+    for bias in (None, zero, -zero):
+        experts, gates = node.tpconv_route_forward(cfg, dev(z), None if bias is None else dev(bias))
+        assert np.array_equal(experts.cpu().numpy(), want_e)
+        # gates are formed from differences of logits up to 8000, exact here, and their exponentials
+        within(gates, want_g, (X + 64) * EPS[dt] * np.abs(want_g) + 1e-30, "gates")
+
+
+def test_routing_in_groups_goes_by_the_logits_too(node):  # noqa: F811
+    """Inside the chosen groups; groups whose keys tie go by their index."""
+    cfg, ocfg = config(node, n_experts=12, top_k=4, score="sigmoid", n_groups=3, top_groups=2)
+    z = np.array([[50, 51, 52, 53, -50, -51, -52, -53, 60, 61, 62, 63],
+                  [-200, -201, -202, -203, 300, 301, 302, 303, 0, 0, 1, 1]], np.float32)
+    zero = np.zeros(12, np.float32)
+    for bias in (None, zero):
+        experts, _ = node.tpconv_route_forward(cfg, dev(z), None if bias is None else dev(bias))
+        assert np.array_equal(experts.cpu().numpy(), on.route_forward(z, bias, ocfg)[0])
+        assert experts.cpu().numpy().tolist() == [[11, 10, 9, 8], [7, 6, 5, 4]]

@@ -156,6 +156,16 @@ def test_route_bias_of_minus_infinity_masks():
         assert not np.isneginf(bias[experts[experts >= 0]]).any()
 
 
+def test_route_of_saturated_scores_goes_by_the_logits():
+    """In the order of the exact scores, which the logits have: in 64 bits sigmoids above 40 are 1."""
+    rng = np.random.default_rng(7)
+    cfg = dict(score="sigmoid", renormalise=True, n_groups=1, top_groups=1, top_k=4, scale=1.0)
+    z = np.where(rng.random((30, 10)) < 0.5, 900.0, -900.0) + rng.integers(0, 6, (30, 10))
+    for bias in (None, np.zeros(10)):
+        experts, _ = on.route_forward(z, bias, cfg)
+        assert (experts == np.argsort(-z, axis=1, kind="stable")[:, :4]).all()
+
+
 def test_renormalised_gates_sum_to_scale_where_scores_underflow():
     for kind in ("softmax", "sigmoid"):
         cfg = dict(score=kind, renormalise=True, n_groups=1, top_groups=1, top_k=2, scale=3.0)
