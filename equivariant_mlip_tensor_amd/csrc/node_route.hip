@@ -137,18 +137,19 @@ template <class T, int LG>
 __device__ __forceinline__ T gate_of(const RouteArgs& a, T z, bool has, T top, T sum) {
   constexpr int L = LG < 3 ? LG : 3;
   if (a.renorm) {
-    T e;
-    // sigmoids far from underflow are divided as they are, others through their logarithms
+    T e = 0;
+    // sigmoids far from underflow are divided as they are, others through their logarithms: by rows, so that a row's
+    // gates do not depend on the others of its wavefront
     bool plain = false;
     if (a.sigmoid) {
       e = has ? sigmoid(z) : T(0);
-      plain = __all(!has || e > T(1e-30));
+      plain = reduce<L>(uint32_t(has && !(e > T(1e-30))), Max{}) == 0;
     }
-    if (!plain) {
+    if (__any(!plain)) {
       const T l = a.sigmoid ? log_sigmoid(z) : z;
       const bool number = has && l == l;
       const T m = reduce<L>(number ? l : -inf<T>(), Max{});
-      e = has ? exp(l - m) : T(0);
+      e = plain ? e : (has ? exp(l - m) : T(0));
     }
     const T total = reduce<L>(e, Sum{});
     return has ? e / total : T(0);
@@ -167,9 +168,8 @@ constexpr int kThreads = 256;
 // two registers more and four wavefronts in 58.
 template <class T, int LG, int VPL, bool BY_SCORE>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void k_route(
-    RouteArgs a, const T* __restrict__ logits,
-                                                    const T* __restrict__ bias, int32_t* __restrict__ experts,
-                                                    T* __restrict__ gates) {
+    RouteArgs a, const T* __restrict__ logits, const T* __restrict__ bias, int32_t* __restrict__ experts,
+    T* __restrict__ gates) {
   constexpr int P = 1 << LG, kRows = kThreads / P, X_MAX = P * VPL;
   using Key = decltype(ordered(T(0)));
   constexpr Key kNaN = 1;

@@ -156,3 +156,24 @@ def test_routing_in_groups_goes_by_the_logits_too(node):  # noqa: F811
         experts, _ = node.tpconv_route_forward(cfg, dev(z), None if bias is None else dev(bias))
         assert np.array_equal(experts.cpu().numpy(), on.route_forward(z, bias, ocfg)[0])
         assert experts.cpu().numpy().tolist() == [[11, 10, 9, 8], [7, 6, 5, 4]]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_routing_of_a_row_does_not_depend_on_its_neighbours(node, dt, renorm):  # noqa: F811
+    """Bit by bit: among rows whose sigmoids underflow, are NaN or are masked, as alone."""
+    import torch
+    rng = np.random.default_rng(5)
+    for X, k in ((8, 2), (16, 3), (100, 6)):
+        cfg = node.RouteConfig(X, k, score="sigmoid", renormalise=renorm)
+        z = rng.standard_normal((64, X)).astype(NP[dt])
+        other = z.copy()
+        other[1::2] = -4000.0 + other[1::2]
+        other[3::8] = np.nan
+        other[5::8] = -np.inf
+        g = rng.standard_normal((64, k)).astype(NP[dt])
+        e, a = node.tpconv_route_forward(cfg, dev(z))
+        e2, b = node.tpconv_route_forward(cfg, dev(other))
+        assert torch.equal(e[::2], e2[::2]) and torch.equal(a[::2], b[::2])
+        d, d2 = (node.tpconv_route_backward(cfg, dev(v), i, dev(g)) for v, i in ((z, e), (other, e2)))
+        assert torch.equal(d[::2], d2[::2])
