@@ -78,10 +78,12 @@ tpconv_status check_route(tpconv_dtype dt, int64_t n_rows, const tpconv_route_co
 
 const Experts* experts_of(tpconv_experts_t h) { return reinterpret_cast<const Experts*>(h); }
 
+// Whether rows times top_k is in [0, 2^31), without the product.
+bool few_enough(const Experts& p, int64_t n_rows) { return n_rows >= 0 && n_rows <= (kMaxRows - 1) / p.top_k; }
+
 tpconv_status check_experts(tpconv_experts_t h, int64_t n_rows) {
   if (h == nullptr) return bad("NULL experts plan");
-  if (n_rows < 0 || n_rows * int64_t(experts_of(h)->top_k) >= kMaxRows)
-    return bad("rows times top_k must be in [0, 2^31)");
+  if (!few_enough(*experts_of(h), n_rows)) return bad("rows times top_k must be in [0, 2^31)");
   return TPCONV_OK;
 }
 
@@ -273,7 +275,7 @@ extern "C" tpconv_status tpconv_experts_maps(tpconv_experts_t h, int64_t* maps) 
 extern "C" void tpconv_experts_destroy(tpconv_experts_t h) { delete reinterpret_cast<Experts*>(h); }
 
 extern "C" size_t tpconv_experts_layout_bytes(tpconv_experts_t h, int64_t n_rows) {
-  if (h == nullptr || n_rows < 0 || n_rows * int64_t(experts_of(h)->top_k) >= kMaxRows) return 0;
+  if (h == nullptr || !few_enough(*experts_of(h), n_rows)) return 0;
   return experts_layout_bytes(*experts_of(h), n_rows);
 }
 
@@ -305,7 +307,7 @@ extern "C" tpconv_status tpconv_experts_forward(tpconv_experts_t h, int64_t n_ro
 }
 
 extern "C" size_t tpconv_experts_workspace_bytes(tpconv_experts_t h, int64_t n_rows) {
-  if (h == nullptr || n_rows < 0 || n_rows * int64_t(experts_of(h)->top_k) >= kMaxRows) return 0;
+  if (h == nullptr || !few_enough(*experts_of(h), n_rows)) return 0;
   return experts_workspace(*experts_of(h), n_rows);
 }
 

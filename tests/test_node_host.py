@@ -162,3 +162,20 @@ def test_dropout_refusals(node):
     assert calls(irr=b"+".join([b"1x0e"] * 33), dim=33) == (UNSUPPORTED, UNSUPPORTED)
     assert calls(irr=b"16777216x0e", dim=1 << 24) == (UNSUPPORTED, UNSUPPORTED)
     assert calls(n=0, x=None, out=None) == (OK, OK)
+
+
+def test_row_counts_whose_entries_pass_64_bits(node):
+    """Rows times top_k is compared, not formed: 2^61 rows of 8 entries would wrap to none."""
+    lib = node._lib
+    for k in (1, 2, 7, 8):
+        plan = node.tpconv_experts_plan("4x0e", "4x0e", 16, k, "f32")
+        h = plan.handle
+        most = ((1 << 31) - 1) // k
+        assert lib.tpconv_experts_layout_bytes(h, most) > 0 and lib.tpconv_experts_workspace_bytes(h, most) > 0
+        for n in (most + 1, 1 << 31, 1 << 61, (1 << 61) + 1, min((1 << 64) // k + 1, (1 << 63) - 1), (1 << 63) - 1):
+            assert lib.tpconv_experts_layout_bytes(h, n) == 0, (k, n)
+            assert lib.tpconv_experts_workspace_bytes(h, n) == 0, (k, n)
+            for status in (lib.tpconv_experts_forward(h, n, *([None] * 7)),
+                           lib.tpconv_experts_layout(h, n, None, None, 0, None, None),
+                           lib.tpconv_experts_backward(h, n, *([None] * 10), 0, None)):
+                assert status == INVALID and b"rows times top_k" in lib.tpconv_last_error(), (k, n)
