@@ -54,9 +54,10 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // ------------------------------------------------------------------ layout
 // Rows are taken in groups of kGroup, fewer where top_k makes more than twice
-// as many entries of them (or of n / 64 when that is more: at most 64 groups);
-// each group is sorted by itself, which needs no exchange between blocks: one
-// launch whatever the size.
+// as many entries of them, more where n / 64 or 64 entries an expert are more
+// (at most 64 groups, and a group's experts have entries enough for their
+// pieces); each group is sorted by itself, which needs no exchange between
+// blocks: one launch whatever the size.
 //   order    the group's rows by the pair (smallest, next) of their experts, so
 //            that a tile of consecutive rows meets few experts
 //   listed   the rows' experts in that order (a tile's are then one run, known
@@ -84,7 +85,10 @@ LayoutShape layout_shape(const Experts& p, int64_t n) {
   // 32, 22 us of 128); longer ones (fewer sums to add) where there are entries enough
   L.piece = kLeastPiece;
   while (L.piece < kPiece && n * k * int64_t(p.maps.size()) > int64_t(1024) * L.piece) L.piece *= 2;
-  L.group = std::max<int64_t>(std::min<int64_t>(kGroup, 2 * kGroup / k), (n + 63) / 64);
+  // An expert has a piece of its own in every group, so with many experts the groups have to be longer: 28000 rows, 2
+  // of 256 experts, 64 channels l <= 3: 104 MB of pieces, gradients in 499 us, layout in 24; in groups of 2048 rows 268
+  // MB, 588 and 11 us
+  L.group = std::max<int64_t>({std::min<int64_t>(kGroup, 2 * kGroup / k), (n + 63) / 64, 64 * X / k});
   L.n_groups = std::max<int64_t>(1, (n + L.group - 1) / L.group);
   const int64_t most = std::min(L.group, std::max<int64_t>(n, 1)) * k;
   L.max_pieces = most / L.piece + X;

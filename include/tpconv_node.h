@@ -175,7 +175,11 @@ tpconv_status tpconv_experts_forward(tpconv_experts_t plan, int64_t n_rows, cons
                                      const int32_t* experts, const void* gates, const void* layout, void* out,
                                      hipStream_t stream);
 
-/* Workspace bytes of tpconv_experts_backward. */
+/* Workspace bytes of tpconv_experts_backward.  Most of them hold parts of
+ * grad_weights, matrices of weight_numel each: at most n_rows top_k / 32 +
+ * n_experts of them above 131072 entries (n_rows top_k times n_maps), n_rows
+ * top_k / 8 + n_experts below.  32768 rows, 8 of 256 experts, 64 channels l <= 3
+ * in fp32: 0.4 GB; 256 channels: 6.5 GB. */
 size_t tpconv_experts_workspace_bytes(tpconv_experts_t plan, int64_t n_rows);
 
 /* tpconv_experts_backward: gradients of <grad_out, out>:

@@ -177,3 +177,14 @@ def test_routing_of_a_row_does_not_depend_on_its_neighbours(node, dt, renorm):  
         assert torch.equal(e[::2], e2[::2]) and torch.equal(a[::2], b[::2])
         d, d2 = (node.tpconv_route_backward(cfg, dev(v), i, dev(g)) for v, i in ((z, e), (other, e2)))
         assert torch.equal(d[::2], d2[::2])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("n,X,k", [(5000, 256, 1), (2341, 256, 7), (2100, 200, 8)])
+def test_experts_in_groups_longer_than_two_rows_a_thread(node, dt, n, X, k):  # noqa: F811
+    """Many experts make the layout's groups longer; two groups, the second short."""
+    log(f"[node] long groups {dt} n={n} X={X} k={k}")
+    rng = np.random.default_rng([n, X])
+    experts = rng.integers(-1, X + 1, (n, k)).astype(np.int32)   # none, doubles and an index outside among them
+    experts[: n // 8] = X - 1
+    check_experts(node, dt, "3x0e+1x1o", "2x0e+2x1o", X, experts, rng.random((n, k)))

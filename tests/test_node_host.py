@@ -179,3 +179,20 @@ def test_row_counts_whose_entries_pass_64_bits(node):
                            lib.tpconv_experts_layout(h, n, None, None, 0, None, None),
                            lib.tpconv_experts_backward(h, n, *([None] * 10), 0, None)):
                 assert status == INVALID and b"rows times top_k" in lib.tpconv_last_error(), (k, n)
+
+
+def test_workspace_is_bounded_by_the_entries(node):
+    """The parts of the weights' gradient: a few for each hundred entries, however many the experts are."""
+    lib = node._lib
+    for dt, size in (("f32", 4), ("f64", 8)):
+        for irr in ("16x0e", "64x0e+64x1o+64x2e+64x3o", "256x4e"):
+            for X, k in ((1, 1), (16, 2), (64, 4), (200, 7), (256, 1), (256, 2), (256, 8)):
+                plan = node.tpconv_experts_plan(irr, irr, X, k, dt)
+                for n in (1, 100, 2048, 2049, 4096, 28000, 32768, 131072, 1000003):
+                    entries = n * k
+                    parts = entries // (32 if entries * plan.n_maps > 131072 else 8) + X + 1
+                    shares = sum((m // 16 + 1) for m in [int(t.split("x")[0]) for t in irr.split("+")]) * entries
+                    bound = size * (parts * plan.weight_numel + shares) + 4096
+                    assert lib.tpconv_experts_workspace_bytes(plan.handle, n) <= bound, (dt, irr, X, k, n)
+    plan = node.tpconv_experts_plan("64x0e+64x1o+64x2e+64x3o", "64x0e+64x1o+64x2e+64x3o", 256, 8, "f32")
+    assert lib.tpconv_experts_workspace_bytes(plan.handle, 32768) < 0.45e9     # x is 0.13 GB
