@@ -90,6 +90,14 @@ def _need(t, shape, dtype, name):
     return t
 
 
+def _need_bytes(t, name):
+    """A device buffer of any dtype; its size and alignment are the library's to check."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous cuda tensor, got {tuple(t.shape)} on {t.device}, "
+                         f"strides={t.stride()}")
+    return t
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -160,6 +168,7 @@ def tpconv_embedding_backward(types, grad_out, n_types: int, scale: float = 1.0,
     if workspace is None:
         need = int(_lib.tpconv_embedding_workspace_bytes(code, n, n_types, dim))
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=grad_out.device)
+    _need_bytes(workspace, "workspace")
     _check(_lib.tpconv_embedding_backward(code, n, n_types, dim, _ptr(types), _ptr(grad_out), stride, float(scale),
                                           _ptr(grad_table), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream_handle(stream)))
@@ -296,6 +305,7 @@ def tpconv_experts_layout(plan: ExpertsPlan, experts, load=None, buffer=None, st
     if buffer is None:
         need = int(_lib.tpconv_experts_layout_bytes(plan.handle, n))
         buffer = torch.empty(max(need, 256), dtype=torch.uint8, device=experts.device)
+    _need_bytes(buffer, "buffer")
     _check(_lib.tpconv_experts_layout(plan.handle, n, _ptr(experts), _ptr(buffer),
                                       buffer.numel() * buffer.element_size(), _ptr(load), _stream_handle(stream)))
     return ExpertsLayout(plan, n, buffer)
@@ -355,7 +365,7 @@ def tpconv_experts_backward(plan: ExpertsPlan, x, weights, experts, gates, grad_
     if workspace is None and (grad_weights is not None or grad_gates is not None):
         bytes_ = int(_lib.tpconv_experts_workspace_bytes(plan.handle, n))
         workspace = torch.empty(max(bytes_, 256), dtype=torch.uint8, device=dev)
-    held = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    held = 0 if workspace is None else _need_bytes(workspace, "workspace").numel() * workspace.element_size()
     _check(_lib.tpconv_experts_backward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(experts), _ptr(gates),
                                         _layout_of(plan, n, layout), _ptr(grad_out), _ptr(grad_x),
                                         _ptr(grad_weights), _ptr(grad_gates), _ptr(workspace), held,

@@ -188,3 +188,27 @@ def test_experts_in_groups_longer_than_two_rows_a_thread(node, dt, n, X, k):  # 
     experts = rng.integers(-1, X + 1, (n, k)).astype(np.int32)   # none, doubles and an index outside among them
     experts[: n // 8] = X - 1
     check_experts(node, dt, "3x0e+1x1o", "2x0e+2x1o", X, experts, rng.random((n, k)))
+
+
+# ------------------------------------------------------------------- refusals
+def test_buffers_that_are_not_on_the_device_are_refused(node):  # noqa: F811
+    """Workspaces and layout buffers in host memory or with gaps, before anything is launched."""
+    import torch
+    x = torch.zeros((4, 8), device="cuda")
+    types = torch.zeros(4, dtype=torch.int32, device="cuda")
+    plan = node.tpconv_experts_plan("8x0e", "8x0e", 3, 2)
+    e, g, w = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.zeros((4, 2), device="cuda"), \
+        torch.zeros((3, 64), device="cuda")
+    layout = node.tpconv_experts_layout(plan, e)
+    wide = torch.zeros((1 << 16, 2), dtype=torch.uint8, device="cuda")[:, 0]
+    for buffer in (torch.zeros(1 << 16, dtype=torch.uint8), torch.zeros(1 << 16, dtype=torch.uint8).pin_memory(), wide):
+        with pytest.raises(ValueError):
+            node.tpconv_embedding_backward(types, x, 3, workspace=buffer)
+        with pytest.raises(ValueError):
+            node.tpconv_experts_layout(plan, e, buffer=buffer)
+        with pytest.raises(ValueError):
+            node.tpconv_experts_backward(plan, x, w, e, g, x, layout, workspace=buffer)
+        with pytest.raises(ValueError):
+            node.tpconv_experts_backward(plan, x, w, e, g, x, need=(False, False, True), workspace=buffer)
+    with pytest.raises(RuntimeError, match="TPCONV_E_WORKSPACE"):
+        node.tpconv_experts_layout(plan, e, buffer=torch.zeros(16, dtype=torch.uint8, device="cuda"))
