@@ -2,7 +2,8 @@
 experts, the experts' equivariant maps, dropout on irreps rows.
 
 numpy only, one row or one expert at a time, straight from the formulas;
-shares no code with the GPU path.
+shares no code with the GPU path.  The functions that end in _many are the same
+for many rows at a time, in array operations.
 """
 
 from __future__ import annotations
@@ -145,6 +146,68 @@ def route_backward(logits, experts, grad_gates, cfg):
     return out
 
 
+def route_many(logits, bias, cfg):
+    """route_forward of numbers and masks (no NaN), and the smallest distance between keys that a row's choice hangs
+    on (inf where nothing is near)."""
+    z = np.asarray(logits, np.float64)
+    n, X = z.shape
+    with np.errstate(all="ignore"):
+        if cfg["score"] == "sigmoid":
+            e = np.exp(-np.abs(z))
+            s = np.where(z >= 0, 1.0, e) / (1.0 + e)
+        else:
+            e = np.where(np.isneginf(z), 0.0, np.exp(z - np.maximum(z.max(1, keepdims=True), -1e300)))
+            s = e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+    b = np.zeros(X) if bias is None else np.asarray(bias, np.float64)
+    key = np.where(np.isneginf(z) | np.isneginf(b), -np.inf, s + np.where(np.isneginf(b), 0.0, b))
+    gap = np.full(n, np.inf)
+    if cfg["n_groups"] > 1:
+        by = key.reshape(n, cfg["n_groups"], -1)
+        two = -np.sort(-by, axis=2)[:, :, :2]
+        best = np.where(np.isneginf(two[:, :, 0]), -np.inf, np.where(np.isneginf(two), 0.0, two).sum(2))
+        order = np.argsort(-best, axis=1, kind="stable")
+        inside = np.zeros(best.shape, bool)
+        np.put_along_axis(inside, order[:, :cfg["top_groups"]], True, 1)
+        if cfg["top_groups"] < cfg["n_groups"]:
+            ranked = np.take_along_axis(best, order, 1)[:, cfg["top_groups"] - 1:cfg["top_groups"] + 1]
+            gap = np.where(np.isneginf(ranked[:, 1]), np.inf, ranked[:, 0] - np.maximum(ranked[:, 1], -1e300))
+        key = np.where(inside[:, :, None], by, -np.inf).reshape(n, X)
+    at = np.argsort(-z, axis=1, kind="stable")
+    at = np.take_along_axis(at, np.argsort(-np.take_along_axis(key, at, 1), axis=1, kind="stable"), 1)
+    ranked = np.take_along_axis(key, at, 1)[:, :cfg["top_k"] + 1]
+    apart = np.where(np.isneginf(ranked[:, 1:]), np.inf, ranked[:, :-1] - np.maximum(ranked[:, 1:], -1e300))
+    gap = np.minimum(gap, apart.min(1, initial=np.inf))
+    at = at[:, :cfg["top_k"]]
+    has = ~np.isneginf(np.take_along_axis(key, at, 1))
+    return np.where(has, at, -1).astype(np.int32), gates_many(z, at, has, s, cfg), gap
+
+
+def gates_many(z, at, has, s, cfg):
+    picked = np.take_along_axis(z, at, 1)
+    if not cfg["renormalise"]:
+        return cfg["scale"] * np.where(has, np.take_along_axis(s, at, 1), 0.0)
+    with np.errstate(all="ignore"):
+        l = np.where(has, log_scores(picked, cfg["score"]), -np.inf)
+        w = np.where(has, np.exp(l - np.maximum(l.max(1, keepdims=True), -1e300)), 0.0)
+    return cfg["scale"] * w / np.maximum(w.sum(1, keepdims=True), 1e-300)
+
+
+def route_backward_many(logits, experts, gates, grad_gates, cfg):
+    """route_backward for route_many's experts and gates."""
+    z, g = np.asarray(logits, np.float64), np.where(experts < 0, 0.0, np.asarray(grad_gates, np.float64))
+    at, c = np.maximum(experts, 0), cfg["scale"]
+    with np.errstate(all="ignore"):
+        rest = 1.0 / (1.0 + np.exp(np.take_along_axis(z, at, 1))) if cfg["score"] == "sigmoid" else 1.0   # 1 - s
+        inner = (g * gates).sum(1, keepdims=True)
+        d = np.where(experts < 0, 0.0, gates * (g - inner / c if cfg["renormalise"] else g) * rest)
+    out = np.zeros_like(z)
+    np.add.at(out, (np.arange(len(z))[:, None], at), d)
+    if not cfg["renormalise"] and cfg["score"] == "softmax":
+        e = np.where(np.isneginf(z), 0.0, np.exp(z - np.maximum(z.max(1, keepdims=True), -1e300)))
+        out -= e / np.maximum(e.sum(1, keepdims=True), 1e-300) * inner
+    return out
+
+
 # -------------------------------------------------------------------- experts
 def expert_maps(irreps_in, irreps_out):
     """[(mul_in, col_in, mul_out, col_out, 2l+1, weight offset)] and an expert's weights."""
@@ -186,6 +249,26 @@ def experts_backward(irreps_in, irreps_out, x, weights, experts, gates, G):
     return gx, gw, gg
 
 
+def experts_many(irreps_in, irreps_out, x, weights, experts, gates, G):
+    """experts_forward and experts_backward: (out, grad_x, grad_weights, grad_gates)."""
+    x, weights, gates, G = (np.asarray(a, np.float64) for a in (x, weights, gates, G))
+    out = np.zeros((len(x), segments(irreps_out)[1]))
+    gx, gw, gg = np.zeros_like(x), np.zeros_like(weights), np.zeros_like(gates)
+    for e in range(len(weights)):
+        for a in range(experts.shape[1]):
+            rows = np.nonzero(experts[:, a] == e)[0]          # each row once
+            w = gates[rows, a][:, None, None]
+            for mi, ci, mo, co, d, at in expert_maps(irreps_in, irreps_out)[0]:
+                M = weights[e, at:at + mi * mo].reshape(mi, mo)
+                xs, Gs = x[rows, ci:ci + mi * d].reshape(-1, mi, d), G[rows, co:co + mo * d].reshape(-1, mo, d)
+                out[rows, co:co + mo * d] += (w * (M.T @ xs)).reshape(len(rows), -1)
+                back = M @ Gs
+                gx[rows, ci:ci + mi * d] += (w * back).reshape(len(rows), -1)
+                gw[e, at:at + mi * mo] += np.tensordot(w * xs, Gs, ((0, 2), (0, 2))).reshape(-1)
+                gg[rows, a] += (xs * back).sum((1, 2))
+    return out, gx, gw, gg
+
+
 # -------------------------------------------------------------------- dropout
 def philox4x32(counter, key, rounds=10):
     """Philox4x32 of four counter words and two key words (Python integers)."""
@@ -213,6 +296,23 @@ def dropout_keep(irreps, n_rows, p, seed, offset):
             out[:, at + u * (2 * l + 1):at + (u + 1) * (2 * l + 1)] = keep[:, c:c + 1]
             c += 1
     return out
+
+
+def dropout_keep_many(irreps, n_rows, p, seed, offset):
+    """dropout_keep, all blocks of the generator at a time."""
+    segs, dim = segments(irreps)
+    channels = sum(m for m, _, _, _ in segs)
+    low, half, block = np.uint64(0xFFFFFFFF), np.uint64(32), np.arange((n_rows * channels + 3) // 4, dtype=np.uint64)
+    c = [block & low, block >> half, np.full_like(block, offset & 0xFFFFFFFF), np.full_like(block, offset >> 32)]
+    k = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> half) ^ c[1] ^ np.uint64(k[0]), b & low, (a >> half) ^ c[3] ^ np.uint64(k[1]), a & low]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    words = np.stack(c, 1).reshape(-1)[:n_rows * channels].reshape(n_rows, channels)
+    of = np.concatenate([np.repeat(np.arange(m), 2 * l + 1) + sum(s[0] for s in segs[:i])
+                         for i, (m, l, _, _) in enumerate(segs)])
+    return (words >= np.uint64(int(np.floor(p * 2.0 ** 32))))[:, of]
 
 
 def dropout_forward(irreps, p, seed, offset, x, residual=None):

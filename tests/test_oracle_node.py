@@ -228,6 +228,45 @@ def test_experts_are_equivariant():
                                on.experts_forward(irr_in, irr_out, rotate(x, irr_in), w, experts, gates), atol=1e-12)
 
 
+# ------------------------------------------------------- many rows at a time
+@pytest.mark.parametrize("cfg", CONFIGS, ids=str)
+def test_route_of_many_rows_is_that_of_each(cfg):
+    rng = np.random.default_rng(13)
+    z = 2.0 * rng.standard_normal((60, 12))
+    z[:20] = np.round(z[:20])                                     # ties
+    z[rng.random(z.shape) < 0.3] = -np.inf
+    z[7], z[8] = -np.inf, 50.0 * z[8]
+    for bias in (None, 0.2 * rng.standard_normal(12), np.where(rng.random(12) < 0.3, -np.inf, 0.1)):
+        experts, gates = on.route_forward(z, bias, cfg)
+        e, g, gap = on.route_many(z, bias, cfg)
+        assert np.array_equal(e, experts)
+        np.testing.assert_allclose(g, gates, rtol=1e-13, atol=0)
+        grad = rng.standard_normal(gates.shape)
+        np.testing.assert_allclose(on.route_backward_many(z, e, g, grad, cfg),
+                                   on.route_backward(z, experts, grad, cfg), rtol=1e-11, atol=1e-15)
+        # the gap: choices outlast a change of the keys by less than half of it
+        for i in range(len(z)):
+            key = on.keys(z[i], bias, cfg["score"])
+            if cfg["n_groups"] == 1 and gap[i] < np.inf:
+                k = np.sort(key[~np.isneginf(key)])[::-1][:cfg["top_k"] + 1]
+                assert abs(gap[i] - (k[:-1] - k[1:]).min()) < 1e-15
+
+
+def test_experts_and_dropout_of_many_rows_are_those_of_each():
+    rng = np.random.default_rng(14)
+    irr_in, irr_out, n, X, k = "3x0e+2x1o+1x2e", "2x1o+4x0e", 40, 5, 3
+    x, G = rng.standard_normal((n, on.segments(irr_in)[1])), rng.standard_normal((n, on.segments(irr_out)[1]))
+    w, gates = rng.standard_normal((X, on.expert_maps(irr_in, irr_out)[1])), rng.random((n, k))
+    experts = rng.integers(-1, X + 1, (n, k))                     # none, doubles and an index outside among them
+    want = (on.experts_forward(irr_in, irr_out, x, w, experts, gates),
+            *on.experts_backward(irr_in, irr_out, x, w, experts, gates, G))
+    for a, b in zip(on.experts_many(irr_in, irr_out, x, w, experts, gates, G), want):
+        np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-13)
+    for irr in ("3x0e+2x1o+1x2e", "1x1o+1x1o+7x0e", "5x0e"):
+        args = (irr, 33, 0.3, 0xFEDCBA9876543210, (1 << 40) + 7)
+        assert (on.dropout_keep_many(*args) == on.dropout_keep(*args)).all()
+
+
 def test_segments_agree_with_the_convolution_oracle():
     for text in ("32x0e+32x1o", "4x1o+2x0e + 3x2e"):
         assert on.segments(text)[1] == parse_irreps(text).dim
