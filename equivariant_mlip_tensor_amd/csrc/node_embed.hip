@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a, int lg, const T* __r
         Pack<T> p = {};
         if (in) p = *reinterpret_cast<const Pack<T>*>(from);
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) p.v[q] *= scale;
+        for (int q = 0; q < kPer; ++q) p.v[q] = in ? scale * p.v[q] : T(0);
         *reinterpret_cast<Pack<T>*>(to) = p;
       } else {
         *to = in ? scale * *from : T(0);

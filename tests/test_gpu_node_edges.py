@@ -212,3 +212,17 @@ def test_buffers_that_are_not_on_the_device_are_refused(node):  # noqa: F811
             node.tpconv_experts_backward(plan, x, w, e, g, x, need=(False, False, True), workspace=buffer)
     with pytest.raises(RuntimeError, match="TPCONV_E_WORKSPACE"):
         node.tpconv_experts_layout(plan, e, buffer=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------------ embedding
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("dim", [3, 4, 64])
+def test_embedding_of_padding_rows_is_zero_whatever_the_scale(node, dt, dim):  # noqa: F811
+    import torch
+    t = np.array([-1, 0, 7, 1, -1], np.int32)
+    table = torch.ones((2, dim), dtype=getattr(torch, {"f32": "float32", "f64": "float64"}[dt]), device="cuda")
+    for scale in (float("inf"), float("nan")):
+        out = node.tpconv_embedding_forward(dev(t), table, scale).cpu().numpy()
+        assert (out[[0, 2, 4]] == 0).all() and not np.isfinite(out[[1, 3]]).any()
+        grad = node.tpconv_embedding_backward(dev(t), torch.ones((5, dim), dtype=table.dtype, device="cuda"), 3, scale)
+        assert (grad[2] == 0).all() and not torch.isfinite(grad[:2]).any()
