@@ -310,14 +310,15 @@ __global__ __launch_bounds__(kThreads) void k_embed_runs(EmbedArgs a, int lg, in
 constexpr int kList = 1024;
 
 template <class T>
-__global__ __launch_bounds__(1024) void k_embed_join(int64_t dim, int64_t chunks, int64_t blocks, int most,
+__global__ __launch_bounds__(1024) void k_embed_join(int64_t block0, int64_t dim, int64_t chunks, int64_t blocks, int most,
                                                      const int32_t* __restrict__ runs, const T* __restrict__ part,
                                                      T* __restrict__ out) {
   __shared__ int64_t list[kList];
   __shared__ int counts[16];
   __shared__ T sums[16][64];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, nw = blockDim.x >> 6;
-  const int64_t t = blockIdx.x / chunks, c = (blockIdx.x - t * chunks) * 64 + lane, col = min(c, dim - 1);
+  const int64_t block = block0 + blockIdx.x, t = block / chunks, c = (block - t * chunks) * 64 + lane;
+  const int64_t col = min(c, dim - 1);
   T total = 0;
   for (int64_t b0 = 0; b0 < blocks; b0 += blockDim.x) {
     const int64_t b = b0 + tid;
@@ -412,9 +413,11 @@ hipError_t backward(const EmbedArgs& a, const T* grad, T* grad_table, void* ws, 
   const int64_t chunks = (a.dim + 63) / 64;
   if (a.n_types * chunks > INT32_MAX) return hipErrorInvalidValue;
   // a wavefront for each 16 blocks to add, 16 at most
-  const int waves = static_cast<int>(std::min<int64_t>(16, (space.blocks + 15) / 16));
-  hipLaunchKernelGGL(k_embed_join<T>, dim3(static_cast<unsigned>(a.n_types * chunks)), dim3(64 * std::max(1, waves)), 0,
-                     s, a.dim, chunks, space.blocks, most, runs, part, grad_table);
+  const int threads = 64 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (space.blocks + 15) / 16)));
+  in_launches(a.n_types * chunks, threads, [&](int64_t first, unsigned blocks) {
+    hipLaunchKernelGGL(k_embed_join<T>, dim3(blocks), dim3(threads), 0, s, first, a.dim, chunks, space.blocks, most, runs,
+                       part, grad_table);
+  });
   return hipGetLastError();
 }
 

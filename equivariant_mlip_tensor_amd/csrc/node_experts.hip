@@ -323,6 +323,7 @@ struct RowArgs {
   int32_t X, k, n_maps, waves;
   int32_t tile;       // rows of a tile, at most kTile
   int32_t n_tiles;
+  int32_t block0;     // this launch's first block
   RowLds lds;
   RowMap map[kMaxMaps];
 };
@@ -696,12 +697,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 8 ? 2 : (ADJ ? 3 : 4)) void k_row
     const T* __restrict__ gates, const int32_t* __restrict__ order, T* __restrict__ dst, const T* __restrict__ other,
     T* __restrict__ gate_part) {
   extern __shared__ char lds[];
-  const int share = static_cast<int>(blockIdx.x) / a.n_tiles;
+  const int block = a.block0 + static_cast<int>(blockIdx.x), share = block / a.n_tiles;
   int mi = 0;
 #pragma unroll
   for (int q = 1; q < kMaxMaps; ++q) mi += share >= a.first[q];
   const RowMap& m = a.map[mi];
-  const int64_t base = int64_t(static_cast<int>(blockIdx.x) - share * a.n_tiles) * a.tile;
+  const int64_t base = int64_t(block - share * a.n_tiles) * a.tile;
   const int rows = static_cast<int>(min<int64_t>(a.tile, a.n_rows - base));
   const int n_base = (share - a.first[mi]) * 16 * a.waves;
 #define TPCONV_MAP_ROWS(D)                                                                                         \
@@ -756,6 +757,7 @@ struct WgradArgs {
   int64_t max_pieces, group;
   int64_t slots;  // pieces of all groups, at most
   int32_t X, k, n_maps, piece;
+  int32_t block0;  // this launch's first block
   int32_t direct;  // every expert has one piece at most: straight into grad_weights, zeros for those without
   WgradMap map[kMaxMaps];
 };
@@ -781,9 +783,10 @@ __global__ __launch_bounds__(256) void k_wgrad(WgradArgs a, const T* __restrict_
   __shared__ T at_gate[kPiece];
   __shared__ int found[2];
   int mi = 0;
-  while (mi + 1 < a.n_maps && static_cast<int>(blockIdx.x) >= a.map[mi + 1].first) ++mi;
+  const int block = a.block0 + static_cast<int>(blockIdx.x);
+  while (mi + 1 < a.n_maps && block >= a.map[mi + 1].first) ++mi;
   const WgradMap m = a.map[mi];
-  const int64_t r = int64_t(blockIdx.x) - m.first;
+  const int64_t r = block - m.first;
   const int64_t slot = r % a.slots;
   const int uv = static_cast<int>(r / a.slots), u0 = uv / m.nv * S, v0 = uv % m.nv * S;
   const int64_t grp = slot / a.max_pieces;
@@ -969,7 +972,7 @@ __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <class T, int KS, bool ADJ, bool GG>
-hipError_t rows_ks(const RowArgs& a, unsigned blocks, const T* src, const T* weights, const int32_t* experts,
+hipError_t rows_ks(RowArgs a, int64_t blocks, const T* src, const T* weights, const int32_t* experts,
                    const T* gates, const int32_t* order, T* dst, const T* other, T* part, hipStream_t s) {
   auto* const f = k_rows<T, KS, ADJ, GG>;
   if (a.lds.total > 64 * 1024) {  // above the default limit of dynamic LDS
@@ -978,8 +981,11 @@ hipError_t rows_ks(const RowArgs& a, unsigned blocks, const T* src, const T* wei
                             static_cast<int>(a.lds.total));
     if (he != hipSuccess) return he;
   }
-  hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * a.waves), a.lds.total, s, a, src, weights, experts, gates, order, dst,
-                     other, part);
+  in_launches(blocks, 64 * a.waves, [&](int64_t block0, unsigned n) {
+    a.block0 = static_cast<int32_t>(block0);
+    hipLaunchKernelGGL(f, dim3(n), dim3(64 * a.waves), a.lds.total, s, a, src, weights, experts, gates, order, dst,
+                       other, part);
+  });
   return hipGetLastError();
 }
 
@@ -1071,7 +1077,7 @@ hipError_t rows(const Experts& p, int64_t n, const T* src, const T* weights, con
   a.lds.ents = take(entries, 4);
   a.lds.total = o;
   if (a.lds.total > 160 * 1024) return hipErrorInvalidValue;
-  const unsigned blocks = static_cast<unsigned>(tiles * n_parts);
+  const int64_t blocks = tiles * n_parts;
   T* const gg = n_parts == 1 ? gate_grad : part;
   for (const ColumnRun& r : ADJ ? p.bare_in : p.bare_out)
     if (dst != nullptr)
@@ -1102,10 +1108,12 @@ BackwardSpace backward_space(const Experts& p, int64_t n) {
 }
 
 template <class T, int S, bool VEC>
-hipError_t wgrad_launch(const WgradArgs& a, int64_t blocks, const T* x, const T* gates, const T* grad,
+hipError_t wgrad_launch(WgradArgs a, int64_t blocks, const T* x, const T* gates, const T* grad,
                         const int32_t* entries, const int32_t* first, const int32_t* pieces, T* out, hipStream_t s) {
-  hipLaunchKernelGGL((k_wgrad<T, S, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a, x, gates, grad,
-                     entries, first, pieces, out);
+  in_launches(blocks, 256, [&](int64_t block0, unsigned n) {
+    a.block0 = static_cast<int32_t>(block0);
+    hipLaunchKernelGGL((k_wgrad<T, S, VEC>), dim3(n), dim3(256), 0, s, a, x, gates, grad, entries, first, pieces, out);
+  });
   return hipGetLastError();
 }
 

@@ -13,6 +13,14 @@ namespace tpconv {
 constexpr int kMaxMaps = 2 * (kMaxL + 1);  // one per (l, parity)
 constexpr int kMaxDropSegs = 32;
 
+// A grid of 2^32 threads or more is taken without an error and not run as asked,
+// so blocks go out in launches of fewer: launch(first block, blocks).
+template <class F>
+void in_launches(int64_t blocks, int threads, F&& launch) {
+  const int64_t most = ((int64_t(1) << 32) - 1) / threads;
+  for (int64_t b = 0; b < blocks; b += most) launch(b, static_cast<unsigned>(blocks - b < most ? blocks - b : most));
+}
+
 // ------------------------------------------------------------- embedding
 struct EmbedArgs {
   int64_t n_rows, n_types, dim, stride;

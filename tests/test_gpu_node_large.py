@@ -44,6 +44,21 @@ def test_embedding(node, dt, n, types, dim, stride):  # noqa: F811
     within(got, 1.7 * np.stack(sums, 1), (count + 6) * EPS[dt] * 1.7 * np.stack(sizes, 1), "grad_table")
 
 
+def test_embedding_gradient_of_more_types_than_one_launch_has_blocks(node):  # noqa: F811
+    """4.2 million types whose sums come from 293 blocks: a type for each block would pass 2^32 threads."""
+    rng = np.random.default_rng(3)
+    n, types = 300001, 4200000
+    t = rng.integers(0, types, n).astype(np.int32)
+    t[:3] = 0, types - 1, -1
+    grad = rng.standard_normal((n, 2))
+    got = node.tpconv_embedding_backward(dev(t), dev(grad), types).cpu().numpy()
+    live = t >= 0
+    count = np.bincount(t[live], minlength=types)
+    for c in range(2):
+        want, size = (np.bincount(t[live], weights=v[live, c], minlength=types) for v in (grad, np.abs(grad)))
+        assert (np.abs(got[:, c] - want) <= (count + 6) * EPS["f64"] * size).all()
+
+
 # -------------------------------------------------------------------- routing
 @pytest.mark.parametrize("dt", ["f32", "f64"])
 @pytest.mark.parametrize("score,renorm,n,X,G,T,k,biased", [
@@ -120,6 +135,45 @@ def test_experts(node, dt, n, irr_in, irr_out, X, k):  # noqa: F811
         within(a, b, c * EPS[dt] * s, what)
     again = node.tpconv_experts_backward(plan, *args, dev(G), node.tpconv_experts_layout(plan, args[2]))
     assert all(torch.equal(a, b) for a, b in zip(got[1:], again))
+
+
+def test_experts_of_more_rows_than_one_launch_has_tiles(node):  # noqa: F811
+    """2^30 rows of two channels: a block for each tile and map would pass 2^32 threads, for the rows and for the
+    weights' gradient.  All values are small whole numbers and every sum stays below 2^24, so results are exact."""
+    import torch
+    n, irr = (1 << 30) + 48, "1x0e+1x0o"
+    plan = node.tpconv_experts_plan(irr, irr, 2, 1)
+    w = torch.tensor([[3.0, -2.0], [5.0, 7.0]], device="cuda")
+    x, G = torch.empty((n, 2), device="cuda"), torch.empty((n, 2), device="cuda")
+    e, gates = torch.empty((n, 1), dtype=torch.int32, device="cuda"), torch.empty((n, 1), device="cuda")
+    step = 48 << 20
+
+    def part(i0):
+        """Rows i0.. of x, G, experts and gates, and what comes of them."""
+        i = torch.arange(i0, min(n, i0 + step), device="cuda", dtype=torch.int32)
+        a = torch.stack([1 + i % 3, 2 - i % 2], 1).float()
+        b = torch.stack([1 - i % 4 // 2 * 2 + (i % 65536 == 5), i % 3 - 1], 1).float()   # a few above a sum of 0
+        ex = ((i // 12) % 3 - 1).int()[:, None]                 # none, 0, 1
+        gate = (1 + (i // 36) % 2).float()[:, None]
+        we = torch.where(ex >= 0, w[ex[:, 0].clamp(min=0).long()], 0.0)
+        live = torch.where(ex >= 0, gate, 0.0)
+        return (a, b, ex, gate), (live * we * a, live * we * b, (we * a * b).sum(1, keepdim=True)), live * a * b
+
+    sums = torch.zeros((2, 2), dtype=torch.float64, device="cuda")
+    for i0 in range(0, n, step):
+        (a, b, ex, gate), _, terms = part(i0)
+        for to, value in ((x, a), (G, b), (e, ex), (gates, gate)):
+            to[i0:i0 + step] = value
+        for q in range(2):
+            sums[q] += (terms * (ex == q)).double().sum(0)
+    layout = node.tpconv_experts_layout(plan, e)
+    out = node.tpconv_experts_forward(plan, x, w, e, gates, layout)
+    gx, gw, gg = node.tpconv_experts_backward(plan, x, w, e, gates, G, layout)
+    for i0 in range(0, n, step):
+        want = part(i0)[1]
+        for got, value, what in zip((out, gx, gg), want, ("out", "grad_x", "grad_gates")):
+            assert torch.equal(got[i0:i0 + step], value), (what, i0)
+    assert torch.equal(gw, sums.float()) and float(sums.abs().max()) < 2 ** 24
 
 
 # -------------------------------------------------------------------- dropout
