@@ -566,6 +566,7 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
   }
 
   const int col = min(n_base + 16 * w + i16, m.N - 1);  // past the last channel: a column that is not written
+  const bool whole = n_base + 16 * w + 16 <= m.N;       // the wavefront has a channel in every column
   T mine[GG ? D : 1][4];                                // GG: this lane's x
   if (GG) {
     mover_dst.finish(xs, other_from, dst_row, rows, n_here, a.waves);
@@ -655,6 +656,9 @@ __device__ __forceinline__ void map_rows(const RowArgs& a, const RowMap& m, int 
           T v[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = prod[q] * mine[GG ? c : 0][q];
+          if (!whole)  // an infinite product in the place of a channel that is not there is no NaN in the sum
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = n_base + 16 * w + i16 < m.N ? v[q] : T(0);
           const T s = sums16(v, i16);
           if (i16 < 4) rsum[16 * c + Mfma<T>::row(g4, i16)] = s;
         }

@@ -226,3 +226,22 @@ def test_embedding_of_padding_rows_is_zero_whatever_the_scale(node, dt, dim):  #
         assert (out[[0, 2, 4]] == 0).all() and not np.isfinite(out[[1, 3]]).any()
         grad = node.tpconv_embedding_backward(dev(t), torch.ones((5, dim), dtype=table.dtype, device="cuda"), 3, scale)
         assert (grad[2] == 0).all() and not torch.isfinite(grad[:2]).any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("mul", [1, 5, 16, 17, 50, 65])
+def test_experts_gate_gradients_that_are_infinite(node, dt, mul):  # noqa: F811
+    """One product overflows, in the last channel: the gate's gradient is infinite with its sign, not NaN."""
+    import torch
+    rng = np.random.default_rng(mul)
+    irr, n, k, X = f"{mul}x1o", 20, 2, 3
+    plan = node.tpconv_experts_plan(irr, irr, X, k, dt)
+    x, G = (rng.random((n, 3 * mul)) + 0.5 for _ in range(2))
+    w = rng.random((X, mul, mul)) + 0.5
+    G[:, -1], w[1, mul - 1, mul - 1] = 1e10, 0.5 * float(np.finfo(NP[dt]).max)   # of the last component alone
+    experts = np.tile(np.array([0, 1], np.int32), (n, 1))
+    experts[::3] = [2, 0]
+    a = [dev(v.astype(NP[dt])) for v in (x, w.reshape(X, -1))] + [dev(experts)] + [dev(np.ones((n, k), NP[dt]))]
+    layout = node.tpconv_experts_layout(plan, a[2])
+    gg = node.tpconv_experts_backward(plan, *a, dev(G.astype(NP[dt])), layout, need=(False, False, True))[2]
+    assert (torch.isposinf(gg).cpu().numpy() == (experts == 1)).all() and not torch.isnan(gg).any()
