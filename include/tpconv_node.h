@@ -111,6 +111,10 @@ tpconv_status tpconv_route_forward(tpconv_dtype dtype, int64_t n_rows, const tpc
  *   renormalised: d_a = w_a (g_a - sum_b g_b w_b / c), times (1 - s_a) for sigmoid;
  *   softmax: c s_j ([j chosen] g_j - sum_a g_a s_a) for every j;
  *   sigmoid: c g_a s_a (1 - s_a).
+ * Renormalised, w is formed from the chosen logits and no others are read: NaN
+ * in these or in grad_gates makes the entries of the chosen NaN, NaN elsewhere
+ * in the row does not (the forward's gates show it).  Not renormalised, a NaN
+ * score makes NaN of the entries whose formula has it.  Masked experts get 0.
  * Entries with index -1 are skipped whatever grad_gates holds there.  An
  * index outside [0, n_experts) is taken as -1; an expert that stands twice in
  * a row gets both gradients.  Errors as the forward. */

@@ -122,7 +122,8 @@ def route_forward(logits, bias, cfg):
 
 
 def route_backward(logits, experts, grad_gates, cfg):
-    """grad_logits through the full Jacobian of the chosen scores."""
+    """grad_logits through the full Jacobian of the chosen scores; renormalised gates are functions of the chosen logits
+    alone, and a masked expert's gradient is 0."""
     z, g = np.asarray(logits, np.float64), np.asarray(grad_gates, np.float64)
     out = np.zeros_like(z)
     for i in range(len(z)):
@@ -130,8 +131,10 @@ def route_backward(logits, experts, grad_gates, cfg):
         e = [int(experts[i, a]) for a in at]
         if not e:
             continue
-        w = gates_of(z[i], e, cfg)
+        # renormalised over the chosen: as if they were the row
+        w = gates_of(z[i, e], list(range(len(e))), cfg) if cfg["renormalise"] else None
         s = scores(z[i], cfg["score"])
+        live = ~np.isneginf(z[i])
         ga = g[i, at]
         if cfg["renormalise"]:
             d = w * (ga - np.dot(ga, w) / cfg["scale"]) if cfg["scale"] else 0.0 * w
@@ -142,7 +145,7 @@ def route_backward(logits, experts, grad_gates, cfg):
             np.add.at(out[i], e, cfg["scale"] * ga * s[e] * (1.0 - s[e]))
         else:
             np.add.at(out[i], e, cfg["scale"] * ga * s[e])
-            out[i] -= cfg["scale"] * s * np.dot(ga, s[e])
+            out[i, live] -= cfg["scale"] * s[live] * np.dot(ga, s[e])
     return out
 
 

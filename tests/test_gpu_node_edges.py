@@ -245,3 +245,28 @@ def test_experts_gate_gradients_that_are_infinite(node, dt, mul):  # noqa: F811
     layout = node.tpconv_experts_layout(plan, a[2])
     gg = node.tpconv_experts_backward(plan, *a, dev(G.astype(NP[dt])), layout, need=(False, False, True))[2]
     assert (torch.isposinf(gg).cpu().numpy() == (experts == 1)).all() and not torch.isnan(gg).any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("X,G,T,k", [(8, 1, 1, 3), (24, 6, 3, 5), (100, 50, 9, 8), (7, 7, 3, 3)])
+def test_routing_gradient_of_not_numbers(node, dt, score, renorm, X, G, T, k):  # noqa: F811
+    """NaN where the formula has one, for the same rows as the forward; the masked get 0."""
+    rng = np.random.default_rng([X, G, 2])
+    cfg, ocfg = config(node, n_experts=X, top_k=k, score=score, renormalise=renorm, n_groups=G, top_groups=T)
+    z = separated(rng, 40, X, None, ocfg, dt, 0.05)
+    put_not_numbers(rng, z, X // G)
+    experts, _ = node.tpconv_route_forward(cfg, dev(z))
+    e = experts.cpu().numpy()
+    g = rng.standard_normal((40, k)).astype(NP[dt])
+    g[11, 0] = np.nan
+    got = node.tpconv_route_backward(cfg, dev(z), experts, dev(np.where(e < 0, 1.0, g).astype(NP[dt])))
+    got = got.cpu().numpy().astype(np.float64)
+    with np.errstate(all="ignore"):
+        want = on.route_backward(z, e, g, ocfg)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert (got[np.isneginf(z)] == 0).all()
+    # a gate (1 at most) times gradients of the row, and their rounding as in test_gpu_node.py
+    size = 3 * (gate_tol(X, dt) + (k + 6) * EPS[dt]) * 2 * np.nansum(np.abs(np.where(e < 0, 0.0, g)), 1, keepdims=True)
+    assert (np.abs(got - want) <= size)[~np.isnan(want)].all()
