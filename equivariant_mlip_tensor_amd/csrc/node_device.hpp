@@ -5,6 +5,11 @@
 
 namespace tpconv {
 
+template <class T>
+struct alignas(16) Pack {  // one 16-byte piece
+  T v[16 / sizeof(T)];
+};
+
 // Orders a wavefront's own LDS accesses: what its lanes wrote before is seen by
 // all of them after, and what they read before is read before it is written
 // again.  No instruction comes of it (a wavefront's LDS operations run in

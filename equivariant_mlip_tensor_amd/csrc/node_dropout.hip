@@ -121,8 +121,6 @@ __global__ __launch_bounds__(kThreads) void k_dropout(DropArgs a, int tile, uint
   }
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 template <class T>
 hipError_t dropout(const DropArgs& a, const T* x, const T* residual, T* out, hipStream_t s) {
   constexpr int kPer = 16 / sizeof(T);

@@ -10,15 +10,6 @@
 namespace tpconv {
 namespace {
 
-template <class T>
-struct alignas(16) Pack {  // one 16-byte piece
-  T v[16 / sizeof(T)];
-};
-
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
-
 // -------------------------------------------------------------------- forward
 // A copy: the table stays in cache, out is streamed.  Lanes share a row in
 // groups of a power of two, so no lane divides by the row's length.  Bound by

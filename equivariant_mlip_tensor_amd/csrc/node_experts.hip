@@ -40,17 +40,10 @@ struct Mfma<double> {
   static __device__ __forceinline__ int row(int g, int r) { return 4 * r + g; }
 };
 
-template <class T>
-struct alignas(16) Pack {  // one 16-byte load
-  T v[16 / sizeof(T)];
-};
-
 int blocks_for(int64_t n, int block) {
   const int64_t g = (n + block - 1) / block;
   return static_cast<int>(g < 1 ? 1 : (g > 65536 ? 65536 : g));
 }
-
-size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // ------------------------------------------------------------------ layout
 // Rows are taken in groups of kGroup, fewer where top_k makes more than twice
@@ -973,8 +966,6 @@ __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int 
 }
 
 // -------------------------------------------------------------------- host
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 template <class T, int KS, bool ADJ, bool GG>
 hipError_t rows_ks(RowArgs a, int64_t blocks, const T* src, const T* weights, const int32_t* experts,
                    const T* gates, const int32_t* order, T* dst, const T* other, T* part, hipStream_t s) {

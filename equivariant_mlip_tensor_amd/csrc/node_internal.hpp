@@ -13,6 +13,10 @@ namespace tpconv {
 constexpr int kMaxMaps = 2 * (kMaxL + 1);  // one per (l, parity)
 constexpr int kMaxDropSegs = 32;
 
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+inline size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+
 // A grid of 2^32 threads or more is taken without an error and not run as asked,
 // so blocks go out in launches of fewer: launch(first block, blocks).
 template <class F>
