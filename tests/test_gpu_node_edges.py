@@ -270,3 +270,40 @@ def test_routing_gradient_of_not_numbers(node, dt, score, renorm, X, G, T, k):  
     # a gate (1 at most) times gradients of the row, and their rounding as in test_gpu_node.py
     size = 3 * (gate_tol(X, dt) + (k + 6) * EPS[dt]) * 2 * np.nansum(np.abs(np.where(e < 0, 0.0, g)), 1, keepdims=True)
     assert (np.abs(got - want) <= size)[~np.isnan(want)].all()
+
+
+def test_experts_second_derivatives_from_the_same_calls(node):  # noqa: F811
+    """The maps are linear in x, in the weights and in the gates, so the gradients of
+
+        S = <grad_x, u> + <grad_weights, v> + <grad_gates, t>
+
+    are sums of forwards and backwards with one argument replaced by its direction; here against differences."""
+    import torch
+    rng = np.random.default_rng(31)
+    irr_in, irr_out, n, X, k = "5x0e+4x1o+3x2e", "3x0e+6x1o+2x2e", 40, 4, 2
+    plan = node.tpconv_experts_plan(irr_in, irr_out, X, k, "f64")
+    experts = rng.integers(-1, X, (n, k)).astype(np.int32)
+    e = dev(experts)
+    layout = node.tpconv_experts_layout(plan, e)
+    shapes = dict(x=(n, plan.dim_in), w=(X, plan.weight_numel), g=(n, k), G=(n, plan.dim_out))
+    a = {name: dev(rng.standard_normal(s)) for name, s in shapes.items()}
+    u, v, t = (dev(rng.standard_normal(shapes[name])) for name in "xwg")
+
+    def forward(x, w, g):
+        return node.tpconv_experts_forward(plan, x, w, e, g, layout)
+
+    def backward(x, w, g, G):
+        return node.tpconv_experts_backward(plan, x, w, e, g, G, layout)
+
+    def S(x, w, g, G):
+        return sum(float((p * q).sum()) for p, q in zip(backward(x, w, g, G), (u, v, t)))
+
+    x, w, g, G = a["x"], a["w"], a["g"], a["G"]
+    at_u, at_v, at_t = backward(u, w, g, G), backward(x, v, g, G), backward(x, w, t, G)
+    second = dict(G=forward(u, w, g) + forward(x, v, g) + forward(x, w, t), x=at_v[0] + at_t[0], w=at_u[1] + at_t[1],
+                  g=at_u[2] + at_v[2])
+    for name, grad in second.items():
+        d = dev(rng.standard_normal(shapes[name]))
+        lo, hi = (S(**dict(a, **{name: a[name] + s * d})) for s in (-0.5, 0.5))
+        # linear in each argument: only the difference's own rounding is left (about 1e4 terms of size 10, step 1/2)
+        assert abs(hi - lo - float((grad * d).sum())) < 1e-8, name
