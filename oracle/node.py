@@ -260,6 +260,8 @@ def experts_many(irreps_in, irreps_out, x, weights, experts, gates, G):
     for e in range(len(weights)):
         for a in range(experts.shape[1]):
             rows = np.nonzero(experts[:, a] == e)[0]          # each row once
+            if not len(rows):
+                continue
             w = gates[rows, a][:, None, None]
             for mi, ci, mo, co, d, at in expert_maps(irreps_in, irreps_out)[0]:
                 M = weights[e, at:at + mi * mo].reshape(mi, mo)

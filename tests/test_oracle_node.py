@@ -267,6 +267,17 @@ def test_experts_and_dropout_of_many_rows_are_those_of_each():
         assert (on.dropout_keep_many(*args) == on.dropout_keep(*args)).all()
 
 
+def test_experts_of_many_rows_where_an_expert_has_none():
+    rng = np.random.default_rng(15)
+    x, G, w = rng.standard_normal((4, 5)), rng.standard_normal((4, 5)), rng.standard_normal((6, 5))
+    for experts in (np.array([[0], [5], [-1], [5]]), np.full((4, 1), -1)):
+        gates = rng.random((4, 1))
+        want = (on.experts_forward("2x0e+1x1o", "2x0e+1x1o", x, w, experts, gates),
+                *on.experts_backward("2x0e+1x1o", "2x0e+1x1o", x, w, experts, gates, G))
+        for a, b in zip(on.experts_many("2x0e+1x1o", "2x0e+1x1o", x, w, experts, gates, G), want):
+            np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-13)
+
+
 def test_segments_agree_with_the_convolution_oracle():
     for text in ("32x0e+32x1o", "4x1o+2x0e + 3x2e"):
         assert on.segments(text)[1] == parse_irreps(text).dim
