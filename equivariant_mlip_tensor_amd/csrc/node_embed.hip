@@ -13,8 +13,8 @@ namespace {
 // -------------------------------------------------------------------- forward
 // A copy: the table stays in cache, out is streamed.  Lanes share a row in
 // groups of a power of two, so no lane divides by the row's length.  Bound by
-// the writes: 250001 fp32 rows of 128 take 31.5 us (4.1 TB/s), 28000 rows of 64
-// into rows of 1024 take 4.3 us, 16 fp64 rows 1.5 us (the launch).
+// the writes: 250001 fp32 rows of 128 take 34 us (3.8 TB/s), 28000 rows of 64
+// into rows of 1024 take 4.5 us, 16 fp64 rows 1.6 us (the launch).
 template <class T, bool VEC>
 __global__ __launch_bounds__(256) void k_embed(EmbedArgs a, int lg, const T* __restrict__ table,
                                                T* __restrict__ out) {
@@ -52,9 +52,13 @@ __global__ __launch_bounds__(256) void k_embed(EmbedArgs a, int lg, const T* __r
 // list in `runs`; the second kernel adds each type's sums over the blocks, in
 // order.  (A walk over all atoms by each type's own threads reads the types as
 // often as there are types: 41 ms at 250001 rows.)  250001 fp32 rows of 128, 97
-// types: 38 us, 3.4 TB/s: each block's sort, then its reads, in turn (blocks of
-// half the length: 37 us and 3.4 more for the join); 28000 rows of 64, 5 types:
-// 9.2 us (latency); 16 fp64 rows in one block: 5.8 us.
+// types: 38 us, 3.4 TB/s: each block's sort, then its reads, in turn, so that
+// wavefronts wait in 71 % of their cycles (blocks of half the length: 37 us and
+// 3.4 more for the join); 28000 rows of 64, 5 types: 9.2 us (latency); 16 fp64
+// rows in one block: 5.7 us.  Narrow rows have many groups and so short slices:
+// with rows of one piece 512 groups share a block, and a run over many slices is
+// joined by one of them, part after part: 250001 rows of one column take 44 us
+// with 2 types, 28 with 5, 15 with 97.
 constexpr int kRows = 1024;  // rows of a block, at most
 constexpr int kThreads = 512;
 constexpr int kCounters = 4096;  // of the sort by counting: 16 KiB of LDS, four blocks still share a CU's
@@ -180,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_embed_runs(EmbedArgs a, int lg, in
         __syncthreads();
       }
   }
-  // number the runs: 4 sorted rows a thread
+  // number the runs: kEach sorted rows a thread
   constexpr int kEach = kRows / kThreads;
   int starts[kEach], mine = 0;
 #pragma unroll
@@ -297,13 +301,13 @@ __global__ __launch_bounds__(kThreads) void k_embed_runs(EmbedArgs a, int lg, in
 // a search of their sorted lists (a thread for each), are listed in order; the
 // wavefronts each add a run of the list, 8 sums on their way at a time, and
 // their results are added in order.  Bound by the latency of search, list and
-// sums in turn: 7.4 us for 97 types of 245 blocks, 5.0 us for 5 types of 438.
+// sums in turn: 7.3 us for 97 types of 245 blocks, 5.3 us for 5 types of 219.
 constexpr int kList = 1024;
 
 template <class T>
-__global__ __launch_bounds__(1024) void k_embed_join(int64_t block0, int64_t dim, int64_t chunks, int64_t blocks, int most,
-                                                     const int32_t* __restrict__ runs, const T* __restrict__ part,
-                                                     T* __restrict__ out) {
+__global__ __launch_bounds__(1024) void k_embed_join(int64_t block0, int64_t dim, int64_t chunks, int64_t blocks,
+                                                     int most, const int32_t* __restrict__ runs,
+                                                     const T* __restrict__ part, T* __restrict__ out) {
   __shared__ int64_t list[kList];
   __shared__ int counts[16];
   __shared__ T sums[16][64];

@@ -146,8 +146,8 @@ __device__ int scan_counters(int* c, int n, int* wave_sums) {
 // results do not depend on its neighbours.  Entries are ranked by counting in
 // order, so theirs is fixed.  Latency bound, so the group's experts are read
 // once, into LDS, where they fit, and the two sorts run in blocks of their own:
-// 10.6 us at 28000 rows of 2 entries over 16 experts, 9.5 us at 4096 rows of 4
-// over 32, 3.8 us for one row.
+// 10.5 us at 28000 rows of 2 entries over 16 experts, 24 us over 256, 9.4 us at
+// 4096 rows of 4 over 32, 3.8 us for one row.
 constexpr int kStaged = 16384;
 
 __global__ __launch_bounds__(1024) void k_layout(int64_t n, int X, int k, int H, int64_t group, int piece,
@@ -285,14 +285,19 @@ __global__ void k_load(int X, int64_t n_groups, const int32_t* __restrict__ firs
 // The next expert's weights are on their way while one's are in use.  A
 // wavefront owns 16 output channels.  ADJ runs the transposed maps on
 // grad_out; GG also dots the products with x for the gates' gradient.
-// 28000 fp32 rows of 64 channels l <= 3, 2 of 16 experts: 148 us, and 216 us
+// 28000 fp32 rows of 64 channels l <= 3, 2 of 16 experts: 145 us, and 213 us
 // transposed with the gates' gradient; 229 MB and 344 MB are 46 and 69 us at the
-// rate of a copy and 7.3 GFLOP are 48 us at that of a library product: bound by
-// the matrix units (chunks that hold some of an expert's rows are multiplied
-// whole) in turn with each wavefront's staging of its tile.  Where few tiles
-// leave two wavefronts a SIMD, the trips to memory and the matrix instructions
-// of one wavefront's experts in turn decide: 4096 rows of 32 channels, 4 of 32
-// experts, 36 us; 2048 fp64 rows of 16 channels l <= 4, 2 of 8, 17 us and 24 us.
+// rate of a copy and 7.3 GFLOP are 48 us at that of a library product.  No unit
+// is full: the matrix units are busy in 35 % of the cycles (24 % transposed; 1.12
+// times the needed products, since chunks that hold some of an expert's rows are
+// multiplied whole) and the vector units in 32 % (35 %); a wavefront waits in 40 %
+// (50 %) of its cycles for memory, LDS or a barrier, with four (three) wavefronts
+// a SIMD to take its place.  (Transposed with the gates' gradient, two wavefronts
+// and no spilled registers: 245 us.)  Where few tiles leave two wavefronts a SIMD,
+// the trips to memory and the matrix instructions of one wavefront's experts in
+// turn decide: 4096 rows of 32 channels, 4 of 32 experts, 35 us (2.2 times the
+// needed products, matrix units 17 %); 2048 fp64 rows of 16 channels l <= 4, 2 of
+// 8, 17 us and 24 us (matrix units 3 %).
 // (32 output channels a wavefront: 213 us for the first; sums in LDS with the
 // members packed into full chunks: 171 us; all maps of a tile in one block: 199.)
 constexpr int kTile = 16;
@@ -738,9 +743,10 @@ __global__ void k_zero_columns(int64_t n_rows, int64_t dim, int32_t off, int32_t
 // stage's loads are in flight in registers; 4 wavefronts share the tile (S =
 // 16: they share the rows, and are added in order at the end).  Each piece's
 // matrix goes to the workspace; k_join adds an expert's pieces in order.
-// Bound by the gathers: each entry's rows of x and G once, 459 MB in 141 us (3.3
-// TB/s) at 28000 fp32 rows of 64 channels l <= 3 with 2 of 16 experts; 12 us for
-// 2048 fp64 rows of 16 channels l <= 4 with 2 of 8.
+// Bound by the gathers and the products in turn: each entry's rows of x and G
+// once, 459 MB in 137 us (3.3 TB/s; matrix units busy in 33 % of the cycles,
+// wavefronts waiting in 39 % of theirs) at 28000 fp32 rows of 64 channels l <= 3
+// with 2 of 16 experts; 11.5 us for 2048 fp64 rows of 16 channels l <= 4, 2 of 8.
 struct WgradMap {
   int32_t in_off, out_off, U, V, d, woff;
   int32_t nu, nv;     // S x S tiles of the matrix
@@ -910,7 +916,7 @@ __global__ __launch_bounds__(256) void k_wgrad(WgradArgs a, const T* __restrict_
 // Adds what the kernels above left in parts, in order: an expert's pieces
 // (blocks [0, X nw): nw blocks of 256 weights each) and the shares of the
 // gates' gradient (the blocks after them).  Bound by latency and the read of the
-// pieces: 12.7 us for 16 experts' 16384 weights and 56000 gates, 5.2 us for 8
+// pieces: 13-16 us for 16 experts' 16384 weights and 56000 gates, 6 us for 8
 // experts' 1280 weights and 4096 gates in fp64.
 template <class T>
 __global__ __launch_bounds__(256) void k_join(int X, int nw, int64_t numel, int n_groups, int64_t max_pieces,

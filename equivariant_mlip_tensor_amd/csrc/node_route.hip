@@ -10,10 +10,11 @@
 // hold it: no sort, and ties are settled exactly.  The forward is bound by its
 // vector instructions, the gradient by its reads of single logits and gates,
 // each of which waits for the expert's number: 131072 fp32 rows of 128 experts
-// in 8 groups, 6 chosen, take 54 us (1000 instructions for four rows, a fourth
-// of them in the groups' search and a fourth in the rounds) and 21 us; 67 MB of
-// logits read and 67 MB of their gradient written are 13 us each at the rate of
-// a copy.  28000 rows of 16 experts take 4.5 us and 5.3 us.
+// in 8 groups, 6 chosen, take 57 us (1090 instructions for four rows, a fourth
+// of them in the groups' search and a fourth in the rounds; the vector units are
+// busy in 95 % of the cycles) and 22 us; 67 MB of logits read and 67 MB of their
+// gradient written are 13 us each at the rate of a copy.  28000 rows of 16
+// experts take 4.4 us and 5.4 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -164,8 +165,8 @@ constexpr int kThreads = 256;
 // keys are the logits, which have the scores' order and tell apart scores that
 // round to one number (0 or 1); with one, equal keys go by the logits, so that a
 // bias of zeros chooses the same.  fp32 rows of up to 128 are held to 96
-// registers, five wavefronts a SIMD: 131072 rows of 128 in groups in 56 us, with
-// two registers more and four wavefronts in 58.
+// registers, five wavefronts a SIMD: 131072 rows of 128 in groups in 56-57 us,
+// with two registers more and four wavefronts in 59.
 template <class T, int LG, int VPL, bool BY_SCORE>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void k_route(
     RouteArgs a, const T* __restrict__ logits, const T* __restrict__ bias, int32_t* __restrict__ experts,
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
     choose(std::false_type{});
     if (by_bias) {
       // equal keys, rare, stand side by side, the last chosen's perhaps among those left: then the rounds are made
-      // again with the logits (131072 rows of 128 in groups: 56 us; with a check in each round 60)
+      // again with the logits (131072 rows of 128 in groups: 56-57 us; with a check in each round 59-60)
       const Key before = of_lane<LG>(picked, max(sub - 1, 0)), left = largest();
       const bool equal = (sub > 0 && sub < a.k && picked == before) || (sub == a.k - 1 && picked == left);
       if (__any(equal && picked > kNaN)) {
