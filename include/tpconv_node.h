@@ -20,7 +20,8 @@
  * synchronising it, no floating-point atomics (repeated calls give bitwise
  * identical outputs).  Data types: TPCONV_F32 and TPCONV_F64, the library's
  * own; sums and softmax statistics are held in the data type (32 bits or
- * more).  Row counts are below 2^31; offsets are 64-bit.  Nothing here
+ * more).  Outputs may overlap neither inputs nor each other, but where a call
+ * says so.  Row counts are below 2^31; offsets are 64-bit.  Nothing here
  * allocates or clears memory through the runtime, so every call can be
  * captured into a HIP graph.
  */

@@ -307,3 +307,37 @@ def test_experts_second_derivatives_from_the_same_calls(node):  # noqa: F811
         lo, hi = (S(**dict(a, **{name: a[name] + s * d})) for s in (-0.5, 0.5))
         # linear in each argument: only the difference's own rounding is left (about 1e4 terms of size 10, step 1/2)
         assert abs(hi - lo - float((grad * d).sum())) < 1e-8, name
+
+
+# -------------------------------------------------------------------- capture
+@pytest.mark.parametrize("irr,X,k", [("64x4e", 3, 2), ("200x3o+5x0e", 200, 8)])
+def test_experts_with_more_than_64_kib_of_lds_in_a_graph(node, irr, X, k):  # noqa: F811
+    """Blocks above the default limit of LDS are set up outside the stream: calls can be captured all the same."""
+    import torch
+    n, g = 300, torch.Generator(device="cuda").manual_seed(3)
+    plan = node.tpconv_experts_plan(irr, irr, X, k, "f64")
+
+    def inputs():
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float64)  # noqa: E731
+        return [r(n, plan.dim_in), r(X, plan.weight_numel),
+                torch.randint(-1, X, (n, k), generator=g, device="cuda").int(), r(n, k), r(n, plan.dim_out)]
+
+    def call(x, w, e, gates, G):
+        layout = node.tpconv_experts_layout(plan, e)
+        return (node.tpconv_experts_forward(plan, x, w, e, gates, layout),
+                *node.tpconv_experts_backward(plan, x, w, e, gates, G, layout))
+
+    held = inputs()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                              # the first call of these kernels
+        got = call(*held)
+    for _ in range(3):
+        new = inputs()
+        for a, b in zip(held, new):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        have = [a.clone() for a in got]
+        for a, b in zip(have, call(*new)):
+            assert torch.equal(a, b)

@@ -174,6 +174,8 @@ def test_experts_of_more_rows_than_one_launch_has_tiles(node):  # noqa: F811
         for got, value, what in zip((out, gx, gg), want, ("out", "grad_x", "grad_gates")):
             assert torch.equal(got[i0:i0 + step], value), (what, i0)
     assert torch.equal(gw, sums.float()) and float(sums.abs().max()) < 2 ** 24
+    del x, G, e, gates, layout, out, gx, gw, gg
+    torch.cuda.empty_cache()
 
 
 # -------------------------------------------------------------------- dropout
