@@ -10,7 +10,7 @@
 // hold it: no sort, and ties are settled exactly.  The forward is bound by its
 // vector instructions, the gradient by its reads of single logits and gates,
 // each of which waits for the expert's number: 131072 fp32 rows of 128 experts
-// in 8 groups, 6 chosen, take 57 us (1090 instructions for four rows, a fourth
+// in 8 groups, 6 chosen, take 55 us (1050 instructions for four rows, a fourth
 // of them in the groups' search and a fourth in the rounds; the vector units are
 // busy in 95 % of the cycles) and 22 us; 67 MB of logits read and 67 MB of their
 // gradient written are 13 us each at the rate of a copy.  28000 rows of 16
@@ -78,6 +78,12 @@ __device__ __forceinline__ uint64_t across(uint64_t v) {
   return uint64_t(across<STEP>(static_cast<uint32_t>(v >> 32))) << 32 | across<STEP>(static_cast<uint32_t>(v));
 }
 
+// v of the lane before (0 in lanes 0, 16, 32, 48)
+__device__ __forceinline__ uint32_t lane_before(uint32_t v) { return dpp<0x111>(v); }
+__device__ __forceinline__ uint64_t lane_before(uint64_t v) {
+  return uint64_t(dpp<0x111>(static_cast<uint32_t>(v >> 32))) << 32 | dpp<0x111>(static_cast<uint32_t>(v));
+}
+
 struct Max {
   template <class T>
   __device__ __forceinline__ T operator()(T a, T b) const {
@@ -110,11 +116,11 @@ __device__ __forceinline__ T of_lane(T v, int from) {
 // every score.
 __device__ __forceinline__ uint32_t ordered(float s) {
   const uint32_t b = __float_as_uint(s + 0.0f);  // one zero
-  return (b >> 31) != 0 ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t ordered(double s) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
-  return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
+  return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
 }
 
 // maximum and sum of exponentials of a row's softmax (masked entries add
@@ -141,12 +147,13 @@ __device__ __forceinline__ T gate_of(const RouteArgs& a, T z, bool has, T top, T
     T e = 0;
     // sigmoids far from underflow are divided as they are, others through their logarithms: by rows, so that a row's
     // gates do not depend on the others of its wavefront
-    bool plain = false;
+    uint64_t low = ~uint64_t(0);  // lanes with a score that is not far from it
     if (a.sigmoid) {
       e = has ? sigmoid(z) : T(0);
-      plain = reduce<L>(uint32_t(has && !(e > T(1e-30))), Max{}) == 0;
+      low = __ballot(has && !(e > T(1e-30)));
     }
-    if (__any(!plain)) {
+    if (low != 0) {
+      const bool plain = ((low >> (threadIdx.x & 63 & ~((1 << LG) - 1))) & ((1u << (1 << LG)) - 1)) == 0;
       const T l = a.sigmoid ? log_sigmoid(z) : z;
       const bool number = has && l == l;
       const T m = reduce<L>(number ? l : -inf<T>(), Max{});
@@ -164,11 +171,12 @@ constexpr int kThreads = 256;
 // summed); 28000 rows of 16 take 4.6 us without, 5.4 with.  Without a bias the
 // keys are the logits, which have the scores' order and tell apart scores that
 // round to one number (0 or 1); with one, equal keys go by the logits, so that a
-// bias of zeros chooses the same.  fp32 rows of up to 128 are held to 96
-// registers, five wavefronts a SIMD: 131072 rows of 128 in groups in 56-57 us,
-// with two registers more and four wavefronts in 59.
+// bias of zeros chooses the same.  Rows of up to 128 are held to the registers of
+// five wavefronts a SIMD (fp64: three): 131072 rows of 128 in groups in 55 us,
+// with two registers more and four wavefronts in 59; 65536 fp64 rows in 57 us,
+// with two wavefronts in 67.
 template <class T, int LG, int VPL, bool BY_SCORE>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void k_route(
+__global__ __launch_bounds__(kThreads, VPL <= 8 ? (sizeof(T) == 4 ? 5 : 3) : 1) void k_route(
     RouteArgs a, const T* __restrict__ logits, const T* __restrict__ bias, int32_t* __restrict__ experts,
     T* __restrict__ gates) {
   constexpr int P = 1 << LG, kRows = kThreads / P, X_MAX = P * VPL;
@@ -190,13 +198,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
   };
   load(int64_t(blockIdx.x) * kRows);
   T shift[BY_SCORE ? VPL : 1];     // the experts' biases
-  int group_of[BY_SCORE ? VPL : 1];
+  uint32_t group_of[(VPL + 3) / 4] = {};  // a byte for each expert
   if (BY_SCORE)
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int e = min(v * P + sub, a.X - 1);
       shift[v] = bias != nullptr ? bias[e] : T(0);
-      group_of[v] = e / per;
+      group_of[v / 4] |= static_cast<uint32_t>(e / per) << (v % 4 * 8);
     }
   for (int64_t i0 = int64_t(blockIdx.x) * kRows; i0 < a.n_rows; i0 += step) {
     const int64_t i = min(i0 + in_block, a.n_rows - 1);  // lanes past the end redo the last row and write nothing
@@ -208,6 +216,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
     T top = 0, sum = 1;
     if (!a.sigmoid) softmax_stats<T, LG>(z, top, sum);
     const T inv = T(1) / sum;
+    bool odd = false;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       T s = z[v];
@@ -218,12 +227,18 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
       }
       const bool masked = z[v] == -inf<T>() || (BY_SCORE && shift[BY_SCORE ? v : 0] == -inf<T>());
       score[v] = masked ? -inf<T>() : s;
+      odd |= score[v] != score[v];
     }
+    odd = __any(odd);  // NaN among the wavefront's scores: rare
     uint32_t out_of_group = 0;  // bit v: the group of expert v * P + sub is not chosen
     if (BY_SCORE && a.top_groups < a.groups) {
       wave_sync();
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) row[v * P + sub] = score[v] == score[v] ? score[v] : lowest(T(0));
+      for (int v = 0; v < VPL; ++v) row[v * P + sub] = score[v];
+      if (odd)
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+          if (score[v] != score[v]) row[v * P + sub] = lowest(T(0));
       wave_sync();
       for (int g = sub; g < a.groups; g += P) {
         T k1 = -inf<T>(), k2 = -inf<T>();
@@ -249,15 +264,24 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
       wave_sync();
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
-        if (group[64 + group_of[BY_SCORE ? v : 0]] == T(0)) out_of_group |= 1u << v;
+        if (group[64 + ((group_of[v / 4] >> (v % 4 * 8)) & 255)] == T(0)) out_of_group |= 1u << v;
     }
     Key key[VPL];
+    auto make_keys = [&](const T (&by)[VPL]) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const Key number = ordered(by_bias ? score[v] : z[v]), live = score[v] == score[v] ? number : kNaN;
-      const bool out = score[v] == -inf<T>() || ((out_of_group >> v) & 1) != 0;
-      key[v] = out ? Key(0) : live;
-    }
+      for (int v = 0; v < VPL; ++v) {
+        const Key number = ordered(by[v]);
+        key[v] = score[v] == -inf<T>() || ((out_of_group >> v) & 1) != 0 ? Key(0) : number;
+      }
+    };
+    if (by_bias)
+      make_keys(score);
+    else
+      make_keys(z);
+    if (odd)
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+        if (score[v] != score[v] && ((out_of_group >> v) & 1) == 0) key[v] = kNaN;
     wave_sync();
 #pragma unroll
     for (int v = 0; v < VPL; ++v) row[v * P + sub] = z[v];  // out of the registers during the rounds
@@ -265,16 +289,13 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
     // the next in the order (key descending, then index ascending or, with LOGITS, logit descending and index
     // ascending), top_k times; lane j keeps the j-th and its key
     int pick = -1;
-    Key picked = 0;
-    auto largest = [&] {
-      Key most = key[0];
-#pragma unroll
-      for (int v = 1; v < VPL; ++v) most = key[v] > most ? key[v] : most;
-      return reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
-    };
+    Key picked = 0, last = 0;
     auto choose = [&](auto LOGITS) {
       for (int j = 0; j < a.k; ++j) {
-        const Key m = largest();
+        Key most = key[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) most = key[v] > most ? key[v] : most;
+        const Key m = reduce<LG>(most, [](Key x, Key y) { return x > y ? x : y; });
         T best = -inf<T>();
         if constexpr (LOGITS) {
 #pragma unroll
@@ -292,17 +313,19 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
           if (e == v * P + sub) key[v] = 0;
-        pick = sub == j ? (m != 0 ? e : -1) : pick;
+        pick = sub == j ? e : pick;
         picked = sub == j ? m : picked;
+        last = m;
       }
     };
     choose(std::false_type{});
     if (by_bias) {
       // equal keys, rare, stand side by side, the last chosen's perhaps among those left: then the rounds are made
-      // again with the logits (131072 rows of 128 in groups: 56-57 us; with a check in each round 59-60)
-      const Key before = of_lane<LG>(picked, max(sub - 1, 0)), left = largest();
-      const bool equal = (sub > 0 && sub < a.k && picked == before) || (sub == a.k - 1 && picked == left);
-      if (__any(equal && picked > kNaN)) {
+      // again with the logits (131072 rows of 128 in groups: 55 us; with a check in each round 59-60)
+      bool equal = sub > 0 && picked > kNaN && picked == lane_before(picked);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) equal |= key[v] == last && last > kNaN;
+      if (__any(equal)) {
         for (int j = 0; j < a.k; ++j) {
           const int e = of_lane<LG>(pick, j);
           const Key m = of_lane<LG>(picked, j);
@@ -313,7 +336,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && VPL <= 8 ? 5 : 1) void 
         choose(std::true_type{});
       }
     }
-    const bool has = sub < a.k && pick >= 0;
+    pick = picked != 0 ? pick : -1;  // nothing was left
+    const bool has = pick >= 0;
     T w = gate_of<T, LG>(a, has ? row[pick] : T(0), has, top, sum);
     if (!a.sigmoid && has && sum != sum) w = sum;  // NaN in, NaN out
     if (live && sub < a.k) {
