@@ -48,13 +48,14 @@ def _jobs():
     units.append((os.path.join(CSRC, "graph.hip"), os.path.join(BUILD, "graph.o"), []))
     units.append((os.path.join(CSRC, "sh.hip"), os.path.join(BUILD, "sh.o"), []))
     units.append((os.path.join(CSRC, "so2.hip"), os.path.join(BUILD, "so2.o"), []))
-    for stem in ("node_embed", "node_route", "node_experts", "node_dropout"):
+    for stem in ("node_dense", "node_norm", "node_experts", "node_embed", "node_route", "node_dropout"):
         units.append((os.path.join(CSRC, stem + ".hip"), os.path.join(BUILD, stem + ".o"), []))
     # the host CG builder runs without FMA contraction so its run-time values
     # are bit-identical to the kernels' compile-time evaluation
     units.append((os.path.join(CSRC, "plan.cpp"), os.path.join(BUILD, "plan.o"), ["-ffp-contract=off"]))
     units.append((os.path.join(CSRC, "api.cpp"), os.path.join(BUILD, "api.o"), []))
-    units.append((os.path.join(CSRC, "node_api.cpp"), os.path.join(BUILD, "node_api.o"), []))
+    for stem in ("node_api", "node_block_api"):
+        units.append((os.path.join(CSRC, stem + ".cpp"), os.path.join(BUILD, stem + ".o"), []))
     return units
 
 

@@ -1,51 +1,13 @@
 // node_api.cpp -- the node operators' C entry points: argument checks, the
 // experts' plan, and dispatch to the kernels of node_*.hip.
 #include <cmath>
-#include <exception>
-#include <new>
 #include <string>
 
+#include "node_check.hpp"
 #include "node_internal.hpp"
 
 namespace tpconv {
 namespace {
-
-constexpr int64_t kMaxRows = int64_t(1) << 31;
-
-// Runs an entry point's body; no C++ exception leaves the library.
-template <class F>
-tpconv_status guarded(F&& body) noexcept {
-  try {
-    return body();
-  } catch (const std::exception& e) {
-    try {
-      return fail(TPCONV_E_INVALID_ARG, e.what());
-    } catch (...) {
-      return TPCONV_E_INVALID_ARG;
-    }
-  } catch (...) {
-    return TPCONV_E_INVALID_ARG;
-  }
-}
-
-tpconv_status bad(const std::string& msg) { return fail(TPCONV_E_INVALID_ARG, msg); }
-
-tpconv_status launched(hipError_t he, const char* what) {
-  if (he != hipSuccess) return fail(TPCONV_E_HIP, std::string(what) + " launch: " + hipGetErrorString(he));
-  return TPCONV_OK;
-}
-
-bool known(tpconv_dtype dt) { return dt == TPCONV_F32 || dt == TPCONV_F64; }
-
-tpconv_status check_workspace(const void* ws, size_t have, size_t need, const char* what) {
-  if (need == 0) return TPCONV_OK;
-  if (ws == nullptr || have < need)
-    return fail(TPCONV_E_WORKSPACE,
-                std::string(what) + " holds " + std::to_string(have) + " bytes, needs " + std::to_string(need));
-  if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
-    return fail(TPCONV_E_WORKSPACE, std::string(what) + " must be 256-byte aligned");
-  return TPCONV_OK;
-}
 
 tpconv_status check_embedding(tpconv_dtype dt, int64_t n_rows, int64_t n_types, int64_t dim, int64_t stride) {
   if (!known(dt)) return bad("unknown dtype");

@@ -98,4 +98,71 @@ struct DropArgs {
 };
 hipError_t launch_dropout(bool f64, const DropArgs& a, const void* x, const void* residual, void* out, hipStream_t s);
 
+// ------------------------------------------------------------ norm, 8 bits
+constexpr int kMaxNormSegs = 32;
+
+struct NormSeg {
+  int32_t off, end;  // columns [off, end)
+  int32_t d;         // 2 l + 1
+  int32_t channel;   // first channel
+};
+struct NormArgs {
+  int64_t n_rows;
+  int32_t dim, n_segs, channels;
+  int32_t lanes;     // of a row (the kernels' own)
+  bool row_scope;
+  double eps;
+  NormSeg seg[kMaxNormSegs];
+};
+size_t norm_workspace(bool f64, const NormArgs& a, int64_t n_rows);
+hipError_t launch_norm_forward(bool f64, const NormArgs& a, const void* x, const void* residual, const void* gamma,
+                               void* sum, void* out, uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_norm_backward(bool f64, const NormArgs& a, const void* h, const void* gamma, const void* grad_out,
+                                const void* grad_sum, void* grad_x, void* grad_gamma, void* ws, hipStream_t s);
+hipError_t launch_pack8(const NormArgs& a, const float* x, uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_unpack8(NormArgs a, const uint8_t* codes, const float* scales, float* x, hipStream_t s);
+
+// -------------------------------------------------------- gated and linear
+// One pair of equal (l, parity) segments.
+struct DenseMap {
+  int32_t in_off, out_off, mul_in, mul_out;
+  int32_t d;       // 2 l + 1
+  int32_t woff;    // first weight
+  int32_t seg_in;  // segment of irreps_in
+  int32_t gate;    // first channel of the output segment
+  int32_t act;
+  bool even;       // 0e
+};
+
+struct Dense {
+  std::vector<DenseMap> maps;
+  std::vector<int64_t> listing;  // seg_in, seg_out, l, woff per map
+  std::vector<ColumnRun> bare_in;
+  int64_t dim_in = 0, dim_out = 0, weight_numel = 0, n_gates = 0;
+  int32_t n_segs_in = 0;
+  int32_t scalar_off = 0, scalar_mul = 0, scalar_seg = 0;  // gated: irreps_in's 0e
+  int32_t scalar_out_mul = 0;                              // linear: mul of irreps_out's 0e
+  int32_t act = TPCONV_ACT_IDENTITY;                       // linear
+  bool gated = false, f64 = false;
+  bool even_out = false;                                   // irreps_out has 0e
+  // linear: grad_out's even scalars pass an activation
+  bool sloped() const { return !gated && even_out && act != TPCONV_ACT_IDENTITY; }
+};
+
+// Rows, or 8-bit codes and scales of them.
+struct DenseInput {
+  const void* rows;
+  const uint8_t* codes;
+  const float* scales;
+};
+
+size_t dense_workspace(const Dense& p, int64_t n_rows);
+hipError_t launch_dense_forward(const Dense& p, int64_t n_rows, const void* x, const void* weights,
+                                const void* gate_weights, const void* bias, const void* residual, void* out,
+                                hipStream_t s);
+hipError_t launch_dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, const void* weights,
+                                 const void* gate_weights, const void* bias, const void* grad_out, void* grad_x,
+                                 void* grad_weights, void* grad_gate_weights, void* grad_bias, void* ws,
+                                 hipStream_t s);
+
 }  // namespace tpconv

@@ -1,8 +1,9 @@
 """ctypes binding of libtpconv.so's node operators (include/tpconv_node.h).
 
-What a mixture-of-experts potential runs on its atoms around the convolution:
-species embedding, routing to experts, the experts' equivariant maps, and
-dropout on irreps rows.  As in ``tpconv``, torch supplies device memory and
+What a mixture-of-experts potential, or one with a feed-forward block, runs on
+its atoms around the convolution: species embedding, routing to experts, the
+experts' equivariant maps, dropout on irreps rows, their norm with the
+residual's sum, rows in 8 bits, gated feed-forward products and linear maps.  As in ``tpconv``, torch supplies device memory and
 the stream and every step runs in the library's HIP kernels.
 
     x = torch.zeros(n, dim, device="cuda")
@@ -13,6 +14,15 @@ the stream and every step runs in the library's HIP kernels.
     layout = tpconv_experts_layout(plan, experts)
     y      = tpconv_experts_forward(plan, x, weights, experts, gates, layout)
     x      = tpconv_dropout_forward("64x0e+64x1o", 0.1, seed, step, y, residual=x)
+
+    norm   = tpconv_norm_plan("64x0e+64x1o")
+    gated  = tpconv_gated_plan("64x0e+64x1o", "128x0e+128x1o")
+    linear = tpconv_linear_plan("128x0e+128x1o", "64x0e+64x1o")
+    y, h, kept = tpconv_norm_forward(norm, x, residual, gamma, need=(True, True, True))
+    t      = tpconv_gated_forward(gated, y, weights, gate_weights, gate_bias)
+    x      = tpconv_linear_forward(linear, t, weights2, bias, residual=h)
+    ...                                       # y is freed; its rows in 8 bits, kept, serve the gradient
+    g_y, g_weights, g_gate_weights, g_bias = tpconv_gated_backward(gated, kept, weights, gate_weights, gate_bias, g_t)
 
 Each forward has its backward; the layouts are those of the header.
 """
@@ -31,9 +41,17 @@ NODE_EXPORTS = ("tpconv_embedding_forward", "tpconv_embedding_workspace_bytes", 
                 "tpconv_route_forward", "tpconv_route_backward", "tpconv_experts_plan", "tpconv_experts_query",
                 "tpconv_experts_maps", "tpconv_experts_destroy", "tpconv_experts_layout_bytes",
                 "tpconv_experts_layout", "tpconv_experts_forward", "tpconv_experts_workspace_bytes",
-                "tpconv_experts_backward", "tpconv_dropout_forward", "tpconv_dropout_backward")
+                "tpconv_experts_backward", "tpconv_dropout_forward", "tpconv_dropout_backward",
+                "tpconv_norm_plan", "tpconv_norm_query", "tpconv_norm_destroy", "tpconv_norm_forward",
+                "tpconv_norm_workspace_bytes", "tpconv_norm_backward", "tpconv_pack8", "tpconv_unpack8",
+                "tpconv_gated_plan", "tpconv_linear_plan", "tpconv_dense_query", "tpconv_dense_maps",
+                "tpconv_dense_destroy", "tpconv_gated_forward", "tpconv_linear_forward",
+                "tpconv_dense_workspace_bytes", "tpconv_gated_backward", "tpconv_linear_backward")
 
 MAX_EXPERTS, MAX_TOP_K, MAX_EXPERT_MUL = 256, 8, 256
+MAX_NORM_DIM, MAX_DENSE_MUL = 8192, 1024
+_SCOPES = {"segment": 0, "row": 1}
+_ACTIVATIONS = {"identity": 0, "silu": 1, "sigmoid": 2, "tanh": 3, "gelu": 4}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _CODE = {torch.float32: F32, torch.float64: F64}
 _DTYPE = {F32: torch.float32, F64: torch.float64}
@@ -49,6 +67,18 @@ class ExpertsInfo(ctypes.Structure):
     _fields_ = [("dim_in", ctypes.c_int64), ("dim_out", ctypes.c_int64), ("weight_numel", ctypes.c_int64),
                 ("n_maps", ctypes.c_int64), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class NormInfo(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int64), ("channels", ctypes.c_int64), ("n_segments", ctypes.c_int32),
+                ("scope", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("eps", ctypes.c_double)]
+
+
+class DenseInfo(ctypes.Structure):
+    _fields_ = [("dim_in", ctypes.c_int64), ("dim_out", ctypes.c_int64), ("weight_numel", ctypes.c_int64),
+                ("n_maps", ctypes.c_int64), ("n_gates", ctypes.c_int64), ("n_scalars", ctypes.c_int64),
+                ("n_bias", ctypes.c_int64), ("n_segments_in", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 def _declare():
@@ -72,6 +102,24 @@ def _declare():
         "tpconv_experts_backward": (i32, [vp, i64] + [vp] * 10 + [sz, vp]),
         "tpconv_dropout_forward": (i32, [text, i32, i64, i64, f64, u64, u64, vp, vp, vp, vp]),
         "tpconv_dropout_backward": (i32, [text, i32, i64, i64, f64, u64, u64, vp, vp, vp]),
+        "tpconv_norm_plan": (i32, [text, i32, f64, i32, ctypes.POINTER(vp)]),
+        "tpconv_norm_query": (i32, [vp, ctypes.POINTER(NormInfo)]),
+        "tpconv_norm_destroy": (None, [vp]),
+        "tpconv_norm_forward": (i32, [vp, i64] + [vp] * 8),
+        "tpconv_norm_workspace_bytes": (sz, [vp, i64]),
+        "tpconv_norm_backward": (i32, [vp, i64] + [vp] * 7 + [sz, vp]),
+        "tpconv_pack8": (i32, [text, i64, i64, vp, vp, vp, vp]),
+        "tpconv_unpack8": (i32, [text, i64, i64, vp, vp, vp, vp]),
+        "tpconv_gated_plan": (i32, [text, text, i32, i32, i32, ctypes.POINTER(vp)]),
+        "tpconv_linear_plan": (i32, [text, text, i32, i32, ctypes.POINTER(vp)]),
+        "tpconv_dense_query": (i32, [vp, ctypes.POINTER(DenseInfo)]),
+        "tpconv_dense_maps": (i32, [vp, vp]),
+        "tpconv_dense_destroy": (None, [vp]),
+        "tpconv_gated_forward": (i32, [vp, i64] + [vp] * 6),
+        "tpconv_linear_forward": (i32, [vp, i64] + [vp] * 6),
+        "tpconv_dense_workspace_bytes": (sz, [vp, i64]),
+        "tpconv_gated_backward": (i32, [vp, i64] + [vp] * 12 + [sz, vp]),
+        "tpconv_linear_backward": (i32, [vp, i64] + [vp] * 10 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(_lib, name)
@@ -407,3 +455,359 @@ def tpconv_dropout_backward(irreps: str, p: float, seed: int, offset: int, grad_
     _check(_lib.tpconv_dropout_backward(irreps.encode(), code, grad_out.shape[0], grad_out.shape[1], float(p), int(seed),
                                         int(offset), _ptr(grad_out), _ptr(grad_x), _stream_handle(stream)))
     return grad_x
+
+
+# ----------------------------------------------------------------------- norm
+def _dtype_code(dtype):
+    return {"f32": F32, "f64": F64, torch.float32: F32, torch.float64: F64, F32: F32, F64: F64}.get(dtype, dtype)
+
+
+# The calls below launch on the current device, where all of their tensors have to be.
+def _here(t, shape, dtype, name):
+    _need(t, shape, dtype, name)
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return t
+
+
+def _scratch(need: int, workspace, device):
+    """(pointer, bytes) of the workspace given, or of one made for the call."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    _need_bytes(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+class PackedRows:
+    """fp32 irreps rows in 8 bits: codes uint8 [n, dim] (e4m3) and scales float32 [n, segments]."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.codes, self.scales = codes, scales
+
+
+def _packed_here(packed: PackedRows, n: int, dim: int, n_segments: int):
+    _here(packed.codes, (n, dim), torch.uint8, "codes")
+    _here(packed.scales, (n, n_segments), torch.float32, "scales")
+    return packed
+
+
+class NormPlan:
+    """Owns a tpconv_norm_t; sizes as attributes."""
+
+    def __init__(self, handle: ctypes.c_void_p):
+        self.handle = handle
+        info = tpconv_norm_query(self)
+        self.info = info
+        for f, _ in NormInfo._fields_:
+            setattr(self, f, getattr(info, f))
+        self.torch_dtype = _DTYPE[info.dtype]
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:
+            _lib.tpconv_norm_destroy(h)
+
+
+def tpconv_norm_plan(irreps: str, scope: str = "segment", eps: float = 1e-6, dtype="f32") -> NormPlan:
+    """Root-mean-square norm of irreps rows; scope: what is normalised together, each "segment" by itself or the whole
+    "row" (its segments counted alike)."""
+    if scope not in _SCOPES:
+        raise ValueError(f"scope must be 'segment' or 'row', got {scope!r}")
+    h = ctypes.c_void_p()
+    _check(_lib.tpconv_norm_plan(irreps.encode(), _SCOPES[scope], float(eps), int(_dtype_code(dtype)),
+                                 ctypes.byref(h)))
+    return NormPlan(h)
+
+
+def tpconv_norm_query(plan: NormPlan) -> NormInfo:
+    info = NormInfo()
+    _check(_lib.tpconv_norm_query(plan.handle, ctypes.byref(info)))
+    return info
+
+
+def tpconv_norm_destroy(plan: NormPlan) -> None:
+    plan.__del__()
+
+
+def tpconv_norm_workspace_bytes(plan: NormPlan, n_rows: int) -> int:
+    return int(_lib.tpconv_norm_workspace_bytes(plan.handle, int(n_rows)))
+
+
+@_on_launch_stream
+def tpconv_norm_forward(plan: NormPlan, x, residual=None, gamma=None, out=None, sum=None, packed=None,
+                        need=(True, True, False), stream=None):
+    """(out, sum, packed): the norm of h = x + residual times gamma [channels], h itself (x, where there is no
+    residual and no `sum` to write it to), and the norm in 8 bits; an output is None when `need` turns it off.  sum may
+    be x or residual itself, or out may."""
+    n, dt = x.shape[0], plan.torch_dtype
+    shape = (n, plan.dim)
+    _here(x, shape, dt, "x")
+    if residual is not None:
+        _here(residual, shape, dt, "residual")
+    if gamma is not None:
+        _here(gamma, (plan.channels,), dt, "gamma")
+    if need[0] and out is None:
+        out = torch.empty_like(x)
+    if need[1] and sum is None and residual is not None:
+        sum = torch.empty_like(x)
+    if need[2] and packed is None:
+        packed = PackedRows(torch.empty(shape, dtype=torch.uint8, device=x.device),
+                            torch.empty((n, plan.n_segments), dtype=torch.float32, device=x.device))
+    if out is not None:
+        _here(out, shape, dt, "out")
+    if sum is not None:
+        _here(sum, shape, dt, "sum")
+    if packed is not None:
+        _packed_here(packed, n, plan.dim, plan.n_segments)
+    if out is not None or sum is not None or packed is not None:
+        _check(_lib.tpconv_norm_forward(plan.handle, n, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum), _ptr(out),
+                                        None if packed is None else packed.codes.data_ptr(),
+                                        None if packed is None else packed.scales.data_ptr(),
+                                        _stream_handle(stream)))
+    return out, x if sum is None and need[1] else sum, packed
+
+
+@_on_launch_stream
+def tpconv_norm_backward(plan: NormPlan, h, gamma, grad_out, grad_sum=None, grad_x=None, grad_gamma=None,
+                         need=(True, True), workspace=None,
+                         stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(grad_x, grad_gamma) of <grad_out, out> + <grad_sum, sum> for the forward's sum h; grad_x is x's and the
+    residual's alike.  An output is None when `need` turns it off.  grad_x may be h, grad_out or grad_sum itself."""
+    n, dt = h.shape[0], plan.torch_dtype
+    shape = (n, plan.dim)
+    _here(h, shape, dt, "h")
+    _here(grad_out, shape, dt, "grad_out")
+    if gamma is not None:
+        _here(gamma, (plan.channels,), dt, "gamma")
+    if grad_sum is not None:
+        _here(grad_sum, shape, dt, "grad_sum")
+    if need[0] and grad_x is None:
+        grad_x = torch.empty_like(h)
+    if need[1] and grad_gamma is None:
+        grad_gamma = h.new_empty(plan.channels)
+    if grad_x is not None:
+        _here(grad_x, shape, dt, "grad_x")
+    held = 0
+    if grad_gamma is not None:
+        _here(grad_gamma, (plan.channels,), dt, "grad_gamma")
+        workspace, held = _scratch(int(_lib.tpconv_norm_workspace_bytes(plan.handle, n)), workspace, h.device)
+    _check(_lib.tpconv_norm_backward(plan.handle, n, _ptr(h), _ptr(gamma), _ptr(grad_out), _ptr(grad_sum),
+                                     _ptr(grad_x), _ptr(grad_gamma), _ptr(workspace), held, _stream_handle(stream)))
+    return grad_x, grad_gamma
+
+
+def _segments_of(irreps: str) -> int:
+    return irreps.count("+") + 1
+
+
+@_on_launch_stream
+def tpconv_pack8(irreps: str, x, packed: Optional[PackedRows] = None, stream=None) -> PackedRows:
+    """fp32 irreps rows [n, dim] in 8 bits, with a scale for each row and segment."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    _here(x, x.shape, torch.float32, "x")
+    n, dim = x.shape
+    if packed is None:
+        packed = PackedRows(torch.empty((n, dim), dtype=torch.uint8, device=x.device),
+                            torch.empty((n, _segments_of(irreps)), dtype=torch.float32, device=x.device))
+    _packed_here(packed, n, dim, _segments_of(irreps))
+    _check(_lib.tpconv_pack8(irreps.encode(), n, dim, _ptr(x), _ptr(packed.codes), _ptr(packed.scales),
+                             _stream_handle(stream)))
+    return packed
+
+
+@_on_launch_stream
+def tpconv_unpack8(irreps: str, packed: PackedRows, out=None, stream=None) -> torch.Tensor:
+    """The rows that `packed` stands for [n, dim]: code times scale."""
+    if packed.codes.dim() != 2:
+        raise ValueError("codes must be 2-D")
+    n, dim = packed.codes.shape
+    _packed_here(packed, n, dim, _segments_of(irreps))
+    if out is None:
+        out = torch.empty((n, dim), dtype=torch.float32, device=packed.codes.device)
+    _here(out, (n, dim), torch.float32, "out")
+    _check(_lib.tpconv_unpack8(irreps.encode(), n, dim, _ptr(packed.codes), _ptr(packed.scales), _ptr(out),
+                               _stream_handle(stream)))
+    return out
+
+
+# ----------------------------------------------------------- gated and linear
+class DensePlan:
+    """Owns a tpconv_dense_t (a gated or a linear map's plan); sizes as attributes."""
+
+    def __init__(self, handle: ctypes.c_void_p):
+        self.handle = handle
+        info = tpconv_dense_query(self)
+        self.info = info
+        for f, _ in DenseInfo._fields_:
+            setattr(self, f, getattr(info, f))
+        self.torch_dtype = _DTYPE[info.dtype]
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:
+            _lib.tpconv_dense_destroy(h)
+
+
+def _activation(name, what):
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"{what} must be one of {', '.join(_ACTIVATIONS)}; got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def tpconv_gated_plan(irreps_in: str, irreps_out: str, scalar_act: str = "silu", gate_act: str = "sigmoid",
+                      dtype="f32") -> DensePlan:
+    """Gated feed-forward product; scalar_act acts on the gates of irreps_out's even scalars, gate_act on the other
+    channels' gates."""
+    h = ctypes.c_void_p()
+    _check(_lib.tpconv_gated_plan(irreps_in.encode(), irreps_out.encode(), _activation(scalar_act, "scalar_act"),
+                                  _activation(gate_act, "gate_act"), int(_dtype_code(dtype)), ctypes.byref(h)))
+    return DensePlan(h)
+
+
+def tpconv_linear_plan(irreps_in: str, irreps_out: str, act: str = "identity", dtype="f32") -> DensePlan:
+    """Equivariant linear map; act acts on irreps_out's even scalars."""
+    h = ctypes.c_void_p()
+    _check(_lib.tpconv_linear_plan(irreps_in.encode(), irreps_out.encode(), _activation(act, "act"),
+                                   int(_dtype_code(dtype)), ctypes.byref(h)))
+    return DensePlan(h)
+
+
+def tpconv_dense_query(plan: DensePlan) -> DenseInfo:
+    info = DenseInfo()
+    _check(_lib.tpconv_dense_query(plan.handle, ctypes.byref(info)))
+    return info
+
+
+def tpconv_dense_maps(plan: DensePlan):
+    """List of (segment of irreps_in, segment of irreps_out, l, weight offset)."""
+    buf = (ctypes.c_int64 * (4 * plan.n_maps))()
+    _check(_lib.tpconv_dense_maps(plan.handle, buf))
+    return [tuple(buf[4 * i:4 * i + 4]) for i in range(plan.n_maps)]
+
+
+def tpconv_dense_destroy(plan: DensePlan) -> None:
+    plan.__del__()
+
+
+def tpconv_dense_workspace_bytes(plan: DensePlan, n_rows: int) -> int:
+    return int(_lib.tpconv_dense_workspace_bytes(plan.handle, int(n_rows)))
+
+
+@_on_launch_stream
+def tpconv_gated_forward(plan: DensePlan, x, weights, gate_weights, gate_bias=None, out=None,
+                         stream=None) -> torch.Tensor:
+    """out [n, dim_out]: the maps' products of x [n, dim_in], each channel times the activation of its gate, a
+    product of x's even scalars.  weights [weight_numel], gate_weights [n_scalars, n_gates], gate_bias [n_gates]."""
+    n, dt = x.shape[0], plan.torch_dtype
+    _here(x, (n, plan.dim_in), dt, "x")
+    _here(weights, (plan.weight_numel,), dt, "weights")
+    _here(gate_weights, (plan.n_scalars, plan.n_gates), dt, "gate_weights")
+    if gate_bias is not None:
+        _here(gate_bias, (plan.n_gates,), dt, "gate_bias")
+    if out is None:
+        out = x.new_empty((n, plan.dim_out))
+    _here(out, (n, plan.dim_out), dt, "out")
+    _check(_lib.tpconv_gated_forward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(gate_weights), _ptr(gate_bias),
+                                     _ptr(out), _stream_handle(stream)))
+    return out
+
+
+@_on_launch_stream
+def tpconv_linear_forward(plan: DensePlan, x, weights, bias=None, residual=None, out=None,
+                          stream=None) -> torch.Tensor:
+    """out [n, dim_out] = residual + the maps' products of x [n, dim_in], with bias [n_bias] and the activation on the
+    even scalars.  weights [weight_numel]; out may be residual itself."""
+    n, dt = x.shape[0], plan.torch_dtype
+    _here(x, (n, plan.dim_in), dt, "x")
+    _here(weights, (plan.weight_numel,), dt, "weights")
+    if bias is not None:
+        _here(bias, (plan.n_bias,), dt, "bias")
+    if residual is not None:
+        _here(residual, (n, plan.dim_out), dt, "residual")
+    if out is None:
+        out = x.new_empty((n, plan.dim_out))
+    _here(out, (n, plan.dim_out), dt, "out")
+    _check(_lib.tpconv_linear_forward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(bias), _ptr(residual), _ptr(out),
+                                      _stream_handle(stream)))
+    return out
+
+
+def _input(plan: DensePlan, x, n: int):
+    """Pointers to x, its codes and its scales, of rows or of PackedRows."""
+    if isinstance(x, PackedRows):
+        _packed_here(x, n, plan.dim_in, plan.n_segments_in)
+        return None, x.codes.data_ptr(), x.scales.data_ptr()
+    _here(x, (n, plan.dim_in), plan.torch_dtype, "x")
+    return x.data_ptr(), None, None
+
+
+@_on_launch_stream
+def tpconv_gated_backward(plan: DensePlan, x, weights, gate_weights, gate_bias, grad_out, grad_x=None,
+                          grad_weights=None, grad_gate_weights=None, grad_gate_bias=None, need=(True, True, True, None),
+                          workspace=None, stream=None) -> Tuple[Optional[torch.Tensor], ...]:
+    """(grad_x, grad_weights, grad_gate_weights[, grad_gate_bias]) of <grad_out, tpconv_gated_forward(...)>.  x: the
+    forward's rows, or PackedRows of them (the gradients at the restored rows).  An output is None when `need` turns it
+    off; the bias's is there where gate_bias is, or where `need` asks for it."""
+    n, dt, dev = grad_out.shape[0], plan.torch_dtype, grad_out.device
+    _here(grad_out, (n, plan.dim_out), dt, "grad_out")
+    rows, codes, scales = _input(plan, x, n)
+    _here(weights, (plan.weight_numel,), dt, "weights")
+    _here(gate_weights, (plan.n_scalars, plan.n_gates), dt, "gate_weights")
+    if gate_bias is not None:
+        _here(gate_bias, (plan.n_gates,), dt, "gate_bias")
+    with_bias = gate_bias is not None if need[3] is None else need[3]
+    if need[0] and grad_x is None:
+        grad_x = torch.empty((n, plan.dim_in), dtype=dt, device=dev)
+    if need[1] and grad_weights is None:
+        grad_weights = torch.empty_like(weights)
+    if need[2] and grad_gate_weights is None:
+        grad_gate_weights = torch.empty_like(gate_weights)
+    if with_bias and grad_gate_bias is None:
+        grad_gate_bias = torch.empty(plan.n_gates, dtype=dt, device=dev)
+    for t, shp, nm in ((grad_x, (n, plan.dim_in), "grad_x"), (grad_weights, (plan.weight_numel,), "grad_weights"),
+                       (grad_gate_weights, (plan.n_scalars, plan.n_gates), "grad_gate_weights"),
+                       (grad_gate_bias, (plan.n_gates,), "grad_gate_bias")):
+        if t is not None:
+            _here(t, shp, dt, nm)
+    workspace, held = _scratch(int(_lib.tpconv_dense_workspace_bytes(plan.handle, n)), workspace, dev)
+    _check(_lib.tpconv_gated_backward(plan.handle, n, rows, codes, scales, _ptr(weights), _ptr(gate_weights),
+                                      _ptr(gate_bias), _ptr(grad_out), _ptr(grad_x), _ptr(grad_weights),
+                                      _ptr(grad_gate_weights), _ptr(grad_gate_bias), _ptr(workspace), held,
+                                      _stream_handle(stream)))
+    got = (grad_x, grad_weights, grad_gate_weights)
+    return got + (grad_gate_bias,) if with_bias or grad_gate_bias is not None else got
+
+
+@_on_launch_stream
+def tpconv_linear_backward(plan: DensePlan, x, weights, bias, grad_out, grad_x=None, grad_weights=None, grad_bias=None,
+                           need=(True, True, None), workspace=None, stream=None) -> Tuple[Optional[torch.Tensor], ...]:
+    """(grad_x, grad_weights[, grad_bias]) of <grad_out, tpconv_linear_forward(...)> (the residual's is grad_out).  x:
+    the forward's rows, or PackedRows of them; with the identity as activation grad_x alone may be asked for without
+    x (None).  An output is None when `need` turns it off; the bias's is there where bias is, or where `need` asks for
+    it."""
+    n, dt, dev = grad_out.shape[0], plan.torch_dtype, grad_out.device
+    _here(grad_out, (n, plan.dim_out), dt, "grad_out")
+    rows, codes, scales = (None, None, None) if x is None else _input(plan, x, n)
+    _here(weights, (plan.weight_numel,), dt, "weights")
+    if bias is not None:
+        _here(bias, (plan.n_bias,), dt, "bias")
+    with_bias = bias is not None if need[2] is None else need[2]
+    if need[0] and grad_x is None:
+        grad_x = torch.empty((n, plan.dim_in), dtype=dt, device=dev)
+    if need[1] and grad_weights is None:
+        grad_weights = torch.empty_like(weights)
+    if with_bias and grad_bias is None:
+        grad_bias = torch.empty(plan.n_bias, dtype=dt, device=dev)
+    for t, shp, nm in ((grad_x, (n, plan.dim_in), "grad_x"), (grad_weights, (plan.weight_numel,), "grad_weights"),
+                       (grad_bias, (plan.n_bias,), "grad_bias")):
+        if t is not None:
+            _here(t, shp, dt, nm)
+    workspace, held = _scratch(int(_lib.tpconv_dense_workspace_bytes(plan.handle, n)), workspace, dev)
+    _check(_lib.tpconv_linear_backward(plan.handle, n, rows, codes, scales, _ptr(weights), _ptr(bias), _ptr(grad_out),
+                                       _ptr(grad_x), _ptr(grad_weights), _ptr(grad_bias), _ptr(workspace), held,
+                                       _stream_handle(stream)))
+    got = (grad_x, grad_weights)
+    return got + (grad_bias,) if with_bias or grad_bias is not None else got

@@ -1,13 +1,18 @@
 /*
  * tpconv_node.h -- C ABI of libtpconv.so's node operators: what a
- * mixture-of-experts potential runs on its atoms around the convolution of
- * tpconv.h.
+ * mixture-of-experts potential, or one with a feed-forward block, runs on its
+ * atoms around the convolution of tpconv.h.
  *
  *   embedding   species -> the first node features, and the table's gradient
  *   routing     each atom's router logits -> top_k experts and their gates
  *   experts     equivariant linear maps on irreps rows, one set per expert,
  *               summed over an atom's experts with its gates
  *   dropout     on irreps rows, equivariant, from a counter-based generator
+ *   norm        root-mean-square norm of irreps rows, with the sum with the
+ *               residual stream before it and an output in 8 bits beside it
+ *   8 bits      rows kept in 8 bits until a gradient needs them
+ *   gated       feed-forward product: two projections, activation, product
+ *   linear      equivariant linear map with bias, activation and residual
  *
  * The pages behind this library name mixture-of-experts potentials (MatRIS-
  * MoE and the Janus system; UMA in the TrimSO(2) abstract) and print no
@@ -225,6 +230,171 @@ tpconv_status tpconv_dropout_forward(const char* irreps, tpconv_dtype dtype, int
 tpconv_status tpconv_dropout_backward(const char* irreps, tpconv_dtype dtype, int64_t n_rows, int64_t dim, double p,
                                       uint64_t seed, uint64_t offset, const void* grad_out, void* grad_x,
                                       hipStream_t stream);
+
+/* ------------------------------------------------------------------- norm --
+ * h = x + residual (residual NULL: h = x), and y the norm of h: with a segment's
+ * mean square ms_s = mean over its mul (2l+1) columns of h^2,
+ *   scope TPCONV_NORM_SEGMENT: r = 1 / sqrt(ms_s + eps), each segment by itself;
+ *   scope TPCONV_NORM_ROW:     r = 1 / sqrt(mean over the segments of ms_s + eps),
+ *                              one factor for the row, each segment counted alike;
+ *   y[s][u][m] = gamma[c(s, u)] r h[s][u][m],
+ * gamma a factor for each channel, channels counted over all segments (NULL:
+ * ones).  Equivariant.  A padding row of zeros has y = 0.  Sums, and what is
+ * formed of them, are held in 64 bits for both types, so squares of any F32
+ * value fit (those of F64 values have to).  Infinities and NaN stay in their
+ * row (scope segment: in their segment).
+ *
+ * 8 bits: a row and segment have one fp32 scale, max(2^-126, c a) with a the
+ * largest magnitude in it and c the fp32 number next to 1/448; a value v is
+ * held as the e4m3 code (OCP, 1-4-3 bits, largest 448) nearest to the fp32
+ * product v i, ties to the even code, i the fp32 number next to 1/scale; it is
+ * restored as code times scale, at most a/28 off.  A segment with an infinity
+ * or NaN is restored as NaN. */
+#define TPCONV_MAX_NORM_DIM 8192
+
+typedef enum { TPCONV_NORM_SEGMENT = 0, TPCONV_NORM_ROW = 1 } tpconv_norm_scope;
+
+typedef struct tpconv_norm_s* tpconv_norm_t;
+
+typedef struct {
+  int64_t dim;      /* row width */
+  int64_t channels; /* of all segments */
+  int32_t n_segments, scope, dtype, reserved;
+  double eps;
+} tpconv_norm_info;
+
+/* tpconv_norm_plan: host only.  irreps as for tpconv_dropout_forward (any mul,
+ * repeated (l, parity) too), at most 32 segments and TPCONV_MAX_NORM_DIM
+ * columns; eps finite and above 0.  Errors: TPCONV_E_INVALID_ARG,
+ * TPCONV_E_IRREPS, TPCONV_E_UNSUPPORTED. */
+tpconv_status tpconv_norm_plan(const char* irreps, int scope, double eps, tpconv_dtype dtype, tpconv_norm_t* out);
+tpconv_status tpconv_norm_query(tpconv_norm_t plan, tpconv_norm_info* info);
+void tpconv_norm_destroy(tpconv_norm_t plan);
+
+/* tpconv_norm_forward: x, residual [n_rows][dim] -> sum (h), out (y) [n_rows]
+ * [dim], codes [n_rows][dim] and scales [n_rows][n_segments] (y in 8 bits; F32
+ * plans; both or neither).  Of sum, out and codes those that are NULL are left
+ * out, but one has to be asked for.  sum may be x or residual itself, or out
+ * may; no other overlap.  Errors: TPCONV_E_INVALID_ARG (codes without scales or
+ * with an F64 plan, NULL x, no output), TPCONV_E_HIP. */
+tpconv_status tpconv_norm_forward(tpconv_norm_t plan, int64_t n_rows, const void* x, const void* residual,
+                                  const void* gamma, void* sum, void* out, uint8_t* codes, float* scales,
+                                  hipStream_t stream);
+
+/* tpconv_norm_backward: gradients of <grad_out, y> + <grad_sum, h> for the
+ * forward's h (grad_sum NULL: without its term):
+ *   grad_x [n_rows][dim], x's and the residual's alike; with u = r h, w = gamma
+ *     grad_out and k_j = 1/columns of j's segment (scope row: over n_segments),
+ *     r (w_j - k_j u_j sum_i w_i u_i) + grad_sum_j, the sum over what is
+ *     normalised together;
+ *   grad_gamma [channels], the sum over rows and components of grad_out u.
+ * Each is overwritten; NULL skips one.  grad_x may be h, grad_out or grad_sum
+ * itself; no other overlap.  workspace: caller-owned, 256-byte aligned,
+ * at least tpconv_norm_workspace_bytes (0 for bad sizes), needed for
+ * grad_gamma; holds nothing between calls.  Errors: TPCONV_E_INVALID_ARG,
+ * TPCONV_E_WORKSPACE, TPCONV_E_HIP. */
+size_t tpconv_norm_workspace_bytes(tpconv_norm_t plan, int64_t n_rows);
+tpconv_status tpconv_norm_backward(tpconv_norm_t plan, int64_t n_rows, const void* h, const void* gamma,
+                                   const void* grad_out, const void* grad_sum, void* grad_x, void* grad_gamma,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* tpconv_pack8: F32 rows x [n_rows][dim] into codes [n_rows][dim] and scales
+ * [n_rows][segments of irreps], as above; tpconv_unpack8: back.  irreps and dim
+ * as for tpconv_norm_plan and tpconv_dropout_forward.  For rows that a gradient
+ * needs again: a quarter of the memory until then (tpconv_gated_backward and
+ * tpconv_linear_backward read the codes themselves).  Errors:
+ * TPCONV_E_INVALID_ARG, TPCONV_E_IRREPS, TPCONV_E_UNSUPPORTED, TPCONV_E_HIP. */
+tpconv_status tpconv_pack8(const char* irreps, int64_t n_rows, int64_t dim, const float* x, uint8_t* codes,
+                           float* scales, hipStream_t stream);
+tpconv_status tpconv_unpack8(const char* irreps, int64_t n_rows, int64_t dim, const uint8_t* codes,
+                             const float* scales, float* x, hipStream_t stream);
+
+/* ------------------------------------------------------- gated and linear --
+ * Both take irreps rows x [n_rows][dim_in] to rows [n_rows][dim_out] by a map
+ * M_s [mul_in][mul_out] for every pair of equal (l, parity) segments, maps in
+ * the order of irreps_in's segments, together weights [weight_numel] (the
+ * segments' rules are those of tpconv_experts_plan, but mul up to
+ * TPCONV_MAX_DENSE_MUL).  Every segment of irreps_out needs its partner; columns
+ * of an input segment without one are not read, and their gradient is 0.
+ *
+ * gated:  z = x_0e Wg + b, one gate for each channel of irreps_out (n_gates of
+ *         them), from the even scalars x_0e, which irreps_in has to have;
+ *         out[s][v][m] = a_s(z[c(s, v)]) sum_u M_s[u][v] x[s][u][m],
+ *         a_s the activation scalar_act for the segment 0e, gate_act for others.
+ *         Rows of 0e alone: the gated unit of a feed-forward layer.
+ *         gate_weights [mul of 0e][n_gates], gate_bias [n_gates] or NULL.
+ * linear: out[s] = residual[s] + M_s x[s], and for 0e residual + a(M x + bias);
+ *         bias [mul of irreps_out's 0e] or NULL, residual [n_rows][dim_out] or
+ *         NULL.
+ * Activations: identity z, silu z/(1+e^-z), sigmoid 1/(1+e^-z), tanh, gelu
+ * z Phi(z) (the exact one).  Products and sums are held in the data type.
+ * Infinities and NaN in a row stay in that row (in the parameters' gradients
+ * they do not); those of the formulas at infinite z are not taken to limits. */
+#define TPCONV_MAX_DENSE_MUL 1024
+
+typedef enum {
+  TPCONV_ACT_IDENTITY = 0,
+  TPCONV_ACT_SILU = 1,
+  TPCONV_ACT_SIGMOID = 2,
+  TPCONV_ACT_TANH = 3,
+  TPCONV_ACT_GELU = 4
+} tpconv_activation;
+
+typedef struct tpconv_dense_s* tpconv_dense_t;
+
+typedef struct {
+  int64_t dim_in, dim_out; /* row widths */
+  int64_t weight_numel;    /* of all maps */
+  int64_t n_maps;
+  int64_t n_gates;         /* gated: channels of irreps_out; linear: 0 */
+  int64_t n_scalars;       /* gated: mul of irreps_in's 0e, rows of gate_weights; linear: 0 */
+  int64_t n_bias;          /* gated: n_gates; linear: mul of irreps_out's 0e */
+  int32_t n_segments_in;   /* a row's scales where x is in 8 bits */
+  int32_t dtype;
+} tpconv_dense_info;
+
+/* Plans, host only.  Errors: TPCONV_E_INVALID_ARG (unknown activation),
+ * TPCONV_E_IRREPS, TPCONV_E_UNSUPPORTED, TPCONV_E_NO_PATHS (a segment of
+ * irreps_out without a partner; gated: no 0e in irreps_in).  A plan of one kind
+ * is refused by the other kind's calls. */
+tpconv_status tpconv_gated_plan(const char* irreps_in, const char* irreps_out, int scalar_act, int gate_act,
+                                tpconv_dtype dtype, tpconv_dense_t* out);
+tpconv_status tpconv_linear_plan(const char* irreps_in, const char* irreps_out, int act, tpconv_dtype dtype,
+                                 tpconv_dense_t* out);
+tpconv_status tpconv_dense_query(tpconv_dense_t plan, tpconv_dense_info* info);
+/* Map list, host buffer of n_maps*4 int64: segment of irreps_in, segment of
+ * irreps_out, l, weight offset. */
+tpconv_status tpconv_dense_maps(tpconv_dense_t plan, int64_t* maps);
+void tpconv_dense_destroy(tpconv_dense_t plan);
+
+/* out is overwritten; the linear map's may be its residual itself, no other
+ * overlap.  Errors: TPCONV_E_INVALID_ARG (another kind's plan, NULL where it is
+ * needed), TPCONV_E_HIP. */
+tpconv_status tpconv_gated_forward(tpconv_dense_t plan, int64_t n_rows, const void* x, const void* weights,
+                                   const void* gate_weights, const void* gate_bias, void* out, hipStream_t stream);
+tpconv_status tpconv_linear_forward(tpconv_dense_t plan, int64_t n_rows, const void* x, const void* weights,
+                                    const void* bias, const void* residual, void* out, hipStream_t stream);
+
+/* Gradients of <grad_out, out> (the linear map's residual's is grad_out).  They
+ * take the forward's x, or codes and scales of it (F32; x NULL), and then are
+ * the formulas' gradients at the restored rows; nothing else is kept from the
+ * forward, gates and products are formed again.  Each output is overwritten;
+ * NULL skips one.  The linear map's grad_x reads no x, and may be asked for
+ * without it, where its activation is the identity.  workspace: caller-owned, 256-byte aligned, at least
+ * tpconv_dense_workspace_bytes (0 for bad sizes; gated: the rows of grad_out
+ * and of its gates, and parts of the parameters' gradients, at most some 20 MB
+ * or the parameters themselves); holds nothing between calls.  Errors: as the
+ * forward, TPCONV_E_WORKSPACE. */
+size_t tpconv_dense_workspace_bytes(tpconv_dense_t plan, int64_t n_rows);
+tpconv_status tpconv_gated_backward(tpconv_dense_t plan, int64_t n_rows, const void* x, const uint8_t* codes,
+                                    const float* scales, const void* weights, const void* gate_weights,
+                                    const void* gate_bias, const void* grad_out, void* grad_x, void* grad_weights,
+                                    void* grad_gate_weights, void* grad_gate_bias, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+tpconv_status tpconv_linear_backward(tpconv_dense_t plan, int64_t n_rows, const void* x, const uint8_t* codes,
+                                     const float* scales, const void* weights, const void* bias,
+                                     const void* grad_out, void* grad_x, void* grad_weights, void* grad_bias,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

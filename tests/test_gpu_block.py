@@ -1,0 +1,816 @@
+"""GPU parity of the feed-forward block's operators (norm, rows in 8 bits, gated
+and linear maps) against the fp64 oracle (oracle/block.py), through the Python
+binding.
+
+Bounds, entry by entry, with eps the unit roundoff of the data type (2^-24,
+2^-53).  A sum of n products errs by at most (n + 4) eps times the same sum of
+absolute values, in whatever order it is taken.
+
+Norm: the oracle is given the kernel's own sum h (which is checked bit by bit).
+Sums over h and what is formed of them run in 64 bits, where a sum over `width`
+columns errs by at most (width + 32) 2^-53 of its absolute values with the few
+steps after it; an fp32 result rounds that once, and gamma's or grad_sum's part
+once more.
+
+Activations: with L and B the bounds of an activation's and its slope's growth
+(oracle.block), an argument with error d gives L d and B d, and the evaluation
+itself at most 16 eps (1 + |z|): exp, erfc and tanh are within 4 units, their
+arguments' rounding times z and the few roundings around them make up the rest.
+"""
+
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import block as ob
+from oracle.node import segments
+from test_gpu_node import EPS, NP, dev, node, within  # noqa: F401  (node is a fixture)
+
+pytestmark = pytest.mark.gpu
+# 1.02 for the bounds' products of two errors; in fp64 the oracle, which computes in 64 bits too, errs by as much as
+# the kernel may, so the two differ by up to twice the bound
+TOL = {"f32": 1.02, "f64": 2.04}
+
+
+def log(msg):
+    print(msg, file=sys.stderr, flush=True)
+
+
+def host(t):
+    return t.cpu().numpy().astype(np.float64)
+
+
+def features(rng, irreps, n, dt, spread=1.0):
+    x = rng.standard_normal((n, segments(irreps)[1])) * np.exp(spread * rng.standard_normal((n, 1)))
+    if n > 10:
+        x[n // 3] = 0                                          # a padding row
+    return x.astype(NP[dt])
+
+
+def shifted(a):
+    """On the device, contiguous, but one element off the alignment of an allocation."""
+    import torch
+    a = np.ascontiguousarray(a)
+    buf = torch.empty(a.size + 1, dtype=torch.from_numpy(a.reshape(-1)[:0]).dtype, device="cuda")
+    view = buf[1:].view(a.shape)
+    view.copy_(torch.from_numpy(a))
+    return view
+
+
+# ----------------------------------------------------------------------- norm
+NORM_ROWS = ["1x0e", "2x0e", "1x1o", "4x0e+4x1o", "3x0e+1x1o+2x2e", "16x0e+16x1o+16x2e+16x3o+16x4e",
+             "32x0e+32x1o+32x2e+32x3o", "64x0e+64x1o+64x2e+64x3o", "5x0e+1x0e+7x1o+3x1o+2x0o", "257x0e", "300x1o+7x2e",
+             "128x0e+128x1o+128x2e+128x3o", "1000x1o+1x0e", "1024x0e+1024x1o+800x2e", "8192x0e", "910x4e+2x0e",
+             "+".join(["8x0e+4x1o"] * 16)]
+
+
+def norm_bounds(irreps, scope, dt, h, gamma, G, H, eps):
+    """(bound of y relative to |y|, of grad_x, of grad_gamma's rows' terms)."""
+    segs = segments(irreps)[0]
+    e, width = EPS[dt], segments(irreps)[1]
+    of_r = 6 * e if dt == "f32" else (width + len(segs) + 12) * e
+    size = ob.norm_backward(irreps, scope, eps, h, gamma, G, H, size=True)
+    grad = (4 * of_r + (0 if dt == "f32" else (width + 8) * e)) * size[0]
+    if dt == "f32":
+        exact = ob.norm_backward(irreps, scope, eps, h, gamma, G, H)[0]
+        plain = exact - (0 if H is None else H)
+        grad = 3 * e * (np.abs(exact) + np.abs(plain)) + (width + 32) * 2.0 ** -53 * size[0]
+    return of_r, grad, (len(h) * max(2 * s[1] + 1 for s in segs) + 4) * e * size[1] + of_r * size[1]
+
+
+def check_norm(node, dt, irreps, scope, n, residual=True, weighted=True, place=dev, spread=1.0):  # noqa: F811
+    import torch
+    rng = np.random.default_rng([n, len(irreps), scope == "row"])
+    x, res = features(rng, irreps, n, dt, spread), features(rng, irreps, n, dt, spread)
+    G, H = features(rng, irreps, n, dt), features(rng, irreps, n, dt)
+    C = ob.channels(irreps)[1]
+    gamma = (1 + 0.3 * rng.standard_normal(C)).astype(NP[dt]) if weighted else None
+    plan = node.tpconv_norm_plan(irreps, scope=scope, eps=1e-6, dtype=dt)
+    xd, rd, gd = place(x), place(res) if residual else None, None if gamma is None else dev(gamma)
+    y, h, none = node.tpconv_norm_forward(plan, xd, rd, gd)
+    assert none is None
+    if residual:
+        assert torch.equal(h, xd + rd)
+    else:
+        assert h is xd
+    hh = host(h)
+    want, _ = ob.norm_forward(irreps, scope, 1e-6, hh, None, gamma)
+    of_r, of_grad, of_gamma = norm_bounds(irreps, scope, dt, hh, gamma, G, H if residual else None, 1e-6)
+    within(y, want, TOL[dt] * of_r * np.abs(want), "y")
+    Gd, Hd = place(G), place(H) if residual else None
+    gx, gg = node.tpconv_norm_backward(plan, h, gd, Gd, Hd)
+    want = ob.norm_backward(irreps, scope, 1e-6, hh, gamma, G, H if residual else None)
+    within(gx, want[0], TOL[dt] * of_grad, "grad_x")
+    within(gg, want[1], TOL[dt] * of_gamma, "grad_gamma")
+    again = node.tpconv_norm_backward(plan, h, gd, Gd, Hd)
+    assert torch.equal(again[0], gx) and torch.equal(again[1], gg)
+    return plan, xd, rd, gd, y, h, Gd, Hd, gx, gg
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("scope", ["segment", "row"])
+@pytest.mark.parametrize("irreps", NORM_ROWS)
+def test_norm(node, dt, scope, irreps):  # noqa: F811
+    wide = segments(irreps)[1]
+    for n in (1, 17, 150) if wide > 512 else (1, 2, 5, 64, 1001):
+        log(f"[block] norm {dt} {scope} {irreps[:40]} n={n}")
+        check_norm(node, dt, irreps, scope, n, residual=n % 2 == 1, weighted=n != 2)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+def test_norm_of_many_rows(node, dt):  # noqa: F811
+    """More rows than one trip of the grid, of a row's every spread over lanes."""
+    for irreps, n in (("1x0e+1x1o", 300001), ("16x0e", 70001), ("32x0e+32x1o+32x2e+32x3o", 9001), ("500x1o", 2100)):
+        log(f"[block] norm {dt} {irreps} n={n}")
+        check_norm(node, dt, irreps, "segment", n)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+def test_norm_off_alignment(node, dt):  # noqa: F811
+    for irreps in ("64x0e+64x1o", "300x1o+4x0e", "1024x0e+1024x1o"):
+        log(f"[block] norm {dt} {irreps} off the alignment")
+        check_norm(node, dt, irreps, "segment", 33, place=shifted)
+
+
+def test_norm_extremes(node):  # noqa: F811
+    """Squares that fp32 does not hold, rows far below eps, rows of zeros, segments of one column, where the gradient
+    is what eps leaves of it."""
+    for scale in (1e30, 3e38 / 60, 1e-20, 1e-30):
+        rng = np.random.default_rng(3)
+        irreps, n = "1x0e+6x0e+3x1o", 20
+        x = (scale * rng.uniform(-3, 3, (n, segments(irreps)[1]))).astype(np.float32)
+        x[4] = 0
+        G = rng.standard_normal(x.shape).astype(np.float32)
+        for scope in ("segment", "row"):
+            log(f"[block] norm of rows about {scale} {scope}")
+            plan = node.tpconv_norm_plan(irreps, scope=scope, eps=1e-6)
+            y, h, _ = node.tpconv_norm_forward(plan, dev(x))
+            want, hh = ob.norm_forward(irreps, scope, 1e-6, x)
+            within(y, want, 6 * EPS["f32"] * np.abs(want) + 2.0 ** -149, "y")
+            assert not host(y)[4].any()
+            gx, gg = node.tpconv_norm_backward(plan, h, None, dev(G))
+            want = ob.norm_backward(irreps, scope, 1e-6, hh, None, G)
+            size = ob.norm_backward(irreps, scope, 1e-6, hh, None, G, size=True)
+            # the difference keeps what 64 bits leave of it
+            within(gx, want[0], 3 * EPS["f32"] * np.abs(want[0]) + 64 * 2.0 ** -53 * size[0] + 2.0 ** -149, "grad_x")
+            within(gg, want[1], (4 * n + 12) * EPS["f32"] * size[1], "grad_gamma")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_norm_keeps_not_numbers_in_their_row(node, dt, bad):  # noqa: F811
+    irreps = "8x0e+4x1o+300x0o"
+    rng = np.random.default_rng(4)
+    x, G = features(rng, irreps, 30, dt), features(rng, irreps, 30, dt)
+    spoiled = x.copy()
+    spoiled[7, 9] = bad                                        # 1o of row 7
+    for scope in ("segment", "row"):
+        plan = node.tpconv_norm_plan(irreps, scope=scope, dtype=dt)
+        clean, dirty = (node.tpconv_norm_forward(plan, dev(v))[0].cpu().numpy() for v in (x, spoiled))
+        gc, gd = (node.tpconv_norm_backward(plan, dev(v), None, dev(G), need=(True, False))[0].cpu().numpy()
+                  for v in (x, spoiled))
+        reach = np.zeros(x.shape, bool)
+        reach[7, 8:20] = True
+        if scope == "row":
+            reach[7] = True
+        for a, b in ((clean, dirty), (gc, gd)):
+            assert np.array_equal(a[~reach], b[~reach])
+            assert np.isnan(b[7, 9])
+
+
+@pytest.mark.parametrize("irreps", ["4x0e+4x1o", "64x0e+64x1o+64x2e+64x3o", "1000x1o", "7x0e+3x1o"])
+def test_norm_in_place(node, irreps):  # noqa: F811
+    import torch
+    rng = np.random.default_rng(5)
+    x, res, G, H = (features(rng, irreps, 77, "f32") for _ in range(4))
+    plan = node.tpconv_norm_plan(irreps)
+    y, h, _ = node.tpconv_norm_forward(plan, dev(x), dev(res))
+    gx, gg = node.tpconv_norm_backward(plan, h, None, dev(G), dev(H))
+    xd, rd = dev(x), dev(res)
+    out, total, _ = node.tpconv_norm_forward(plan, xd, rd, sum=rd, out=xd)
+    assert out is xd and total is rd and torch.equal(out, y) and torch.equal(total, h)
+    xd = dev(x)
+    assert node.tpconv_norm_forward(plan, xd, dev(res), out=xd, need=(True, False, False))[1] is None
+    assert torch.equal(xd, y)
+    for which in range(3):
+        a = [h.clone(), dev(G), dev(H)]
+        got = node.tpconv_norm_backward(plan, a[0], None, a[1], a[2], grad_x=a[which])
+        assert torch.equal(a[which], gx) and torch.equal(got[1], gg)
+
+
+def test_norm_outputs_on_their_own(node):  # noqa: F811
+    import torch
+    irreps = "32x0e+32x1o"
+    rng = np.random.default_rng(6)
+    plan = node.tpconv_norm_plan(irreps)
+    x, res, gamma = dev(features(rng, irreps, 50, "f32")), dev(features(rng, irreps, 50, "f32")), None
+    y, h, p = node.tpconv_norm_forward(plan, x, res, gamma, need=(True, True, True))
+    for need in ((True, False, False), (False, True, False), (False, False, True), (False, True, True)):
+        got = node.tpconv_norm_forward(plan, x, res, gamma, need=need)
+        assert [g is not None for g in got] == list(need)
+        if need[0]:
+            assert torch.equal(got[0], y)
+        if need[1]:
+            assert torch.equal(got[1], h)
+        if need[2]:
+            assert torch.equal(got[2].codes, p.codes) and torch.equal(got[2].scales, p.scales)
+    assert node.tpconv_norm_forward(plan, x, need=(False, False, False)) == (None, None, None)
+    G = dev(features(rng, irreps, 50, "f32"))
+    gx, gg = node.tpconv_norm_backward(plan, h, None, G)
+    a, none = node.tpconv_norm_backward(plan, h, None, G, need=(True, False))
+    assert none is None and torch.equal(a, gx)
+    none, b = node.tpconv_norm_backward(plan, h, None, G, need=(False, True))
+    assert none is None and torch.equal(b, gg)
+
+
+def test_norm_without_rows(node):  # noqa: F811
+    import torch
+    for irreps in ("4x0e+4x1o", "700x1o"):
+        plan = node.tpconv_norm_plan(irreps)
+        x = torch.empty(0, plan.dim, device="cuda")
+        y, h, p = node.tpconv_norm_forward(plan, x, x, need=(True, True, True))
+        assert y.shape == x.shape and p.scales.shape == (0, plan.n_segments)
+        gx, gg = node.tpconv_norm_backward(plan, h, None, x, grad_gamma=torch.full((plan.channels,), 7.0, device="cuda"))
+        assert gx.shape == x.shape and not gg.any()
+
+
+# --------------------------------------------------------------------- 8 bits
+def same_bits(a, b):
+    return np.array_equal(a.view(np.uint8), b.view(np.uint8))
+
+
+@pytest.mark.parametrize("irreps", NORM_ROWS)
+def test_pack8(node, irreps):  # noqa: F811
+    """The same codes, scales and restored rows as the definition, bit by bit."""
+    rng = np.random.default_rng(7)
+    for n, place in ((1, dev), (37, dev), (37, shifted)):
+        log(f"[block] pack8 {irreps[:40]} n={n} {place.__name__}")
+        x = features(rng, irreps, n, "f32", spread=10.0)
+        p = node.tpconv_pack8(irreps, place(x))
+        codes, scales = ob.pack8(irreps, x)
+        assert same_bits(p.scales.cpu().numpy(), scales)
+        assert np.array_equal(p.codes.cpu().numpy(), codes)
+        out = place(np.zeros_like(x))
+        assert same_bits(node.tpconv_unpack8(irreps, p, out=out).cpu().numpy(), ob.unpack8(irreps, codes, scales))
+
+
+def test_pack8_of_special_values(node):  # noqa: F811
+    irreps = "8x0e+4x1o"
+    f = np.float32
+    x = np.zeros((12, 20), f)
+    x[0, :8] = [448, 447, 1, -448, 0.5, 2.0 ** -9, 2.0 ** -10, -0.0]
+    x[1, :8] = np.array([448, 2.0 ** -10, 2.0 ** -10 * 1.01, 3 * 2.0 ** -10, 232, 216, 248, 440], f)      # ties
+    x[2, 3], x[3, 9], x[4, 1], x[5, 19] = np.nan, np.inf, -np.inf, -np.nan
+    x[6, :] = 2.0 ** -149
+    x[7, :] = np.float32(1e-37)
+    x[8, :] = np.finfo(f).max
+    x[9, :] = -np.finfo(f).tiny
+    x[10, :8] = np.finfo(f).max * 2.0 ** -np.arange(8, dtype=f)
+    x[11, 0] = 1e-40
+    p = node.tpconv_pack8(irreps, dev(x))
+    codes, scales = ob.pack8(irreps, x)
+    got = p.scales.cpu().numpy()
+    nan = np.isnan(scales)
+    assert np.array_equal(np.isnan(got), nan) and same_bits(got[~nan], scales[~nan])
+    back = node.tpconv_unpack8(irreps, p).cpu().numpy()
+    want = ob.unpack8(irreps, codes, scales)
+    assert np.array_equal(back, want, equal_nan=True)
+    for row, cols in ((2, slice(0, 8)), (3, slice(8, 20)), (4, slice(0, 8)), (5, slice(8, 20))):
+        assert np.isnan(back[row, cols]).all()                 # a segment with no number in it
+        assert np.isfinite(np.delete(back[row], np.arange(20)[cols])).all()
+    live = ~np.isnan(want)
+    assert np.array_equal(p.codes.cpu().numpy()[live], codes[live])
+
+
+@pytest.mark.parametrize("irreps", ["4x0e+4x1o", "7x0e+3x1o", "64x0e+64x1o+64x2e+64x3o", "1000x1o+1x0e", "8192x0e"])
+@pytest.mark.parametrize("scope", ["segment", "row"])
+def test_norm_in_8_bits(node, irreps, scope):  # noqa: F811
+    """The norm's codes are those of the norm."""
+    import torch
+    rng = np.random.default_rng(8)
+    plan = node.tpconv_norm_plan(irreps, scope=scope)
+    x, res, gamma = (dev(features(rng, irreps, 41, "f32")), dev(features(rng, irreps, 41, "f32")),
+                     dev(rng.standard_normal(plan.channels).astype(np.float32)))
+    y, _, p = node.tpconv_norm_forward(plan, x, res, gamma, need=(True, True, True))
+    q = node.tpconv_pack8(irreps, y)
+    assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+
+
+# ----------------------------------------------------------- gated and linear
+def product_error(x, dx, M, e):
+    """(value's size, error) of rows x [.., K] with error dx times M."""
+    size = np.abs(x) @ np.abs(M)
+    return size, dx @ np.abs(M) + (M.shape[0] + 4) * e * size
+
+
+def apart(x, s):
+    """[n * (2l+1), mul]"""
+    return np.swapaxes(ob.part(x, s), 1, 2).reshape(-1, s[0])
+
+
+def together(y, s, n):
+    """[n * (2l+1), mul] into columns [n, mul * (2l+1)]."""
+    return np.swapaxes(y.reshape(n, 2 * s[1] + 1, -1), 1, 2).reshape(n, -1)
+
+
+def columns(s):
+    return slice(s[3], s[3] + s[0] * (2 * s[1] + 1))
+
+
+def gate_errors(dt, irr_in, irr_out, act, gate, x, Wg, b):
+    """For each segment of irr_out: activations, slopes, and their errors [n, mul]."""
+    e = EPS[dt]
+    x0 = apart(x, ob.even_scalars(irr_in))
+    z = ob.gates(irr_in, irr_out, x, Wg, b)
+    size, dz = product_error(x0, 0 * x0, Wg, e)
+    dz = dz + 2 * e * (size + (0 if b is None else np.abs(b)))
+    first = dict(zip([s[3] for s in segments(irr_out)[0]], ob.channels(irr_out)[0]))
+    out = {}
+    for t in segments(irr_out)[0]:
+        c = slice(first[t[3]], first[t[3]] + t[0])
+        kind = ob.kinds(irr_out, act, gate)[t[1], t[2]]
+        a, slope = ob.activation(kind, z[:, c])
+        own = 16 * e * (1 + np.abs(z[:, c]))
+        out[t[3]] = (c, a, slope, ob.GROWTH[kind] * dz[:, c] + own, ob.BEND[kind] * dz[:, c] + own)
+    return out
+
+
+def gated_bounds(dt, irr_in, irr_out, act, gate, x, W, Wg, b, G=None):
+    """Bounds of out, or with G of (grad_x, grad_weights, grad_gate_weights, grad_gate_bias)."""
+    e, n = EPS[dt], len(x)
+    x = x.astype(np.float64)
+    act_of = gate_errors(dt, irr_in, irr_out, act, gate, x, Wg, b)
+    out = np.zeros((n, segments(irr_out)[1]))
+    gx, gW = np.zeros(x.shape), np.zeros(len(W))
+    C = ob.channels(irr_out)[1]
+    dz, ddz = np.zeros((n, C)), np.zeros((n, C))
+    for s, t, at in ob.maps(irr_in, irr_out)[0]:
+        d, M = 2 * s[1] + 1, ob.matrix(W, s, t, at)
+        c, a, slope, da, ds = act_of[t[3]]
+        a, slope, da, ds = (np.repeat(v, d, 0) for v in (a, slope, da, ds))
+        xs = apart(x, s)
+        u = xs @ M
+        _, du = product_error(xs, 0 * xs, M, e)
+        out[:, columns(t)] = together(np.abs(a) * du + np.abs(u) * da + da * du + e * np.abs(a * u), t, n)
+        if G is None:
+            continue
+        g = apart(G.astype(np.float64), t)
+        v, dv = g * a, np.abs(g) * da + e * np.abs(g * a)
+        _, err = product_error(v, dv, M.T, e)
+        gx[:, columns(s)] += together(err, s, n)
+        gW[at:at + M.size] = (np.abs(xs).T @ dv + (n * d + 6) * e * (np.abs(xs).T @ np.abs(v))).reshape(-1)
+        sums = lambda q: q.reshape(n, d, -1).sum(1)  # noqa: E731
+        dot, ddot = sums(g * u), sums(np.abs(g) * du) + (d + 2) * e * sums(np.abs(g * u))
+        dz[:, c] = dot * slope[::d]
+        ddz[:, c] = np.abs(slope[::d]) * ddot + (np.abs(dot) + ddot) * ds[::d] + 2 * e * np.abs(dz[:, c])
+    if G is None:
+        return TOL[dt] * out
+    s = ob.even_scalars(irr_in)
+    x0, Wg = apart(x, s), np.asarray(Wg, np.float64)
+    size, err = product_error(dz, ddz, Wg.T, e)
+    gx[:, columns(s)] += err + 2 * e * (size + np.abs(ob.gated_backward(irr_in, irr_out, act, gate, x, W, Wg, b, G)[0]
+                                                      [:, columns(s)]))
+    # the sum goes on from the first term's: its terms are counted with the second's
+    even = ob.even_scalars(irr_out)
+    if even is not None:
+        t, at = even, next(at for s2, t2, at in ob.maps(irr_in, irr_out)[0] if t2 == even)
+        a = act_of[t[3]][1]
+        gx[:, columns(s)] += C * e * (np.abs(ob.part(G, t)[:, :, 0] * a) @ np.abs(ob.matrix(W, s, t, at)).T)
+    gWg = np.abs(x0).T @ ddz + (n + 6) * e * (np.abs(x0).T @ np.abs(dz))
+    gb = ddz.sum(0) + (n + 6) * e * np.abs(dz).sum(0)
+    return tuple(TOL[dt] * v for v in (gx, gW, gWg, gb))
+
+
+def linear_bounds(dt, irr_in, irr_out, act, x, W, b, res, G=None):
+    e, n = EPS[dt], len(x)
+    x = x.astype(np.float64)
+    out = np.zeros((n, segments(irr_out)[1]))
+    gx, gW, gb = np.zeros(x.shape), np.zeros(len(W)), np.zeros(0)
+    for s, t, at in ob.maps(irr_in, irr_out)[0]:
+        d, M = 2 * s[1] + 1, ob.matrix(W, s, t, at)
+        xs = apart(x, s)
+        size, dz = product_error(xs, 0 * xs, M, e)
+        z, slope, ds = xs @ M, np.ones((n * d, t[0])), 0.0
+        even = (t[1], t[2]) == (0, "e")
+        if even:
+            z = z if b is None else z + b
+            dz = dz + 2 * e * (size + (0 if b is None else np.abs(b)))
+            value, slope = ob.activation(act, z)
+            own = 16 * e * (1 + np.abs(z)) if act != "identity" else 0
+            z, dz, ds = value, ob.GROWTH[act] * dz + own, ob.BEND[act] * dz + own
+        out[:, columns(t)] = together(dz, t, n)
+        if G is None:
+            continue
+        g = apart(G.astype(np.float64), t)
+        v, dv = g * slope, np.abs(g) * ds + e * np.abs(g * slope)
+        gx[:, columns(s)] = together(product_error(v, dv, M.T, e)[1], s, n)
+        gW[at:at + M.size] = (np.abs(xs).T @ dv + (n * d + 6) * e * (np.abs(xs).T @ np.abs(v))).reshape(-1)
+        if even:
+            gb = dv.sum(0) + (n + 6) * e * np.abs(v).sum(0)
+    if G is not None:
+        return tuple(TOL[dt] * v for v in (gx, gW, gb))
+    full = ob.linear_forward(irr_in, irr_out, act, x, W, b, res)
+    return TOL[dt] * (out + e * np.abs(full))
+
+
+PAIRS = [("1x0e", "1x0e"), ("4x0e+4x1o", "4x0e+4x1o"), ("16x0e+16x1o+16x2e+16x3o+16x4e",) * 2,
+         ("32x0e+32x1o+32x2e+32x3o",) * 2, ("64x0e+64x1o+64x2e+64x3o", "64x0e+64x1o+64x2e+64x3o"),
+         ("3x1o+17x0e+5x2e+2x0o", "7x0o+31x1o+33x0e"), ("65x0e+33x4e", "70x4e+130x0e"), ("100x0e", "300x0e"),
+         ("300x0e+20x1e", "8x1e"), ("12x0e+40x3o+9x2e", "200x3o+12x2e"), ("64x0e+68x1o", "36x0e+20x1o"),
+         ("1024x0e", "6x0e")]
+SIZES = [1, 15, 17, 64, 65, 100, 333]
+
+
+def block_inputs(rng, dt, irr_in, irr_out, n):
+    x, G = features(rng, irr_in, n, dt, 0.5), features(rng, irr_out, n, dt, 0.5)
+    W = np.concatenate([rng.standard_normal(s[0] * t[0]) / np.sqrt(s[0]) for s, t, _ in ob.maps(irr_in, irr_out)[0]])
+    return x, G, W.astype(NP[dt])
+
+
+def check_gated(node, dt, irr_in, irr_out, n, act="silu", gate="sigmoid", bias=True, place=dev,  # noqa: F811
+                packed=False):
+    import torch
+    rng = np.random.default_rng([n, len(irr_in), len(irr_out)])
+    x, G, W = block_inputs(rng, dt, irr_in, irr_out, n)
+    m0, C = ob.even_scalars(irr_in)[0], ob.channels(irr_out)[1]
+    Wg = (rng.standard_normal((m0, C)) / np.sqrt(m0)).astype(NP[dt])
+    b = (0.5 * rng.standard_normal(C)).astype(NP[dt]) if bias else None
+    plan = node.tpconv_gated_plan(irr_in, irr_out, act, gate, dt)
+    xd, Wd, Wgd, bd, Gd = place(x), place(W), place(Wg), None if b is None else place(b), place(G)
+    out = node.tpconv_gated_forward(plan, xd, Wd, Wgd, bd)
+    within(out, ob.gated_forward(irr_in, irr_out, act, gate, x, W, Wg, b),
+           gated_bounds(dt, irr_in, irr_out, act, gate, x, W, Wg, b), "out")
+    if packed:
+        kept = node.tpconv_pack8(irr_in, xd)
+        x = ob.unpack8(irr_in, *ob.pack8(irr_in, x))
+        at_x = node.tpconv_gated_backward(plan, dev(x), Wd, Wgd, bd, Gd)
+    else:
+        kept = xd
+    got = node.tpconv_gated_backward(plan, kept, Wd, Wgd, bd, Gd)
+    assert len(got) == (4 if bias else 3)
+    if packed:
+        assert all(torch.equal(p, q) for p, q in zip(got, at_x))     # the same rows, the same bits
+    want = ob.gated_backward(irr_in, irr_out, act, gate, x, W, Wg, b, G)
+    bounds = gated_bounds(dt, irr_in, irr_out, act, gate, x, W, Wg, b, G)
+    for name, p, q, r in zip(("grad_x", "grad_weights", "grad_gate_weights", "grad_gate_bias"), got, want, bounds):
+        within(p, q, r, name)
+    again = node.tpconv_gated_backward(plan, kept, Wd, Wgd, bd, Gd)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+    return plan, kept, Wd, Wgd, bd, Gd, out, got
+
+
+def check_linear(node, dt, irr_in, irr_out, n, act="silu", bias=True, residual=True, place=dev,  # noqa: F811
+                 packed=False):
+    import torch
+    rng = np.random.default_rng([n, len(irr_in), len(irr_out), 1])
+    x, G, W = block_inputs(rng, dt, irr_in, irr_out, n)
+    even = ob.even_scalars(irr_out)
+    b = (0.5 * rng.standard_normal(even[0])).astype(NP[dt]) if bias and even else None
+    res = features(rng, irr_out, n, dt) if residual else None
+    plan = node.tpconv_linear_plan(irr_in, irr_out, act, dt)
+    xd, Wd, bd, rd, Gd = place(x), place(W), None if b is None else place(b), None if res is None else place(res), place(G)
+    out = node.tpconv_linear_forward(plan, xd, Wd, bd, rd)
+    within(out, ob.linear_forward(irr_in, irr_out, act, x, W, b, res),
+           linear_bounds(dt, irr_in, irr_out, act, x, W, b, res), "out")
+    kept = xd
+    if packed:
+        kept = node.tpconv_pack8(irr_in, xd)
+        x = ob.unpack8(irr_in, *ob.pack8(irr_in, x))
+        at_x = node.tpconv_linear_backward(plan, dev(x), Wd, bd, Gd)
+    got = node.tpconv_linear_backward(plan, kept, Wd, bd, Gd)
+    if packed:
+        assert all(torch.equal(p, q) for p, q in zip(got, at_x))
+    want = ob.linear_backward(irr_in, irr_out, act, x, W, b, G)
+    for name, p, q, r in zip(("grad_x", "grad_weights", "grad_bias"), got, want,
+                             linear_bounds(dt, irr_in, irr_out, act, x, W, b, res, G)):
+        within(p, q, r, name)
+    again = node.tpconv_linear_backward(plan, kept, Wd, bd, Gd)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+    return plan, kept, Wd, bd, rd, Gd, out, got
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("irr_in,irr_out", PAIRS)
+def test_gated(node, dt, irr_in, irr_out):  # noqa: F811
+    for n in SIZES:
+        log(f"[block] gated {dt} {irr_in} -> {irr_out} n={n}")
+        check_gated(node, dt, irr_in, irr_out, n, bias=n % 2 == 1)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("irr_in,irr_out", PAIRS + [("3x0o+2x1o", "4x0o+1x1o")])
+def test_linear(node, dt, irr_in, irr_out):  # noqa: F811
+    for n in SIZES:
+        log(f"[block] linear {dt} {irr_in} -> {irr_out} n={n}")
+        check_linear(node, dt, irr_in, irr_out, n, act="identity" if n % 3 == 1 else "silu", bias=n % 2 == 1,
+                     residual=n % 5 == 0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("act", sorted(ob.GROWTH))
+def test_activations(node, dt, act):  # noqa: F811
+    irr = "20x0e+5x1o"
+    log(f"[block] activations {dt} {act}")
+    check_gated(node, dt, irr, irr, 70, act=act, gate="sigmoid")
+    check_gated(node, dt, irr, irr, 70, act="silu", gate=act)
+    check_linear(node, dt, irr, irr, 70, act=act)
+
+
+@pytest.mark.parametrize("irr_in,irr_out", PAIRS)
+def test_gradients_from_8_bits(node, irr_in, irr_out):  # noqa: F811
+    for n in (1, 65, 333):
+        log(f"[block] gradients from 8 bits {irr_in} -> {irr_out} n={n}")
+        check_gated(node, "f32", irr_in, irr_out, n, packed=True)
+        check_linear(node, "f32", irr_in, irr_out, n, packed=True)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+def test_dense_off_alignment(node, dt):  # noqa: F811
+    for irr_in, irr_out in (PAIRS[3], PAIRS[4]):
+        log(f"[block] gated and linear {dt} {irr_in} off the alignment")
+        check_gated(node, dt, irr_in, irr_out, 50, place=shifted, packed=dt == "f32")
+        check_linear(node, dt, irr_in, irr_out, 50, place=shifted, packed=dt == "f32")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+def test_dense_of_many_rows(node, dt):  # noqa: F811
+    """Groups of every length, parameters' gradients in many runs."""
+    for n, irr in ((3001, "16x0e+16x1o+16x2e"), (20011, "8x0e+3x1o"), (70001, "5x0e")):
+        log(f"[block] gated and linear {dt} {irr} n={n}")
+        check_gated(node, dt, irr, irr, n)
+        check_linear(node, dt, irr, irr, n)
+
+
+def test_dense_keeps_not_numbers_in_their_row(node):  # noqa: F811
+    """A row of NaN and one of infinities: no other row's result changes by a bit, forward and gradient."""
+    import torch
+    irr_in, irr_out = "20x0e+9x1o+5x2e", "33x0e+17x1o+5x2e"
+    rng = np.random.default_rng(9)
+    n = 130
+    x, G, W = block_inputs(rng, "f32", irr_in, irr_out, n)
+    C = ob.channels(irr_out)[1]
+    Wg, b = (rng.standard_normal(s).astype(np.float32) for s in ((20, C), (C,)))
+    spoiled, bad = x.copy(), [3, 77, 129]
+    spoiled[3], spoiled[77], spoiled[129] = np.nan, np.inf, -np.inf
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    gated, linear = node.tpconv_gated_plan(irr_in, irr_out), node.tpconv_linear_plan(irr_in, irr_out, "gelu")
+    runs = []
+    for v in (x, spoiled):
+        v = dev(v)
+        runs.append((node.tpconv_gated_forward(gated, v, dev(W), dev(Wg), dev(b)),
+                     node.tpconv_gated_backward(gated, v, dev(W), dev(Wg), dev(b), dev(G), need=(1, 0, 0, 0))[0],
+                     node.tpconv_linear_forward(linear, v, dev(W), dev(b[:33])),
+                     node.tpconv_linear_backward(linear, v, dev(W), dev(b[:33]), dev(G), need=(1, 0, 0))[0]))
+    for a, c in zip(*runs):
+        assert torch.equal(a[keep], c[keep])
+    assert torch.isnan(runs[1][0][3]).all()
+
+
+def test_linear_onto_its_residual(node):  # noqa: F811
+    import torch
+    for irr_in, irr_out in (PAIRS[4], PAIRS[5]):
+        plan, x, W, b, res, _, out, _ = check_linear(node, "f32", irr_in, irr_out, 100)
+        got = node.tpconv_linear_forward(plan, x, W, b, res, out=res)
+        assert got is res and torch.equal(res, out)
+
+
+def test_dense_outputs_on_their_own(node):  # noqa: F811
+    import torch
+    irr_in, irr_out = PAIRS[5]
+    plan, x, W, Wg, b, G, _, full = check_gated(node, "f32", irr_in, irr_out, 65)
+    for i in range(4):
+        need = tuple(k == i for k in range(4))
+        got = node.tpconv_gated_backward(plan, x, W, Wg, b, G, need=need)
+        assert [g is not None for g in (got + (None,))[:4]] == list(need)
+        assert torch.equal(got[i], full[i])
+    plan, x, W, b, _, G, _, full = check_linear(node, "f32", irr_in, irr_out, 65, act="identity")
+    for i in range(3):
+        got = node.tpconv_linear_backward(plan, x, W, b, G, need=tuple(k == i for k in range(3)))
+        assert torch.equal(got[i], full[i])
+    assert torch.equal(node.tpconv_linear_backward(plan, None, W, b, G, need=(True, False, False))[0], full[0])
+    with pytest.raises(ValueError):
+        node.tpconv_linear_backward(plan, x, W, b[:3], G)
+
+
+def test_dense_without_rows(node):  # noqa: F811
+    import torch
+    irr_in, irr_out = PAIRS[5]
+    gated, linear = node.tpconv_gated_plan(irr_in, irr_out), node.tpconv_linear_plan(irr_in, irr_out, "silu")
+    new = lambda *s: torch.full(s, 5.0, device="cuda")  # noqa: E731
+    x, G, W = new(0, gated.dim_in), new(0, gated.dim_out), new(gated.weight_numel)
+    Wg, b = new(gated.n_scalars, gated.n_gates), new(gated.n_gates)
+    assert node.tpconv_gated_forward(gated, x, W, Wg, b).shape == G.shape
+    got = node.tpconv_gated_backward(gated, x, W, Wg, b, G, grad_weights=new(gated.weight_numel),
+                                     grad_gate_weights=new(*Wg.shape), grad_gate_bias=new(gated.n_gates))
+    assert got[0].shape == x.shape and not any(t.any() for t in got[1:])
+    got = node.tpconv_linear_backward(linear, x, W, new(33), G, grad_weights=new(gated.weight_numel), grad_bias=new(33))
+    assert not any(t.any() for t in got[1:])
+
+
+def test_binding_refusals(node):  # noqa: F811
+    """Types, shapes, strides and places that the calls do not take."""
+    import torch
+    from equivariant_mlip_tensor_amd.tpconv import TPConvError
+    plan = node.tpconv_norm_plan("4x0e+2x1o")
+    x = torch.zeros(6, 10, device="cuda")
+    for bad in (x.cpu(), x.double(), x[:, :9], torch.zeros(6, 20, device="cuda")[:, ::2], x.half()):
+        with pytest.raises(ValueError):
+            node.tpconv_norm_forward(plan, bad)
+        with pytest.raises(ValueError):
+            node.tpconv_norm_forward(plan, x, bad)
+        with pytest.raises(ValueError):
+            node.tpconv_norm_backward(plan, x, None, bad)
+    with pytest.raises(ValueError):
+        node.tpconv_norm_forward(plan, x, gamma=torch.zeros(5, device="cuda"))
+    with pytest.raises(ValueError):
+        node.tpconv_pack8("4x0e+2x1o", x.double())
+    with pytest.raises(TPConvError):
+        node.tpconv_pack8("4x0e+3x1o", x)
+    linear = node.tpconv_linear_plan("4x0e+2x1o", "3x0e")
+    W = torch.zeros(12, device="cuda")
+    for args in ((x, W[:11]), (x[:, :9], W), (x, W.double()), (x, W, torch.zeros(4, device="cuda")),
+                 (x, W, None, torch.zeros(6, 4, device="cuda"))):
+        with pytest.raises(ValueError):
+            node.tpconv_linear_forward(linear, *args)
+
+
+# ------------------------------------------------------------ the block as used
+BLOCK = ("16x0e+16x1o+16x2e", "48x0e+24x1o+16x2e")
+
+
+class Block:
+    """x = h + linear(gated(norm(h))), h = x + residual: plans, parameters, forward and backward."""
+
+    def __init__(self, node, dt="f32", n=200, irreps=BLOCK, seed=0, eps=1e-6):  # noqa: F811
+        self.node, self.n, self.irreps = node, n, irreps
+        narrow, wide = irreps
+        rng = np.random.default_rng(seed)
+        self.norm = node.tpconv_norm_plan(narrow, eps=eps, dtype=dt)
+        self.gated = node.tpconv_gated_plan(narrow, wide, dtype=dt)
+        self.linear = node.tpconv_linear_plan(wide, narrow, "gelu", dtype=dt)
+        _, _, W1 = block_inputs(rng, dt, narrow, wide, 1)
+        _, _, W2 = block_inputs(rng, dt, wide, narrow, 1)
+        f = lambda *s: rng.standard_normal(s).astype(NP[dt])  # noqa: E731
+        m0, C = self.gated.n_scalars, self.gated.n_gates
+        self.p = dict(gamma=1 + 0.2 * f(self.norm.channels), W1=W1, Wg=f(m0, C) / np.sqrt(m0).astype(NP[dt]),
+                      bg=f(C), W2=W2, b=f(self.linear.n_bias))
+        self.x, self.res, self.G = (features(rng, narrow, n, dt, 0.3) for _ in range(3))
+
+    def put(self):
+        return {k: dev(v) for k, v in {**self.p, "x": self.x, "res": self.res, "G": self.G}.items()}
+
+    def forward(self, t, packed=False):
+        y, h, kept = self.node.tpconv_norm_forward(self.norm, t["x"], t["res"], t["gamma"], need=(True, True, packed))
+        v = self.node.tpconv_gated_forward(self.gated, y, t["W1"], t["Wg"], t["bg"])
+        out = self.node.tpconv_linear_forward(self.linear, v, t["W2"], t["b"], residual=h)
+        return out, (h, kept if packed else y, self.node.tpconv_pack8(self.irreps[1], v) if packed else v)
+
+    def backward(self, t, saved):
+        h, y, v = saved
+        g_v, g_W2, g_b = self.node.tpconv_linear_backward(self.linear, v, t["W2"], t["b"], t["G"])
+        g_y, g_W1, g_Wg, g_bg = self.node.tpconv_gated_backward(self.gated, y, t["W1"], t["Wg"], t["bg"], g_v)
+        g_x, g_gamma = self.node.tpconv_norm_backward(self.norm, h, t["gamma"], g_y, t["G"])
+        return dict(x=g_x, gamma=g_gamma, W1=g_W1, Wg=g_Wg, bg=g_bg, W2=g_W2, b=g_b)
+
+
+def test_block_against_differences(node):  # noqa: F811
+    """The block's gradients in fp64 against central differences along random directions: with a step of 1e-4 the
+    third derivatives leave about 1e-8 of the loss's terms, and rounding 1e-16 of them over 1e-4.  (eps of 0.05: a
+    padding row's third derivatives are of the order of eps^-3/2.)"""
+    import torch
+    blk = Block(node, "f64", n=40, eps=0.05)
+    t = blk.put()
+    out, saved = blk.forward(t)
+    grads = blk.backward(t, saved)
+    size = float((out.abs() * t["G"].abs()).sum())
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for name, grad in grads.items():
+        way = torch.randn(grad.shape, generator=g, device="cuda", dtype=torch.float64)
+        way /= way.norm()
+        ends = []
+        for sign in (1, -1):
+            moved = dict(t, **{name: t[name] + sign * 1e-4 * way})
+            ends.append(float((blk.forward(moved)[0] * t["G"]).sum()))
+        slope = (ends[0] - ends[1]) / 2e-4
+        assert abs(slope - float((grad * way).sum())) <= 1e-7 * size, name
+
+
+def test_block_with_rows_in_8_bits(node):  # noqa: F811
+    """Gradients with the saved rows in 8 bits.  The rows of norm and gated product are off by at most 1/16 of each
+    value or 1/28672 of its segment's largest; the gradients are compared with those of the same restored rows in
+    fp32 (each operator's own test holds these to the definition)."""
+    import torch
+    blk = Block(node)
+    t = blk.put()
+    out, saved = blk.forward(t)
+    out8, saved8 = blk.forward(t, packed=True)
+    assert torch.equal(out, out8)                               # the forward does not change
+    restored = (saved8[0], node.tpconv_unpack8(BLOCK[0], saved8[1]), node.tpconv_unpack8(BLOCK[1], saved8[2]))
+    a, b = blk.backward(t, saved8), blk.backward(t, restored)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    for got, want, irreps in ((restored[1], saved[1], BLOCK[0]), (restored[2], saved[2], BLOCK[1])):
+        got, want = host(got), host(want)
+        for s in segments(irreps)[0]:
+            p, q = got[:, columns(s)], want[:, columns(s)]
+            assert (np.abs(p - q) <= np.maximum(np.abs(q) / 16, np.abs(q).max(1, keepdims=True) / 28672) * 1.00001).all()
+
+
+def test_block_on_another_stream(node):  # noqa: F811
+    import torch
+    blk = Block(node)
+    t = blk.put()
+    out, saved = blk.forward(t)
+    want = blk.backward(t, saved)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        out2, saved2 = blk.forward(t)
+        got = blk.backward(t, saved2)
+    y, h, p = node.tpconv_norm_forward(blk.norm, t["x"], t["res"], t["gamma"], need=(True, True, True), stream=side)
+    v = node.tpconv_gated_forward(blk.gated, y, t["W1"], t["Wg"], t["bg"], stream=side)
+    out3 = node.tpconv_linear_forward(blk.linear, v, t["W2"], t["b"], residual=h, stream=side)
+    grads = node.tpconv_gated_backward(blk.gated, y, t["W1"], t["Wg"], t["bg"], v, stream=side)
+    side.synchronize()
+    assert torch.equal(out, out2) and torch.equal(out, out3) and all(torch.equal(want[k], got[k]) for k in want)
+    assert all(torch.equal(a, b) for a, b in zip(grads, node.tpconv_gated_backward(blk.gated, y, t["W1"], t["Wg"],
+                                                                                   t["bg"], v)))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_block_captured(node, packed):  # noqa: F811
+    """A captured training step, replayed on new inputs with eager steps of another size between the replays; two
+    captured graphs whose workspaces come from one pool."""
+    import torch
+    blocks = [Block(node, n=200), Block(node, n=77, seed=3)]
+    tensors = [b.put() for b in blocks]
+    other = Block(node, n=500, seed=5)
+    t_other = other.put()
+    out, saved = other.forward(t_other, packed)
+    want_other = other.backward(t_other, saved)
+    for b, t in zip(blocks, tensors):                           # kernels loaded before the capture
+        b.backward(t, b.forward(t, packed)[1])
+    torch.cuda.synchronize()
+    graphs, results, pool = [], [], None
+    for b, t in zip(blocks, tensors):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            o, s = b.forward(t, packed)
+            results.append((o, b.backward(t, s)))
+        pool = graph.pool()
+        graphs.append(graph)
+    rng = np.random.default_rng(11)
+    for step in range(4):
+        for b, t, graph, (o, got) in zip(blocks, tensors, graphs, results):
+            for k in ("x", "res", "G"):
+                t[k].copy_(dev(features(rng, BLOCK[0], b.n, "f32", 0.3)))
+            graph.replay()
+            torch.cuda.synchronize()
+            o2, s2 = b.forward(t, packed)
+            want = b.backward(t, s2)
+            assert torch.equal(o, o2) and all(torch.equal(got[k], want[k]) for k in want), step
+        eager = other.backward(t_other, other.forward(t_other, packed)[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(eager[k], want_other[k]) for k in eager)
+
+
+def test_calls_do_not_write_past_their_outputs(node):  # noqa: F811
+    """Outputs, workspaces and codes inside larger buffers: what lies around them stays as it was."""
+    import torch
+    guard, mark = 1024, 0xA5
+    made = []
+
+    def room(shape, dtype):
+        size = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((guard + size + guard,), mark, dtype=torch.uint8, device="cuda")
+        made.append((buf, size))
+        return buf[guard:guard + size].view(dtype).view(shape)
+
+    f32 = torch.float32
+    for irr_in, irr_out, n in (PAIRS[5] + (67,), PAIRS[4] + (41,), PAIRS[1] + (1,)):
+        rng = np.random.default_rng(12)
+        x, G, W = block_inputs(rng, "f32", irr_in, irr_out, n)
+        gated, linear = node.tpconv_gated_plan(irr_in, irr_out), node.tpconv_linear_plan(irr_in, irr_out, "silu")
+        norm = node.tpconv_norm_plan(irr_in)
+        m0, C, nb = gated.n_scalars, gated.n_gates, linear.n_bias
+        xd, Gd, Wd = dev(x), dev(G), dev(W)
+        Wg, b = dev(rng.standard_normal((m0, C)).astype(np.float32)), dev(rng.standard_normal(C).astype(np.float32))
+        kept = node.PackedRows(room(x.shape, torch.uint8), room((n, norm.n_segments), f32))
+        node.tpconv_norm_forward(norm, xd, xd, out=room(x.shape, f32), sum=room(x.shape, f32), packed=kept)
+        ws = room((node.tpconv_norm_workspace_bytes(norm, n),), torch.uint8)
+        node.tpconv_norm_backward(norm, xd, None, xd, grad_x=room(x.shape, f32), grad_gamma=room((norm.channels,), f32),
+                                  workspace=ws)
+        node.tpconv_unpack8(irr_in, kept, out=room(x.shape, f32))
+        node.tpconv_gated_forward(gated, xd, Wd, Wg, b, out=room(G.shape, f32))
+        ws = room((node.tpconv_dense_workspace_bytes(gated, n),), torch.uint8)
+        node.tpconv_gated_backward(gated, kept, Wd, Wg, b, Gd, grad_x=room(x.shape, f32),
+                                   grad_weights=room(W.shape, f32), grad_gate_weights=room((m0, C), f32),
+                                   grad_gate_bias=room((C,), f32), workspace=ws)
+        node.tpconv_linear_forward(linear, xd, Wd, b[:nb].clone(), out=room(G.shape, f32))
+        ws = room((node.tpconv_dense_workspace_bytes(linear, n),), torch.uint8)
+        node.tpconv_linear_backward(linear, xd, Wd, b[:nb].clone(), Gd, grad_x=room(x.shape, f32),
+                                    grad_weights=room(W.shape, f32), grad_bias=room((nb,), f32), workspace=ws)
+    torch.cuda.synchronize()
+    for buf, size in made:
+        assert (buf[:guard] == mark).all() and (buf[guard + size:] == mark).all()
