@@ -48,6 +48,11 @@ def _jobs():
     units.append((os.path.join(CSRC, "graph.hip"), os.path.join(BUILD, "graph.o"), []))
     units.append((os.path.join(CSRC, "sh.hip"), os.path.join(BUILD, "sh.o"), []))
     units.append((os.path.join(CSRC, "so2.hip"), os.path.join(BUILD, "so2.o"), []))
+    for dbl in (1, 0):
+        for mode in (3, 1, 0, 4, 2):   # gated gradient, gated, linear, transposed, linear's slope
+            units.append((os.path.join(CSRC, "node_dense_rows.hip"),
+                          os.path.join(BUILD, f"node_dense_m{mode}_{'f64' if dbl else 'f32'}.o"),
+                          [f"-DTPCONV_DOUBLE={dbl}", f"-DTPCONV_MODE={mode}"]))
     for stem in ("node_dense", "node_norm", "node_experts", "node_embed", "node_route", "node_dropout"):
         units.append((os.path.join(CSRC, stem + ".hip"), os.path.join(BUILD, stem + ".o"), []))
     # the host CG builder runs without FMA contraction so its run-time values

@@ -1,415 +1,10 @@
-// node_dense.hip -- equivariant products of irreps rows with one set of maps,
-// and what stands around them: the linear map with bias, activation and
-// residual, the gated feed-forward product, and their gradients.
-//   u_s[i][v][m] = sum_u M_s[u][v] x_s[i][u][m]           (a map of segment s)
-//   z[i][c]      = sum_u Wg[u][c] x_0e[i][u] + b[c]       (gated: its gates)
-//   linear: out = residual + a(u + bias);  gated: out[s][v][m] = a(z[c(s, v)]) u_s[v][m]
-// A map's 2l+1 components all see the same matrix, so it is a matrix product
-// whose rows are (component, atom); it runs on the matrix cores
-// (v_mfma_f32_16x16x4f32, v_mfma_f64_16x16x4f64: the library's data types).
-// A matrix instruction's 16 rows are 16 atoms at one component, so a lane ends
-// up with all 2l+1 components of its (atom, channel) pairs, and with their gate:
-// activation, product, their derivatives and the gate gradient's sum over
-// components need no exchange between lanes.
-#include <hip/hip_runtime.h>
-
-#include <algorithm>
-
-#include "node_device.hpp"
-#include "node_internal.hpp"
+// node_dense.hip -- the linear and gated maps' parameters' gradients, and the
+// passes that make up their calls (the products themselves: node_dense.hpp).
+#include "node_dense.hpp"
 
 namespace tpconv {
+namespace dense {
 namespace {
-
-// -------------------------------------------------------------- activations
-template <class T>
-__device__ __forceinline__ T normal_below(T z) {  // Phi(z)
-  return T(0.5) * erfc(z * T(-0.70710678118654752440));
-}
-
-template <class T>
-__device__ __forceinline__ T activated(int kind, T z) {
-  switch (kind) {
-    case TPCONV_ACT_SILU: return z / (T(1) + exp(-z));
-    case TPCONV_ACT_SIGMOID: return T(1) / (T(1) + exp(-z));
-    case TPCONV_ACT_TANH: return tanh(z);
-    case TPCONV_ACT_GELU: return z * normal_below(z);
-    default: return z;
-  }
-}
-
-// The activation and its slope, the slope in forms that do not cancel where it
-// saturates: 1 - s as the sigmoid of -z, 1 - tanh^2 by exponentials.
-template <class T>
-__device__ __forceinline__ void activated_with_slope(int kind, T z, T& value, T& slope) {
-  switch (kind) {
-    case TPCONV_ACT_SILU: {
-      const T s = T(1) / (T(1) + exp(-z)), t = T(1) / (T(1) + exp(z));
-      value = z / (T(1) + exp(-z));
-      slope = s + z * s * t;
-      return;
-    }
-    case TPCONV_ACT_SIGMOID: {
-      value = T(1) / (T(1) + exp(-z));
-      slope = value / (T(1) + exp(z));
-      return;
-    }
-    case TPCONV_ACT_TANH: {
-      value = tanh(z);
-      const T e = exp(T(-2) * fabs(z)), q = T(1) / (T(1) + e);
-      slope = T(4) * e * q * q;
-      return;
-    }
-    case TPCONV_ACT_GELU: {
-      const T below = normal_below(z);
-      value = z * below;
-      slope = below + z * exp(T(-0.5) * z * z) * T(0.39894228040143267794);
-      return;
-    }
-    default:
-      value = z;
-      slope = T(1);
-  }
-}
-
-// ------------------------------------------------------------------ staging
-// Rows of a segment on their way to LDS: `len` elements of each of `rows` rows,
-// element c of row s at lds[s * pitch + c], in pieces of PER, kBatch of a
-// thread's in flight.
-constexpr int kBatch = 8;
-
-// (row, piece) of number q of rows of `pieces` pieces; q stays below 2^16, so
-// the rounded product is exact
-__device__ __forceinline__ void split(int q, int pieces, float inv, int& row, int& piece) {
-  row = static_cast<int>((static_cast<float>(q) + 0.5f) * inv);
-  piece = q - row * pieces;
-}
-
-template <class T, int PER>
-__device__ __forceinline__ void stage_rows(T* lds, int pitch, const T* from, int64_t ld, int rows, int len, int tid,
-                                           int threads) {
-  struct alignas(PER * sizeof(T)) Piece {
-    T v[PER];
-  };
-  const int pieces = len / PER, total = rows * pieces;
-  const float inv = 1.0f / static_cast<float>(pieces);
-  for (int q0 = tid; q0 < total; q0 += kBatch * threads) {
-    Piece p[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      int s, c;
-      split(min(q0 + j * threads, total - 1), pieces, inv, s, c);
-      p[j] = *reinterpret_cast<const Piece*>(from + s * ld + c * PER);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      int s, c;
-      split(min(q0 + j * threads, total - 1), pieces, inv, s, c);
-      if (q0 + j * threads < total) *reinterpret_cast<Piece*>(lds + s * pitch + c * PER) = p[j];
-    }
-  }
-}
-
-// The same from 8 bits: codes of a row and segment times its scale.
-template <int PER>
-__device__ __forceinline__ void stage_codes(float* lds, int pitch, const uint8_t* from, int64_t ld,
-                                            const float* scales, int64_t ld_scales, int rows, int len, int tid,
-                                            int threads) {
-  const int pieces = len / PER, total = rows * pieces;
-  const float inv = 1.0f / static_cast<float>(pieces);
-  for (int q0 = tid; q0 < total; q0 += kBatch * threads) {
-    int code[kBatch];
-    float scale[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      int s, c;
-      split(min(q0 + j * threads, total - 1), pieces, inv, s, c);
-      const uint8_t* const at = from + s * ld + c * PER;
-      if constexpr (PER == 4)
-        code[j] = *reinterpret_cast<const int*>(at);
-      else
-        code[j] = *at;
-      scale[j] = scales[s * ld_scales];
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      int s, c;
-      split(min(q0 + j * threads, total - 1), pieces, inv, s, c);
-      if (q0 + j * threads >= total) continue;
-      float* const to = lds + s * pitch + c * PER;
-      to[0] = __builtin_amdgcn_cvt_f32_fp8(code[j], 0) * scale[j];
-      if constexpr (PER == 4) {
-        to[1] = __builtin_amdgcn_cvt_f32_fp8(code[j], 1) * scale[j];
-        to[2] = __builtin_amdgcn_cvt_f32_fp8(code[j], 2) * scale[j];
-        to[3] = __builtin_amdgcn_cvt_f32_fp8(code[j], 3) * scale[j];
-      }
-    }
-  }
-}
-
-// A segment of rows to stage from.
-struct RowSource {
-  const void* rows;      // T, or codes where `scales`
-  const float* scales;   // of the segment in row 0
-  int64_t ld, ld_scales; // elements of a row; scales of a row
-  int32_t off;           // the segment's first column
-  int32_t K;             // its channels
-  int32_t packed;        // pieces of 16 bytes (codes: of 4)
-};
-
-// `count` channels of d components from channel k0 on, of rows base ..
-template <class T>
-__device__ __forceinline__ void stage_source(const RowSource& a, T* lds, int pitch, int64_t base, int rows, int k0,
-                                             int count, int d, int tid, int threads) {
-  const int64_t at = base * a.ld + a.off + k0 * d;
-  const int len = count * d;
-  if (sizeof(T) == 4 && a.scales != nullptr) {
-    const uint8_t* const from = static_cast<const uint8_t*>(a.rows) + at;
-    float* const to = reinterpret_cast<float*>(lds);
-    if (a.packed)
-      stage_codes<4>(to, pitch, from, a.ld, a.scales + base * a.ld_scales, a.ld_scales, rows, len, tid, threads);
-    else
-      stage_codes<1>(to, pitch, from, a.ld, a.scales + base * a.ld_scales, a.ld_scales, rows, len, tid, threads);
-    return;
-  }
-  const T* const from = static_cast<const T*>(a.rows) + at;
-  if (a.packed)
-    stage_rows<T, 16 / sizeof(T)>(lds, pitch, from, a.ld, rows, len, tid, threads);
-  else
-    stage_rows<T, 1>(lds, pitch, from, a.ld, rows, len, tid, threads);
-}
-
-// ------------------------------------------------------------------- products
-// A block takes a tile of atoms, one map and up to 64 (fp64: 32) of its output
-// channels, 16 to a wavefront.  The atoms' segment goes to LDS as it lies in
-// memory; a row's pitch is 4 more (fp64: 2) than a multiple of 64 (32) banks, so
-// 16 atoms times 4 channels fall into as many banks, whatever 2l+1 (it is odd).
-// The weights go straight to registers.  Results pass through LDS on their way
-// out, so that rows are written (and a residual or grad_out is read) in whole
-// pieces.
-enum Mode { kLinear, kGated, kLinearGrad, kGatedGrad, kTransposed };
-
-constexpr int atoms_of(int d) { return d == 1 ? 64 : (d == 3 ? 32 : 16); }
-
-// One product's operands: rows and weights W[k * ldw + n], or, transposed,
-// W[n * ldw + k].
-struct Term {
-  RowSource src;
-  const void* weights;
-  int32_t ldw;
-  int32_t transposed_packed;  // transposed: 16-byte pieces along k
-};
-
-struct DenseJob {
-  Term main;       // components d
-  Term gate;       // kGated, kGatedGrad: the gates' (rows of 0e); kTransposed: the second term of 0e, K = 0 without
-  int32_t d, N;
-  int32_t out_off; // first column in a row of out (kLinearGrad: of dz)
-  int32_t g_off;   // first column in a row of grad_out
-  int32_t bias;    // first bias of the job, -1: none
-  int32_t gate0;   // first gate
-  int32_t act;
-  int32_t packed_out, packed_g;
-  int32_t first;   // first share (a block of output channels) of this job
-};
-
-struct DenseArgs {
-  int64_t n_rows;
-  int64_t ld_out, ld_g, n_gates;
-  void* out;
-  const void* extra;  // kLinear: residual, kLinearGrad, kGatedGrad: grad_out
-  const void* bias;
-  void* dz;           // kGatedGrad: [n_rows][n_gates]
-  int64_t groups;     // of atoms, a block's
-  int32_t group;      // atoms of one: 16, 32 or 64
-  int32_t n_jobs, shares, waves;
-  int64_t block0;
-  DenseJob job[kMaxMaps];
-};
-
-// acc[t][m] += rows of tile t, component m
-template <class T, int D, int KS, bool ADJ, int MT>
-__device__ __forceinline__ void accumulate(const Term& t, T* lds, int64_t base, int rows, int col,
-                                           typename Mfma<T>::Acc (&acc)[MT][D]) {
-  constexpr int CH = 4 * KS, P = CH * D + 16 / int(sizeof(T));
-  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, g4 = lane >> 4;
-  const T* const W = static_cast<const T*>(t.weights);
-  for (int k0 = 0; k0 < t.src.K; k0 += CH) {
-    const int count = min(CH, t.src.K - k0);
-    T b[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int k = 4 * s + g4;
-      const int64_t kc = k0 + min(k, count - 1);
-      const T v = ADJ ? W[int64_t(col) * t.ldw + kc] : W[kc * t.ldw + col];
-      b[s] = k < count ? v : T(0);
-    }
-    __syncthreads();  // what was in LDS is read
-    stage_source(t.src, lds, P, base, rows, k0, count, D, tid, blockDim.x);
-    if (count < CH)  // no NaN from channels that are not there
-      for (int q = tid; q < rows * (CH - count) * D; q += blockDim.x) {
-        const int s = q / ((CH - count) * D);
-        lds[s * P + count * D + (q - s * (CH - count) * D)] = T(0);
-      }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (16 * i >= rows) break;
-      const T* const ap = lds + (16 * i + i16) * P + g4 * D;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int m = 0; m < D; ++m) acc[i][m] = Mfma<T>::step(ap[4 * s * D + m], b[s], acc[i][m]);
-    }
-  }
-}
-
-template <class T, int D, int KS, int MODE>
-__device__ __forceinline__ void dense_tile(const DenseArgs& a, const DenseJob& j, int64_t base, int rows, int n0,
-                                           T* lds) {
-  constexpr int TA = atoms_of(D), MT = TA / 16;
-  constexpr bool ADJ = MODE == kTransposed;
-  using Acc = typename Mfma<T>::Acc;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
-  const int wide = 16 * a.waves, n_here = min(wide, j.N - n0), c = 16 * w + i16;
-  const int col = min(n0 + c, j.N - 1);  // past the last channel: a column that is not written
-
-  Acc u[MT][D];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int m = 0; m < D; ++m) u[i][m] = Acc{0, 0, 0, 0};
-  accumulate<T, D, KS, ADJ, MT>(j.main, lds, base, rows, col, u);
-
-  Acc z[MT][1];
-  if constexpr (MODE == kGated || MODE == kGatedGrad) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) z[i][0] = Acc{0, 0, 0, 0};
-    accumulate<T, 1, KS, false, MT>(j.gate, lds, base, rows, j.gate0 + col, z);
-  }
-  if constexpr (MODE == kTransposed && D == 1)
-    if (j.gate.src.K > 0) accumulate<T, 1, KS, true, MT>(j.gate, lds, base, rows, col, u);
-
-  const int pitch = wide * D + 16 / int(sizeof(T));
-  const T bias = MODE != kTransposed && j.bias >= 0 ? static_cast<const T*>(a.bias)[j.bias + col] : T(0);
-  __syncthreads();
-  if constexpr (MODE == kLinearGrad || MODE == kGatedGrad) {
-    const RowSource g{a.extra, nullptr, a.ld_g, 0, j.g_off, j.N, j.packed_g};
-    stage_source(g, lds, pitch, base, rows, n0, n_here, D, tid, blockDim.x);
-    __syncthreads();
-  }
-  if (c < n_here) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (16 * i >= rows) break;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int s = 16 * i + Mfma<T>::row(g4, q);
-        T* const at = lds + s * pitch + c * D;
-        if constexpr (MODE == kGated) {
-          const T gate = activated(j.act, z[i][0][q] + bias);
-#pragma unroll
-          for (int m = 0; m < D; ++m) at[m] = gate * u[i][m][q];
-        } else if constexpr (MODE == kGatedGrad) {
-          T gate, slope, dot = 0;
-          activated_with_slope(j.act, z[i][0][q] + bias, gate, slope);
-#pragma unroll
-          for (int m = 0; m < D; ++m) {
-            const T g = at[m];
-            dot = fma(g, u[i][m][q], dot);
-            at[m] = g * gate;
-          }
-          if (s < rows) static_cast<T*>(a.dz)[(base + s) * a.n_gates + j.gate0 + n0 + c] = dot * slope;
-        } else if constexpr (MODE == kLinearGrad) {
-          T value, slope;
-          activated_with_slope(j.act, u[i][0][q] + bias, value, slope);
-          at[0] *= slope;
-        } else if constexpr (MODE == kLinear && D == 1) {
-          at[0] = activated(j.act, u[i][0][q] + bias);
-        } else {
-#pragma unroll
-          for (int m = 0; m < D; ++m) at[m] = u[i][m][q];
-        }
-      }
-    }
-  }
-  __syncthreads();
-  // out, in whole pieces where rows allow it
-  T* const out = static_cast<T*>(a.out) + base * a.ld_out + j.out_off + n0 * D;
-  const T* const res = MODE == kLinear && a.extra != nullptr
-                           ? static_cast<const T*>(a.extra) + base * a.ld_out + j.out_off + n0 * D
-                           : nullptr;
-  auto write = [&](auto per) {
-    constexpr int PER = decltype(per)::value;
-    struct alignas(PER * sizeof(T)) Piece {
-      T v[PER];
-    };
-    const int pieces = n_here * D / PER, total = rows * pieces;
-    const float inv = 1.0f / static_cast<float>(pieces);
-    for (int q0 = tid; q0 < total; q0 += kBatch * blockDim.x) {
-      Piece r[kBatch] = {};
-      if (MODE == kLinear && res != nullptr)
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          int s, e;
-          split(min(q0 + k * int(blockDim.x), total - 1), pieces, inv, s, e);
-          r[k] = *reinterpret_cast<const Piece*>(res + s * a.ld_out + e * PER);
-        }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (q0 + k * int(blockDim.x) >= total) break;
-        int s, e;
-        split(q0 + k * blockDim.x, pieces, inv, s, e);
-        Piece p = *reinterpret_cast<const Piece*>(lds + s * pitch + e * PER);
-        if (MODE == kLinear && res != nullptr)
-#pragma unroll
-          for (int x = 0; x < PER; ++x) p.v[x] += r[k].v[x];
-        *reinterpret_cast<Piece*>(out + s * a.ld_out + e * PER) = p;
-      }
-    }
-  };
-  if (j.packed_out)
-    write(std::integral_constant<int, 16 / sizeof(T)>{});
-  else
-    write(std::integral_constant<int, 1>{});
-}
-
-template <class T, int KS, int MODE>
-__global__ __launch_bounds__(256) void k_dense(DenseArgs a) {
-  extern __shared__ char lds[];
-  // a group's shares run on one XCD (blocks go round them), so its rows of 0e are fetched once there
-  const int64_t block = a.block0 + blockIdx.x, eight = block / (8 * a.shares);
-  const int in = static_cast<int>(block - eight * 8 * a.shares), share = in >> 3;
-  const int64_t group = eight * 8 + (in & 7);
-  if (group >= a.groups) return;
-  int ji = 0;
-  while (ji + 1 < a.n_jobs && share >= a.job[ji + 1].first) ++ji;
-  const DenseJob& j = a.job[ji];
-  const int n0 = (share - j.first) * 16 * a.waves;
-  T* const mem = reinterpret_cast<T*>(lds);
-  const int64_t from = group * a.group;
-  const int atoms = static_cast<int>(min<int64_t>(a.group, a.n_rows - from));
-#define TPCONV_DENSE(D)                                                                                  \
-  case D:                                                                                                \
-    for (int i = 0; i < atoms; i += atoms_of(D)) {                                                       \
-      if (i > 0) __syncthreads();                                                                        \
-      dense_tile<T, D, KS, MODE>(a, j, from + i, min(atoms - i, atoms_of(D)), n0, mem);                  \
-    }                                                                                                    \
-    break;
-  if constexpr (MODE == kLinearGrad) {
-    dense_tile<T, 1, KS, MODE>(a, j, from, atoms, n0, mem);
-  } else {
-    switch (j.d) {
-      TPCONV_DENSE(1)
-      TPCONV_DENSE(3)
-      TPCONV_DENSE(5)
-      TPCONV_DENSE(7)
-      TPCONV_DENSE(9)
-      default: break;
-    }
-  }
-#undef TPCONV_DENSE
-}
 
 // --------------------------------------------------------- parameters' gradients
 // dM[u][v] = sum over atoms and components of x[i][u][m] g[i][v][m]: a matrix
@@ -435,7 +30,6 @@ struct ParamArgs {
   int64_t n_rows;
   void* part;           // NULL: one run each, written to the gradients
   int32_t n_jobs;
-  int32_t block0;
   ParamJob job[kMaxMaps + 1];
 };
 
@@ -446,16 +40,25 @@ constexpr int tile_side() {
 // atoms of a stage, a multiple of 4
 constexpr int stage_atoms(int d) { return d == 1 ? 32 : (d == 3 ? 16 : 8); }
 
-template <class T, int D>
+template <class T, int D, bool VEC, bool X8>
 __device__ __forceinline__ void param_tile(const ParamArgs& a, const ParamJob& j, int uv, int run, T* lds) {
   constexpr int S = tile_side<T>(), SA = stage_atoms(D), P = S * D + 16, H = S / 2, F = H / 16;
   using Acc = typename Mfma<T>::Acc;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i16 = lane & 15, g4 = lane >> 4;
+  const Place p;
+  const int tid = p.tid, w = p.wave, i16 = p.lane & 15, g4 = p.lane >> 4;
   const int u0 = uv / j.nv * S, v0 = uv % j.nv * S;
   const int nu = min(S, j.x.K - u0), nv = min(S, j.g.K - v0);
   const int64_t from = run * j.run, upto = min(from + j.run, a.n_rows);
   T* const xs = lds;
   T* const gs = lds + SA * P;
+  Mover<T, S * D, SA, P, VEC, X8> mx;
+  Mover<T, S * D, SA, P, VEC, false> mg;
+  auto issue = [&](int64_t base) {
+    const int rows = static_cast<int>(min<int64_t>(SA, upto - base));
+    mx.issue(p, j.x, base, rows, u0, nu, D);
+    mg.issue(p, j.g, base, rows, v0, nv, D);
+  };
+  if (from < upto) issue(from);
   // channels that are not there stay zero
   for (int q = tid; q < 2 * SA * P; q += 256) lds[q] = T(0);
   const int tu = (w >> 1) * H, tv = (w & 1) * H;
@@ -468,10 +71,11 @@ __device__ __forceinline__ void param_tile(const ParamArgs& a, const ParamJob& j
   for (int64_t base = from; base < upto; base += SA) {
     const int rows = static_cast<int>(min<int64_t>(SA, upto - base));
     __syncthreads();
-    stage_source(j.x, xs, P, base, rows, u0, nu, D, tid, 256);
-    stage_source(j.g, gs, P, base, rows, v0, nv, D, tid, 256);
+    mx.land(p, xs, rows, nu * D);
+    mg.land(p, gs, rows, nv * D);
     for (int q = tid; q < (SA - rows) * P; q += 256) xs[rows * P + q] = gs[rows * P + q] = T(0);
     __syncthreads();
+    if (base + SA < upto) issue(base + SA);
     if (D == 1 && j.column_sums && u0 == 0)
       for (int s = tid / S; s < rows; s += 256 / S) column += gs[s * P + tid % S];
 #pragma unroll
@@ -521,23 +125,32 @@ __device__ __forceinline__ void param_tile(const ParamArgs& a, const ParamJob& j
   }
 }
 
-template <class T>
-__global__ __launch_bounds__(256) void k_param(ParamArgs a) {
-  extern __shared__ char lds[];
-  const int block = a.block0 + static_cast<int>(blockIdx.x);
+template <class T, bool X8>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_param(ParamArgs a) {
+  extern __shared__ char dynamic[];
+  const int block = static_cast<int>(blockIdx.x);
   int ji = 0;
   while (ji + 1 < a.n_jobs && block >= a.job[ji + 1].first) ++ji;
-  const ParamJob& j = a.job[ji];
+  const ParamJob j = a.job[ji];
   const int r = block - j.first, uv = r % (j.nu * j.nv), run = r / (j.nu * j.nv);
-  T* const mem = reinterpret_cast<T*>(lds);
+  T* const lds = reinterpret_cast<T*>(dynamic);
+  const bool vec = j.x.packed && j.g.packed;
+#define TPCONV_PARAM(D)                                \
+  case D:                                              \
+    if (vec)                                           \
+      param_tile<T, D, true, X8>(a, j, uv, run, lds);  \
+    else                                               \
+      param_tile<T, D, false, X8>(a, j, uv, run, lds); \
+    break;
   switch (j.d) {
-    case 1: param_tile<T, 1>(a, j, uv, run, mem); break;
-    case 3: param_tile<T, 3>(a, j, uv, run, mem); break;
-    case 5: param_tile<T, 5>(a, j, uv, run, mem); break;
-    case 7: param_tile<T, 7>(a, j, uv, run, mem); break;
-    case 9: param_tile<T, 9>(a, j, uv, run, mem); break;
+    TPCONV_PARAM(1)
+    TPCONV_PARAM(3)
+    TPCONV_PARAM(5)
+    TPCONV_PARAM(7)
+    TPCONV_PARAM(9)
     default: break;
   }
+#undef TPCONV_PARAM
 }
 
 // The runs' matrices and column sums, added in order in 64 bits: 64 values a
@@ -592,11 +205,18 @@ bool pieces16(const void* p, int64_t ld, int64_t off, int64_t len) {
   return aligned16(p) && ld % per == 0 && off % per == 0 && len % per == 0;
 }
 
+// Whether rows' channels can be taken four at a time, 16 bytes apart or a multiple of it.
+template <class T>
+bool in_fours(const void* p, int64_t ld, int64_t off, int64_t channels) {
+  constexpr int per = 16 / sizeof(T);
+  return aligned16(p) && ld % per == 0 && off % per == 0 && channels % 4 == 0;
+}
+
 // x's segment s_in as a source
 template <class T>
 RowSource source_of(const Dense& p, const DenseInput& x, int32_t off, int32_t mul, int d, int seg) {
   RowSource r{};
-  r.ld = p.dim_in;
+  r.ld = static_cast<int32_t>(p.dim_in);
   r.off = off;
   r.K = mul;
   if (x.codes != nullptr) {
@@ -615,53 +235,11 @@ template <class T>
 RowSource source_rows(const void* rows, int64_t ld, int32_t off, int32_t mul, int d) {
   RowSource r{};
   r.rows = rows;
-  r.ld = ld;
+  r.ld = static_cast<int32_t>(ld);
   r.off = off;
   r.K = mul;
   r.packed = pieces16<T>(rows, ld, off, int64_t(mul) * d);
   return r;
-}
-
-template <class T>
-constexpr int most_waves() {
-  return sizeof(T) == 4 ? 4 : 2;
-}
-
-// Shares of the jobs, LDS and launch; the jobs' sizes and terms are set.
-template <class T, int MODE>
-hipError_t run_dense(DenseArgs& a, hipStream_t s) {
-  if (a.n_rows == 0 || a.n_jobs == 0) return hipSuccess;
-  int widest = 1, deepest = 1;
-  for (int i = 0; i < a.n_jobs; ++i) {
-    widest = std::max(widest, a.job[i].N);
-    deepest = std::max({deepest, a.job[i].main.src.K, a.job[i].gate.src.K});
-  }
-  a.waves = std::min(most_waves<T>(), (widest + 15) / 16);
-  // channels that LDS holds at a time: 64 (fp64: 32), fewer where no map has so many
-  const int ks = sizeof(T) == 4 ? (deepest <= 16 ? 4 : (deepest <= 32 ? 8 : 16)) : (deepest <= 16 ? 4 : 8);
-  size_t lds = 0;
-  a.shares = 0;
-  for (int i = 0; i < a.n_jobs; ++i) {
-    DenseJob& j = a.job[i];
-    j.first = a.shares;
-    a.shares += (j.N + 16 * a.waves - 1) / (16 * a.waves);
-    const size_t pad = 16 / sizeof(T), wide = std::max(4 * ks, 16 * a.waves);
-    lds = std::max(lds, sizeof(T) * atoms_of(j.d) * (wide * j.d + pad));  // 37 KiB at most
-  }
-  a.group = 64;
-  while (a.group > 16 && (a.n_rows + a.group - 1) / a.group * a.shares < 2048) a.group /= 2;
-  a.groups = (a.n_rows + a.group - 1) / a.group;
-  const int64_t blocks = (a.groups + 7) / 8 * 8 * a.shares;
-  auto go = [&](auto* f) -> hipError_t {
-    in_launches(blocks, 64 * a.waves, [&](int64_t block0, unsigned n) {
-      a.block0 = block0;
-      hipLaunchKernelGGL(f, dim3(n), dim3(64 * a.waves), lds, s, a);
-    });
-    return hipGetLastError();
-  };
-  if (ks == 4) return go(k_dense<T, 4, MODE>);
-  if (ks == 8 || sizeof(T) == 8) return go(k_dense<T, 8, MODE>);
-  return go(k_dense<T, sizeof(T) == 4 ? 16 : 8, MODE>);
 }
 
 // The jobs of a pass over the maps: rows of x times the maps.
@@ -697,17 +275,16 @@ hipError_t dense_forward(const Dense& p, int64_t n_rows, const void* x, const vo
                          const void* bias, const void* residual, void* out, hipStream_t s) {
   DenseArgs a{};
   a.n_rows = n_rows;
-  a.ld_out = p.dim_out;
-  a.n_gates = p.n_gates;
+  a.ld_out = static_cast<int32_t>(p.dim_out);
+  a.n_gates = static_cast<int32_t>(p.n_gates);
   a.out = out;
   a.extra = residual;
   forward_jobs<T>(p, DenseInput{x, nullptr, nullptr}, weights, gate_weights, bias, a, false);
   for (int i = 0; i < a.n_jobs; ++i) {
     DenseJob& j = a.job[i];
-    const int64_t len = int64_t(j.N) * j.d;
-    j.packed_out = pieces16<T>(out, p.dim_out, j.out_off, len) && aligned16(residual);
+    j.packed_out = in_fours<T>(out, p.dim_out, j.out_off, j.N) && aligned16(residual);
   }
-  return p.gated ? run_dense<T, kGated>(a, s) : run_dense<T, kLinear>(a, s);
+  return p.gated ? run_dense<T, kGated, false>(a, s) : run_dense<T, kLinear, false>(a, s);
 }
 
 // How the atoms of the parameters' jobs are cut into runs: about kParamBlocks
@@ -790,14 +367,14 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
   if (p.gated || p.sloped()) {
     DenseArgs a{};
     a.n_rows = n_rows;
-    a.ld_g = p.dim_out;
-    a.n_gates = p.n_gates;
+    a.ld_g = static_cast<int32_t>(p.dim_out);
+    a.n_gates = static_cast<int32_t>(p.n_gates);
     a.extra = grad_out;
     forward_jobs<T>(p, x, weights, gate_weights, bias, a, !p.gated);
     if (p.gated) {
       du = reinterpret_cast<T*>(mem);
       a.out = mem;
-      a.ld_out = p.dim_out;
+      a.ld_out = static_cast<int32_t>(p.dim_out);
       a.dz = dz;
     } else {
       a.out = dz;
@@ -806,10 +383,20 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
     }
     for (int i = 0; i < a.n_jobs; ++i) {
       DenseJob& j = a.job[i];
-      j.packed_g = pieces16<T>(grad_out, p.dim_out, j.g_off, int64_t(j.N) * j.d);
-      j.packed_out = pieces16<T>(a.out, a.ld_out, j.out_off, int64_t(j.N) * j.d);
+      j.packed_g = in_fours<T>(grad_out, p.dim_out, j.g_off, j.N);
+      j.packed_out = in_fours<T>(a.out, a.ld_out, j.out_off, j.N);
+      j.packed_dz = p.gated && in_fours<T>(a.dz, a.n_gates, j.gate0, j.N);
     }
-    const hipError_t he = p.gated ? run_dense<T, kGatedGrad>(a, s) : run_dense<T, kLinearGrad>(a, s);
+    const bool x8 = x.codes != nullptr;
+    auto go = [&](auto codes) {
+      return p.gated ? run_dense<T, kGatedGrad, decltype(codes)::value>(a, s)
+                     : run_dense<T, kLinearGrad, decltype(codes)::value>(a, s);
+    };
+    hipError_t he;
+    if constexpr (sizeof(T) == 4)
+      he = x8 ? go(std::true_type{}) : go(std::false_type{});
+    else
+      he = go(std::false_type{});
     if (he != hipSuccess) return he;
   }
   // rows of the gradient that a map's output segment gets
@@ -821,7 +408,7 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
     DenseArgs a{};
     a.n_rows = n_rows;
     a.out = grad_x;
-    a.ld_out = p.dim_in;
+    a.ld_out = static_cast<int32_t>(p.dim_in);
     for (const DenseMap& m : p.maps) {
       DenseJob& j = a.job[a.n_jobs++];
       j.main.src = grad_rows(m);
@@ -835,8 +422,10 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
         j.gate.src = source_rows<T>(dz, p.n_gates, 0, static_cast<int32_t>(p.n_gates), 1);
         j.gate.weights = gate_weights;
         j.gate.ldw = static_cast<int32_t>(p.n_gates);
+        j.gate.packed = pieces16<T>(gate_weights, p.n_gates, 0, 0);
       }
-      j.packed_out = pieces16<T>(grad_x, p.dim_in, m.in_off, int64_t(m.mul_in) * m.d);
+      j.main.packed = pieces16<T>(j.main.weights, m.mul_out, 0, 0);
+      j.packed_out = in_fours<T>(grad_x, p.dim_in, m.in_off, m.mul_in);
     }
     if (p.gated && !p.even_out) {  // the even scalars reach the gates alone
       DenseJob& j = a.job[a.n_jobs++];
@@ -847,9 +436,10 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
       j.N = p.scalar_mul;
       j.out_off = p.scalar_off;
       j.bias = -1;
-      j.packed_out = pieces16<T>(grad_x, p.dim_in, p.scalar_off, p.scalar_mul);
+      j.main.packed = pieces16<T>(gate_weights, p.n_gates, 0, 0);
+      j.packed_out = in_fours<T>(grad_x, p.dim_in, p.scalar_off, p.scalar_mul);
     }
-    hipError_t he = run_dense<T, kTransposed>(a, s);
+    hipError_t he = run_dense<T, kTransposed, false>(a, s);
     if (he != hipSuccess) return he;
     for (const ColumnRun& r : p.bare_in) {
       const int64_t b = (n_rows * r.len + 255) / 256;
@@ -901,10 +491,10 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
   }
   join.n_jobs = a.n_jobs;
   if (a.n_jobs == 0) return hipSuccess;
-  in_launches(blocks, 256, [&](int64_t block0, unsigned n) {
-    a.block0 = static_cast<int32_t>(block0);
-    hipLaunchKernelGGL(k_param<T>, dim3(n), dim3(256), lds, s, a);
-  });
+  auto* f = k_param<T, false>;
+  if constexpr (sizeof(T) == 4)
+    if (x.codes != nullptr) f = k_param<T, true>;
+  hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves), lds, s, a);
   hipError_t he = hipGetLastError();
   if (he != hipSuccess || h.single) return he;
   hipLaunchKernelGGL(k_param_join<T>, dim3(static_cast<unsigned>(joins)), dim3(1024), 0, s, join,
@@ -913,6 +503,9 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
 }
 
 }  // namespace
+}  // namespace dense
+
+using namespace dense;
 
 size_t dense_workspace(const Dense& p, int64_t n_rows) {
   return p.f64 ? dense_space<double>(p, n_rows).total : dense_space<float>(p, n_rows).total;

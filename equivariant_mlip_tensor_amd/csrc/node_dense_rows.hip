@@ -1,0 +1,29 @@
+// node_dense_rows.hip -- the products of node_dense.hpp for one data type and
+// mode (TPCONV_DOUBLE, TPCONV_MODE), so that they compile side by side.
+#include "node_dense.hpp"
+
+namespace tpconv {
+namespace dense {
+
+template <class T, int MODE, bool X8>
+hipError_t run_dense(DenseArgs& a, hipStream_t s) {
+  if (a.n_rows == 0 || a.n_jobs == 0) return hipSuccess;
+  int widest = 1;
+  for (int i = 0; i < a.n_jobs; ++i) widest = std::max({widest, a.job[i].N, a.job[i].main.src.K, a.job[i].gate.src.K});
+  if (widest <= 16) return launch_jobs<T, 16, MODE, X8>(a, s);
+  if (widest <= 32 || sizeof(T) == 8) return launch_jobs<T, 32, MODE, X8>(a, s);
+  return launch_jobs<T, sizeof(T) == 4 ? 64 : 32, MODE, X8>(a, s);
+}
+
+#if TPCONV_DOUBLE
+using Real = double;
+#else
+using Real = float;
+#endif
+template hipError_t run_dense<Real, TPCONV_MODE, false>(DenseArgs&, hipStream_t);
+#if !TPCONV_DOUBLE && (TPCONV_MODE == 2 || TPCONV_MODE == 3)
+template hipError_t run_dense<Real, TPCONV_MODE, true>(DenseArgs&, hipStream_t);
+#endif
+
+}  // namespace dense
+}  // namespace tpconv
