@@ -598,7 +598,7 @@ __device__ __forceinline__ void run_job(const DenseArgs& a, const DenseJob& j, i
 }
 
 template <class T, int C, int MODE, bool X8>
-__global__ __launch_bounds__(64 * kWaves, 2) void k_dense(DenseArgs a) {
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && MODE != kGatedGrad ? 3 : 2) void k_dense(DenseArgs a) {
   extern __shared__ char dynamic[];
   int ji = 0;
   while (ji + 1 < a.n_jobs && static_cast<int>(blockIdx.x) >= a.job[ji + 1].first) ++ji;
@@ -623,8 +623,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_dense(DenseArgs a) {
 }
 
 // -------------------------------------------------------------------- host
-// Blocks of a launch: three for each CU where there are tiles enough.
-constexpr int64_t kDenseBlocks = 768;
+// Blocks of a launch, two for each that a CU holds at a time (28000 rows of 64 channels l <= 3, linear and its
+// transposed products: 512 blocks 109 and 87 us, 768: 95 and 77, 1024: 95 and 76, 1536: 88 and 74).
+constexpr int64_t kDenseBlocks = 1536;
 
 // Blocks of the jobs, LDS and launch; the jobs' sizes and terms are set.
 template <class T, int C, int MODE, bool X8>

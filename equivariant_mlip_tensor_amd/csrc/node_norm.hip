@@ -11,11 +11,14 @@
 // the rows they take, so a column's segment and channel are found once, gamma
 // stays in registers, and grad_gamma is summed in registers down the rows.
 // Rows of up to 256 pieces (16 bytes, or single elements where a segment does
-// not start at a multiple of one) are held by 1 to 64 lanes of a wavefront, and
-// longer ones by a block.
-// Sums run in 64 bits for both types: squares of any fp32 value fit, and the
-// gradient's difference keeps what fp32 would cancel in a segment of one or two
-// columns.
+// not start at a multiple of one; the gradient: 128) are held by 1 to 64 lanes
+// of a wavefront, and longer ones by a block.
+// Sums, and the factors formed of them, run in 64 bits for both types, so that
+// squares of any fp32 value fit.
+// 28000 fp32 rows of 1024 with a residual: 78 us (459 MB, 5.9 TB/s); the gradient
+// 112 us (459 MB, 4.1 TB/s), joining grad_gamma's parts 10; into 8 bits 39 us (143
+// MB, latency of the maxima), back 24 us (6.0 TB/s).  4096 rows of 512 with codes:
+// 12 us.  16 fp64 rows of 16: 2.5 and 4.4 us (latency).
 #include <hip/hip_runtime.h>
 
 #include "node_device.hpp"
@@ -26,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostBlocks = 1024;      // 4 blocks for each CU
-constexpr int kMostGradBlocks = 768;
+constexpr int kMostGradBlocks = 2048;
 
 // What a lane keeps of its pieces' columns.
 template <class T, int PER, int NP>
@@ -53,6 +56,17 @@ struct Columns {
   }
 };
 
+// A column's place in a row (bytes) that the compiler takes for new: the row's
+// start stays in scalar registers and the place beside it, where pointers of
+// every piece of every array, carried from row to row, took 64 registers (and
+// gamma's pieces, loaded ahead of the loop, spilled).
+template <class T>
+__device__ __forceinline__ uint32_t place_of(int col) {
+  uint32_t at = static_cast<uint32_t>(col) * sizeof(T);
+  asm volatile("" : "+v"(at));
+  return at;
+}
+
 template <class T, int PER, int NP>
 __device__ __forceinline__ void load_row(T (&v)[NP][PER], const T* row, const int (&col)[NP]) {
   struct alignas(PER * sizeof(T)) Piece {
@@ -61,10 +75,21 @@ __device__ __forceinline__ void load_row(T (&v)[NP][PER], const T* row, const in
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
     Piece p = {};
-    if (col[j] >= 0) p = *reinterpret_cast<const Piece*>(row + col[j]);
+    if (col[j] >= 0) p = *reinterpret_cast<const Piece*>(reinterpret_cast<const char*>(row) + place_of<T>(col[j]));
 #pragma unroll
     for (int e = 0; e < PER; ++e) v[j][e] = p.v[e];
   }
+}
+
+// A piece of a row in LDS.
+template <class T, int PER>
+__device__ __forceinline__ void load_piece(T (&v)[PER], const T* row, int col) {
+  struct alignas(PER * sizeof(T)) Piece {
+    T v[PER];
+  };
+  const Piece p = *reinterpret_cast<const Piece*>(reinterpret_cast<const char*>(row) + place_of<T>(col < 0 ? 0 : col));
+#pragma unroll
+  for (int e = 0; e < PER; ++e) v[e] = p.v[e];
 }
 
 template <class T, int PER, int NP>
@@ -78,23 +103,39 @@ __device__ __forceinline__ void store_row(const T (&v)[NP][PER], T* row, const i
       Piece p;
 #pragma unroll
       for (int e = 0; e < PER; ++e) p.v[e] = v[j][e];
-      *reinterpret_cast<Piece*>(row + col[j]) = p;
+      *reinterpret_cast<Piece*>(reinterpret_cast<char*>(row) + place_of<T>(col[j])) = p;
     }
+}
+
+// Sums over the 16 lanes of a row of lanes by moves on the vector units: with
+// the lane next to it, the pair, the four and the eight beside it.
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
 
 // Reductions over a row's lanes; every lane gets the result.  ALL: the row is
 // a block's (sums by wavefront pass through LDS, added in order), else `lanes`
 // neighbours' of a wavefront.
-template <bool ALL>
+template <bool ALL, bool FULL>  // FULL: of whole wavefronts
 struct Team {
   int lanes;
   double* lds;  // ALL: two sets of 32 segments' sums of each wavefront
 
   template <class V, class F>
   __device__ __forceinline__ V wave(V v, F&& f) const {
-    if (ALL) {
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) v = f(v, __shfl_xor(v, o, 64));
+    if constexpr (FULL) {
+      v = f(v, moved<0xB1>(v));
+      v = f(v, moved<0x4E>(v));
+      v = f(v, moved<0x141>(v));
+      v = f(v, moved<0x140>(v));
+      v = f(v, __shfl_xor(v, 16, 64));
+      v = f(v, __shfl_xor(v, 32, 64));
     } else {
       for (int o = 1; o < lanes; o <<= 1) v = f(v, __shfl_xor(v, o, 64));
     }
@@ -107,14 +148,14 @@ struct Team {
 
 // r of a segment's or row's mean square: the root's error is a few units of 64
 // bits, so r itself is next to exact in fp32 and within 3 units in fp64.
-__device__ __forceinline__ double inverse_root(double ms, double eps) { return 1.0 / sqrt(ms + eps); }
+__device__ __forceinline__ double inverse_root(double ms, double eps) { return rsqrt(ms + eps); }
 
 __device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Sums over what is normalised together of up to N values of each piece; for
 // each piece, its segment's or row's sums.
 template <bool ALL, int NP, int N>
-__device__ __forceinline__ void together(const Team<ALL>& team, const NormArgs& a, const int (&seg)[NP],
+__device__ __forceinline__ void together(const Team<ALL, (NP > 1)>& team, const NormArgs& a, const int (&seg)[NP],
                                          const double (&v)[N][NP], double (&total)[N][NP]) {
   const int groups = a.row_scope ? 1 : a.n_segs;
   const int w = threadIdx.x >> 6, nw = blockDim.x >> 6;
@@ -158,7 +199,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&v)[4]) {
 }
 
 template <bool ALL, int PER, int NP>
-__device__ __forceinline__ void write_codes(const Team<ALL>& team, const NormArgs& a,
+__device__ __forceinline__ void write_codes(const Team<ALL, (NP > 1)>& team, const NormArgs& a,
                                             const Columns<float, PER, NP>& cols, const float (&y)[NP][PER],
                                             uint8_t* codes, float* scales) {
   // magnitudes are compared as whole numbers: NaN is above infinity, so it is not lost
@@ -210,19 +251,27 @@ __device__ __forceinline__ void write_codes(const Team<ALL>& team, const NormArg
   }
 }
 
+// The first row of this thread's lanes and, with more than one piece a lane
+// (a wavefront's or block's lanes all have it), the same for all of them.
+template <int NP>
+__device__ __forceinline__ int first_row(int rows_of_block, int lanes) {
+  const int row = static_cast<int>(blockIdx.x) * rows_of_block + static_cast<int>(threadIdx.x) / lanes;
+  return NP > 1 ? __builtin_amdgcn_readfirstlane(row) : row;
+}
+
 // ------------------------------------------------------------------ forward
 // NORM: y is the norm of h; without it, h itself (rows into 8 bits alone).
 template <class T, int PER, int NP, bool ALL, int THREADS, bool NORM>
 __global__ __launch_bounds__(THREADS) void k_norm(NormArgs a, const T* x, const T* residual, const T* gamma, T* sum,
                                                   T* out, uint8_t* codes, float* scales) {
   __shared__ double lds[ALL ? kMaxNormSegs * (THREADS / 64) : 1];
-  const int lanes = ALL ? THREADS : a.lanes;
+  const int lanes = ALL ? THREADS : (NP > 1 ? 64 : a.lanes);
   const int lane = ALL ? threadIdx.x : threadIdx.x & (lanes - 1);
-  const Team<ALL> team{lanes, lds};
+  const Team<ALL, (NP > 1)> team{lanes, lds};
   Columns<T, PER, NP> cols;
   cols.find(a, lane, lanes, gamma);
-  const int64_t teams = int64_t(gridDim.x) * (THREADS / lanes);
-  for (int64_t row = int64_t(blockIdx.x) * (THREADS / lanes) + threadIdx.x / lanes; row < a.n_rows; row += teams) {
+  const int teams = static_cast<int>(gridDim.x) * (THREADS / lanes);
+  for (int64_t row = first_row<NP>(THREADS / lanes, lanes); row < a.n_rows; row += teams) {
     const int64_t at = row * a.dim;
     T h[NP][PER];
     load_row(h, x + at, cols.col);
@@ -266,48 +315,58 @@ template <class T, int PER, int NP, bool ALL, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_norm_grad(NormArgs a, const T* h_rows, const T* gamma, const T* grad_out,
                                                        const T* grad_sum, T* grad_x, T* grad_gamma, T* part) {
   __shared__ double lds[ALL ? 2 * kMaxNormSegs * (THREADS / 64) : 1];
-  extern __shared__ char dynamic[];  // column sums, where wavefronts hold rows
-  const int lanes = ALL ? THREADS : a.lanes;
+  extern __shared__ char dynamic[];  // gamma by column (in registers it takes a fifth of them); then column sums,
+                                     // where wavefronts hold rows
+  const int lanes = ALL ? THREADS : (NP > 1 ? 64 : a.lanes);
   const int lane = ALL ? threadIdx.x : threadIdx.x & (lanes - 1);
-  const Team<ALL> team{lanes, lds};
+  const Team<ALL, (NP > 1)> team{lanes, lds};
   Columns<T, PER, NP> cols;
-  cols.find(a, lane, lanes, gamma);
+  cols.find(a, lane, lanes, nullptr);
+  T* const weight = reinterpret_cast<T*>(dynamic);
+  for (int s = 0; s < a.n_segs; ++s)
+    for (int c = a.seg[s].off + threadIdx.x; c < a.seg[s].end; c += THREADS)
+      weight[c] = gamma != nullptr ? gamma[a.seg[s].channel + (c - a.seg[s].off) / a.seg[s].d] : T(1);
+  __syncthreads();
   T mine[NP][PER];
 #pragma unroll
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int e = 0; e < PER; ++e) mine[j][e] = 0;
-  const int64_t teams = int64_t(gridDim.x) * (THREADS / lanes);
-  for (int64_t row = int64_t(blockIdx.x) * (THREADS / lanes) + threadIdx.x / lanes; row < a.n_rows; row += teams) {
+  const int teams = static_cast<int>(gridDim.x) * (THREADS / lanes);
+  for (int64_t row = first_row<NP>(THREADS / lanes, lanes); row < a.n_rows; row += teams) {
     const int64_t at = row * a.dim;
     T h[NP][PER], g[NP][PER], more[NP][PER];
     load_row(h, h_rows + at, cols.col);
     load_row(g, grad_out + at, cols.col);
-    if (grad_sum != nullptr) load_row(more, grad_sum + at, cols.col);
     double v[2][NP], total[2][NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       double q = 0, p = 0;
+      T gamma[PER];
+      load_piece(gamma, weight, cols.col[j]);
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         const double he = h[j][e];
         q = fma(he, he, q);
-        p = fma(he, double(g[j][e]) * double(cols.gamma[j][e]), p);
+        p = fma(he, double(g[j][e]) * double(gamma[e]), p);
       }
       v[0][j] = cols.col[j] >= 0 ? q * cols.share[j] : 0.0;
       v[1][j] = cols.col[j] >= 0 ? p : 0.0;
       total[0][j] = total[1][j] = 0;
     }
     together<ALL, NP, 2>(team, a, cols.seg, v, total);
+    if (grad_sum != nullptr) load_row(more, grad_sum + at, cols.col);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const double r = inverse_root(total[0][j], a.eps);
-      const double c = total[1][j] * r * r * cols.share[j];
+      const T pull = static_cast<T>(total[1][j] * r * cols.share[j]), by = static_cast<T>(r);
+      T gamma[PER];
+      load_piece(gamma, weight, cols.col[j]);
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const double he = h[j][e], ge = g[j][e];
-        mine[j][e] += static_cast<T>(ge * (he * r));
-        h[j][e] = static_cast<T>(r * (ge * double(cols.gamma[j][e]) - he * c));
+        const T u = static_cast<T>(double(h[j][e]) * r);
+        mine[j][e] = fma(g[j][e], u, mine[j][e]);
+        h[j][e] = by * fma(-u, pull, g[j][e] * gamma[e]);
         if (grad_sum != nullptr) h[j][e] += more[j][e];
       }
     }
@@ -319,6 +378,7 @@ __global__ __launch_bounds__(THREADS) void k_norm_grad(NormArgs a, const T* h_ro
     return;
   }
   // the wavefront's groups of lanes, then the block's wavefronts, in order
+  __syncthreads();  // gamma is read
   T* const sums = reinterpret_cast<T*>(dynamic);
   const int w = threadIdx.x >> 6;
 #pragma unroll
@@ -351,33 +411,35 @@ __global__ __launch_bounds__(THREADS) void k_norm_grad(NormArgs a, const T* h_ro
 }
 
 // The blocks' column sums, added in order: a block takes as many whole channels
-// of a segment as 64 columns hold, its wavefronts every 16th row of sums.
+// of a segment as 16 columns hold, a row of 16 lanes every 64th row of sums.
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a, int blocks, const T* __restrict__ part,
                                                     T* __restrict__ grad_gamma) {
-  __shared__ double sums[16][64];
+  __shared__ double sums[64][16];
   int s = 0, b = blockIdx.x;
   for (; s < a.n_segs; ++s) {
-    const int per = 64 / a.seg[s].d, mul = (a.seg[s].end - a.seg[s].off) / a.seg[s].d, n = (mul + per - 1) / per;
+    const int per = 16 / a.seg[s].d, mul = (a.seg[s].end - a.seg[s].off) / a.seg[s].d, n = (mul + per - 1) / per;
     if (b < n) break;
     b -= n;
   }
   const NormSeg g = a.seg[s];
-  const int per = 64 / g.d, u0 = b * per, mul = (g.end - g.off) / g.d;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int per = 16 / g.d, u0 = b * per, mul = (g.end - g.off) / g.d;
+  const int lane = threadIdx.x & 15, w = threadIdx.x >> 4;
   const int c = g.off + u0 * g.d + lane;
   double v = 0;
   if (lane < per * g.d && c < g.end) {
 #pragma unroll 8
-    for (int q = w; q < blocks; q += 16) v += double(part[int64_t(q) * a.dim + c]);
+    for (int q = w; q < blocks; q += 64) v += double(part[int64_t(q) * a.dim + c]);
   }
   sums[w][lane] = v;
   __syncthreads();
-  if (w == 0) {
+  if (w < 4) {  // 4 rows of lanes take 16 sums each
     v = 0;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) v += sums[q][lane];
-    sums[0][lane] = v;
+    for (int q = 0; q < 16; ++q) v += sums[16 * w + q][lane];
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+    sums[w][lane] = v;
   }
   __syncthreads();
   if (threadIdx.x < per && u0 + int(threadIdx.x) < mul) {
@@ -395,8 +457,8 @@ __global__ __launch_bounds__(THREADS) void k_unpack8(NormArgs a, const uint8_t* 
   const int lanes = a.lanes, lane = threadIdx.x & (lanes - 1);
   Columns<float, PER, NP> cols;
   cols.find(a, lane, lanes, nullptr);
-  const int64_t teams = int64_t(gridDim.x) * (THREADS / lanes);
-  for (int64_t row = int64_t(blockIdx.x) * (THREADS / lanes) + threadIdx.x / lanes; row < a.n_rows; row += teams) {
+  const int teams = static_cast<int>(gridDim.x) * (THREADS / lanes);
+  for (int64_t row = first_row<NP>(THREADS / lanes, lanes); row < a.n_rows; row += teams) {
     const int64_t at = row * a.dim;
     float v[NP][PER];
 #pragma unroll
@@ -430,20 +492,24 @@ bool in_pieces(const NormArgs& a) {
 }
 
 // How a row's pieces are spread: lanes of a wavefront (a power of two), or a
-// block's threads, and pieces a lane.
+// block's threads, and pieces a lane (two, as far as 1024 threads reach).
 struct Spread {
   int lanes, np;
   bool all;
 };
-Spread spread(int pieces) {
+Spread spread(int pieces, bool grad) {
   if (pieces <= 64) {
     int l = 1;
     while (l < pieces) l *= 2;
     return {l, 1, false};
   }
-  if (pieces <= 256) return {64, pieces <= 128 ? 2 : 4, false};
-  if (pieces <= 2048) return {256, pieces <= 1024 ? 4 : 8, true};
-  return {1024, 8, true};
+  if (pieces <= 128) return {64, 2, false};
+  // the gradient holds three rows: a wavefront's registers do not (28000 rows of 1024: 170 us, 112 by two wavefronts;
+  // the norm itself 78)
+  if (pieces <= 256 && !grad) return {64, 4, false};
+  int threads = 128;
+  while (threads < 1024 && 2 * threads < pieces) threads *= 2;
+  return {threads, pieces <= 2048 ? 2 : (pieces <= 4096 ? 4 : 8), true};
 }
 
 int64_t blocks_of(const Spread& sp, int64_t n_rows, int most) {
@@ -452,24 +518,36 @@ int64_t blocks_of(const Spread& sp, int64_t n_rows, int most) {
   return b < 1 ? 1 : (b > most ? most : b);
 }
 
-// f(pieces of 16 bytes?, NP, ALL, THREADS) as constants
-template <class T, class F>
+// f(elements of a piece, NP, ALL, THREADS) as constants
+template <class T, bool GRAD, class F>
 hipError_t dispatch(bool vec, const Spread& sp, F&& f) {
-  using std::integral_constant;
   auto at = [&](auto per) -> hipError_t {
+    constexpr int kMost = TPCONV_MAX_NORM_DIM / decltype(per)::value;  // pieces
     auto go = [&](auto np, auto all, auto threads) { return f(per, np, all, threads); };
-    using I = integral_constant<int, 256>;
+    using std::integral_constant;
+    using N2 = integral_constant<int, 2>;
+    using N4 = integral_constant<int, 4>;
+    using Wave = std::false_type;
+    using Block = std::true_type;
+    using Quarter = integral_constant<int, kThreads>;
     if (!sp.all) {
-      if (sp.np == 1) return go(integral_constant<int, 1>{}, std::false_type{}, I{});
-      if (sp.np == 2) return go(integral_constant<int, 2>{}, std::false_type{}, I{});
-      return go(integral_constant<int, 4>{}, std::false_type{}, I{});
+      if (sp.np == 1) return go(integral_constant<int, 1>{}, Wave{}, Quarter{});
+      if constexpr (!GRAD)
+        if (sp.np == 4) return go(N4{}, Wave{}, Quarter{});
+      return go(N2{}, Wave{}, Quarter{});
     }
-    if (sp.lanes == 1024) return go(integral_constant<int, 8>{}, std::true_type{}, integral_constant<int, 1024>{});
-    if (sp.np == 4) return go(integral_constant<int, 4>{}, std::true_type{}, I{});
-    return go(integral_constant<int, 8>{}, std::true_type{}, I{});
+    if constexpr (kMost > 4096)
+      if (sp.np == 8) return go(integral_constant<int, 8>{}, Block{}, integral_constant<int, 1024>{});
+    if constexpr (kMost > 2048)
+      if (sp.np == 4) return go(N4{}, Block{}, integral_constant<int, 1024>{});
+    if constexpr (GRAD)
+      if (sp.lanes == 128) return go(N2{}, Block{}, integral_constant<int, 128>{});
+    if (sp.lanes == 256) return go(N2{}, Block{}, Quarter{});
+    if (sp.lanes == 512) return go(N2{}, Block{}, integral_constant<int, 512>{});
+    return go(N2{}, Block{}, integral_constant<int, 1024>{});
   };
-  if (vec) return at(integral_constant<int, 16 / sizeof(T)>{});
-  return at(integral_constant<int, 1>{});
+  if (vec) return at(std::integral_constant<int, 16 / sizeof(T)>{});
+  return at(std::integral_constant<int, 1>{});
 }
 
 bool all_aligned(std::initializer_list<const void*> ptrs) {
@@ -483,9 +561,9 @@ hipError_t forward(NormArgs a, const T* x, const T* residual, const T* gamma, T*
                    float* scales, hipStream_t s) {
   const bool vec = in_pieces<T>(a) && all_aligned({x, residual, sum, out}) &&
                    reinterpret_cast<uintptr_t>(codes) % 4 == 0;
-  const Spread sp = spread(vec ? a.dim * int(sizeof(T)) / 16 : a.dim);
+  const Spread sp = spread(vec ? a.dim * int(sizeof(T)) / 16 : a.dim, false);
   a.lanes = sp.lanes;
-  return dispatch<T>(vec, sp, [&](auto per, auto np, auto all, auto threads) {
+  return dispatch<T, false>(vec, sp, [&](auto per, auto np, auto all, auto threads) {
     hipLaunchKernelGGL((k_norm<T, per.value, np.value, all.value, threads.value, NORM>),
                        dim3(static_cast<unsigned>(blocks_of(sp, a.n_rows, kMostBlocks))), dim3(threads.value), 0, s, a,
                        x, residual, gamma, sum, out, codes, scales);
@@ -497,12 +575,12 @@ template <class T>
 hipError_t backward(NormArgs a, const T* h, const T* gamma, const T* grad_out, const T* grad_sum, T* grad_x,
                     T* grad_gamma, T* part, hipStream_t s) {
   const bool vec = in_pieces<T>(a) && all_aligned({h, grad_out, grad_sum, grad_x});
-  const Spread sp = spread(vec ? a.dim * int(sizeof(T)) / 16 : a.dim);
+  const Spread sp = spread(vec ? a.dim * int(sizeof(T)) / 16 : a.dim, true);
   a.lanes = sp.lanes;
   const int64_t blocks = blocks_of(sp, a.n_rows, kMostGradBlocks);
   if (blocks == 1 && !sp.all) part = nullptr;
-  const hipError_t he = dispatch<T>(vec, sp, [&](auto per, auto np, auto all, auto threads) {
-    const size_t lds = all.value || grad_gamma == nullptr ? 0 : sizeof(T) * (threads.value / 64) * a.dim;
+  const hipError_t he = dispatch<T, true>(vec, sp, [&](auto per, auto np, auto all, auto threads) {
+    const size_t lds = sizeof(T) * (all.value ? 1 : threads.value / 64) * a.dim;
     hipLaunchKernelGGL((k_norm_grad<T, per.value, np.value, all.value, threads.value>),
                        dim3(static_cast<unsigned>(blocks)), dim3(threads.value), lds, s, a, h, gamma, grad_out,
                        grad_sum, grad_x, grad_gamma, part);
@@ -511,7 +589,7 @@ hipError_t backward(NormArgs a, const T* h, const T* gamma, const T* grad_out, c
   if (he != hipSuccess || grad_gamma == nullptr || part == nullptr) return he;
   int join = 0;
   for (int i = 0; i < a.n_segs; ++i) {
-    const int per = 64 / a.seg[i].d, mul = (a.seg[i].end - a.seg[i].off) / a.seg[i].d;
+    const int per = 16 / a.seg[i].d, mul = (a.seg[i].end - a.seg[i].off) / a.seg[i].d;
     join += (mul + per - 1) / per;
   }
   hipLaunchKernelGGL(k_norm_join<T>, dim3(static_cast<unsigned>(join)), dim3(1024), 0, s, a,
@@ -556,9 +634,9 @@ hipError_t launch_pack8(const NormArgs& a, const float* x, uint8_t* codes, float
 
 hipError_t launch_unpack8(NormArgs a, const uint8_t* codes, const float* scales, float* x, hipStream_t s) {
   const bool vec = in_pieces<float>(a) && aligned16(x) && reinterpret_cast<uintptr_t>(codes) % 4 == 0;
-  const Spread sp = spread(vec ? a.dim / 4 : a.dim);
+  const Spread sp = spread(vec ? a.dim / 4 : a.dim, false);
   a.lanes = sp.lanes;
-  return dispatch<float>(vec, sp, [&](auto per, auto np, auto, auto threads) {
+  return dispatch<float, false>(vec, sp, [&](auto per, auto np, auto, auto threads) {
     hipLaunchKernelGGL((k_unpack8<per.value, np.value, threads.value>),
                        dim3(static_cast<unsigned>(blocks_of(sp, a.n_rows, 2 * kMostBlocks))), dim3(threads.value), 0, s,
                        a, codes, scales, x);

@@ -7,10 +7,12 @@ Bounds, entry by entry, with eps the unit roundoff of the data type (2^-24,
 absolute values, in whatever order it is taken.
 
 Norm: the oracle is given the kernel's own sum h (which is checked bit by bit).
-Sums over h and what is formed of them run in 64 bits, where a sum over `width`
-columns errs by at most (width + 32) 2^-53 of its absolute values with the few
-steps after it; an fp32 result rounds that once, and gamma's or grad_sum's part
-once more.
+Sums over h and the factors formed of them run in 64 bits, where a sum over
+`width` columns errs by at most (width + 32) 2^-53 of its absolute values; an
+fp32 result y rounds that once, and gamma's part once more.  In the fp32
+gradient r (w - u k) + grad_sum, k = sum_i w_i u_i / columns: w rounds once, u, k
+and r once each, their difference, the product with r and the last sum once each,
+so it is within 5 eps of the same with plus, and eps of itself.
 
 Activations: with L and B the bounds of an activation's and its slope's growth
 (oracle.block), an argument with error d gives L d and B d, and the evaluation
@@ -74,8 +76,7 @@ def norm_bounds(irreps, scope, dt, h, gamma, G, H, eps):
     grad = (4 * of_r + (0 if dt == "f32" else (width + 8) * e)) * size[0]
     if dt == "f32":
         exact = ob.norm_backward(irreps, scope, eps, h, gamma, G, H)[0]
-        plain = exact - (0 if H is None else H)
-        grad = 3 * e * (np.abs(exact) + np.abs(plain)) + (width + 32) * 2.0 ** -53 * size[0]
+        grad = 5.1 * e * (size[0] + np.abs(exact))
     return of_r, grad, (len(h) * max(2 * s[1] + 1 for s in segs) + 4) * e * size[1] + of_r * size[1]
 
 
@@ -134,8 +135,7 @@ def test_norm_off_alignment(node, dt):  # noqa: F811
 
 
 def test_norm_extremes(node):  # noqa: F811
-    """Squares that fp32 does not hold, rows far below eps, rows of zeros, segments of one column, where the gradient
-    is what eps leaves of it."""
+    """Squares that fp32 does not hold, rows far below eps, rows of zeros, segments of one column."""
     for scale in (1e30, 3e38 / 60, 1e-20, 1e-30):
         rng = np.random.default_rng(3)
         irreps, n = "1x0e+6x0e+3x1o", 20
@@ -152,8 +152,7 @@ def test_norm_extremes(node):  # noqa: F811
             gx, gg = node.tpconv_norm_backward(plan, h, None, dev(G))
             want = ob.norm_backward(irreps, scope, 1e-6, hh, None, G)
             size = ob.norm_backward(irreps, scope, 1e-6, hh, None, G, size=True)
-            # the difference keeps what 64 bits leave of it
-            within(gx, want[0], 3 * EPS["f32"] * np.abs(want[0]) + 64 * 2.0 ** -53 * size[0] + 2.0 ** -149, "grad_x")
+            within(gx, want[0], 5.1 * EPS["f32"] * (size[0] + np.abs(want[0])) + 2.0 ** -148, "grad_x")
             within(gg, want[1], (4 * n + 12) * EPS["f32"] * size[1], "grad_gamma")
 
 
