@@ -53,6 +53,9 @@ def _jobs():
             units.append((os.path.join(CSRC, "node_dense_rows.hip"),
                           os.path.join(BUILD, f"node_dense_m{mode}_{'f64' if dbl else 'f32'}.o"),
                           [f"-DTPCONV_DOUBLE={dbl}", f"-DTPCONV_MODE={mode}"]))
+    for gated in (1, 0):
+        units.append((os.path.join(CSRC, "node_dense_back.hip"), os.path.join(BUILD, f"node_dense_back{gated}.o"),
+                      [f"-DTPCONV_GATED={gated}"]))
     for stem in ("node_dense", "node_norm", "node_experts", "node_embed", "node_route", "node_dropout"):
         units.append((os.path.join(CSRC, stem + ".hip"), os.path.join(BUILD, stem + ".o"), []))
     # the host CG builder runs without FMA contraction so its run-time values

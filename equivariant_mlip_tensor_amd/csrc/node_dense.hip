@@ -156,13 +156,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_param(ParamArgs a) {
 // The runs' matrices and column sums, added in order in 64 bits: 64 values a
 // block, its 16 wavefronts every 16th run.
 struct JoinJob {
-  int64_t at, numel, sums;  // of a run: first value, matrix, column sums
+  int64_t at, per;          // first value; values of a run
+  int32_t rows, cols, sums; // a matrix, and column sums after it, of those values
+  int32_t ld;               // of the matrix in the gradient
   int32_t runs, first;
   void *matrix, *columns;
 };
 struct JoinArgs {
   int32_t n_jobs;
-  JoinJob job[kMaxMaps + 1];
+  JoinJob job[2 * kMaxMaps];
 };
 
 template <class T>
@@ -170,24 +172,24 @@ __global__ __launch_bounds__(1024) void k_param_join(JoinArgs a, const T* __rest
   __shared__ double sums[16][64];
   int ji = 0;
   while (ji + 1 < a.n_jobs && static_cast<int>(blockIdx.x) >= a.job[ji + 1].first) ++ji;
-  const JoinJob& j = a.job[ji];
+  const JoinJob j = a.job[ji];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t per = j.numel + j.sums, q = int64_t(static_cast<int>(blockIdx.x) - j.first) * 64 + lane;
+  const int q = (static_cast<int>(blockIdx.x) - j.first) * 64 + lane, numel = j.rows * j.cols, held = numel + j.sums;
   double v = 0;
-  if (q < per) {
+  if (q < held) {
 #pragma unroll 4
-    for (int r = w; r < j.runs; r += 16) v += double(part[j.at + r * per + q]);
+    for (int r = w; r < j.runs; r += 16) v += double(part[j.at + r * j.per + q]);
   }
   sums[w][lane] = v;
   __syncthreads();
-  if (w > 0 || q >= per) return;
+  if (w > 0 || q >= held) return;
   v = 0;
 #pragma unroll
   for (int r = 0; r < 16; ++r) v += sums[r][lane];
-  if (q < j.numel) {
-    if (j.matrix != nullptr) static_cast<T*>(j.matrix)[q] = static_cast<T>(v);
+  if (q < numel) {
+    if (j.matrix != nullptr) static_cast<T*>(j.matrix)[q / j.cols * j.ld + q % j.cols] = static_cast<T>(v);
   } else if (j.columns != nullptr) {
-    static_cast<T*>(j.columns)[q - j.numel] = static_cast<T>(v);
+    static_cast<T*>(j.columns)[q - numel] = static_cast<T>(v);
   }
 }
 
@@ -287,6 +289,28 @@ hipError_t dense_forward(const Dense& p, int64_t n_rows, const void* x, const vo
   return p.gated ? run_dense<T, kGated, false>(a, s) : run_dense<T, kLinear, false>(a, s);
 }
 
+}  // namespace
+
+int64_t cut_back(BackArgs& a, int C, bool gated) {
+  int64_t work = 0, parts = 0;
+  auto cost = [&](const BackJob& j) { return j.d + (gated ? 1 : 0); };
+  for (int i = 0; i < a.n_jobs; ++i) work += cost(a.job[i]);
+  int32_t blocks = 0;
+  for (int i = 0; i < a.n_jobs; ++i) {
+    BackJob& j = a.job[i];
+    const int atoms = atoms_of<float>(j.d, C);
+    const int64_t tiles = (a.n_rows + atoms - 1) / atoms;
+    j.first = blocks;
+    j.blocks = static_cast<int32_t>(std::min<int64_t>(tiles, (kBackBlocks * cost(j) + work - 1) / work));
+    blocks += j.blocks;
+    j.at = parts;
+    parts += j.blocks * (int64_t(j.K) * j.N + int64_t(j.K0) * j.N + (gated || (j.d == 1 && j.even) ? j.N : 0));
+  }
+  return parts;
+}
+
+namespace {
+
 // How the atoms of the parameters' jobs are cut into runs: about kParamBlocks
 // blocks of equal work, a run a whole number of stages.
 constexpr int kParamBlocks = 1024;
@@ -336,6 +360,34 @@ struct DenseSpace {
   size_t rows, gates, parts, total;
 };
 
+// Whether the gradients' one pass over the rows takes the plan (its LDS and registers hold 64 channels of l <= 3 in
+// fp32), and with how many channels; 0: it does not.
+int back_channels(const Dense& p) {
+  int most = p.gated ? p.scalar_mul : 1;
+  if (p.f64) return 0;
+  for (const DenseMap& m : p.maps) {
+    if (m.d > 7 || m.mul_in % 4 != 0 || m.mul_out % 4 != 0) return 0;
+    most = std::max({most, m.mul_in, m.mul_out});
+  }
+  return most <= 32 ? 32 : (most <= 64 ? 64 : 0);
+}
+
+// The jobs' sizes for the one pass.
+void back_jobs(const Dense& p, BackArgs& a) {
+  a.n_jobs = 0;
+  for (const DenseMap& m : p.maps) {
+    BackJob& j = a.job[a.n_jobs++];
+    j.d = m.d;
+    j.K = m.mul_in;
+    j.N = m.mul_out;
+    j.K0 = p.gated ? p.scalar_mul : 0;
+    j.x_off = m.in_off;
+    j.gate0 = m.gate;
+    j.act = m.act;
+    j.even = m.even;
+  }
+}
+
 template <class T>
 DenseSpace dense_space(const Dense& p, int64_t n_rows) {
   DenseSpace w{};
@@ -350,9 +402,158 @@ DenseSpace dense_space(const Dense& p, int64_t n_rows) {
     at = align_up(sizeof(T) * static_cast<size_t>(n_rows) * p.scalar_out_mul);
   }
   w.parts = at;
-  if (!h.single) at += align_up(sizeof(T) * static_cast<size_t>(h.total));
-  w.total = at;
+  size_t parts = h.single ? 0 : align_up(sizeof(T) * static_cast<size_t>(h.total));
+  if (const int C = back_channels(p)) {
+    BackArgs a{};
+    a.n_rows = n_rows;
+    back_jobs(p, a);
+    parts = std::max(parts, align_up(sizeof(T) * static_cast<size_t>(cut_back(a, C, p.gated))));
+  }
+  w.total = at + parts;
   return w;
+}
+
+template <class T>
+hipError_t clear_bare(const Dense& p, int64_t n_rows, void* grad_x, hipStream_t s) {
+  for (const ColumnRun& r : p.bare_in) {
+    const int64_t b = (n_rows * r.len + 255) / 256;
+    hipLaunchKernelGGL(k_clear_columns<T>, dim3(static_cast<unsigned>(b > 65536 ? 65536 : b)), dim3(256), 0, s, n_rows,
+                       p.dim_in, r.off, r.len, static_cast<T*>(grad_x));
+    const hipError_t he = hipGetLastError();
+    if (he != hipSuccess) return he;
+  }
+  return hipSuccess;
+}
+
+// A job of the transposed products: grad_x of channels N from rows `src`.
+template <class T>
+void transposed_job(DenseJob& j, const RowSource& src, const void* weights, int32_t ldw, int d, int N, int32_t off,
+                    void* grad_x, int64_t ld) {
+  j.main.src = src;
+  j.main.weights = weights;
+  j.main.ldw = ldw;
+  j.main.packed = pieces16<T>(weights, ldw, 0, 0);
+  j.d = d;
+  j.N = N;
+  j.out_off = off;
+  j.bias = -1;
+  j.packed_out = in_fours<T>(grad_x, ld, off, N);
+}
+
+// Gated: the even scalars' gradient, from their own map's rows (`du`, or none) and the gates'.
+template <class T>
+void even_job(const Dense& p, DenseJob& j, const RowSource* du, const DenseMap* m, const T* dz, const void* weights,
+              const void* gate_weights, void* grad_x) {
+  const RowSource gates = source_rows<T>(dz, p.n_gates, 0, static_cast<int32_t>(p.n_gates), 1);
+  const int32_t ldg = static_cast<int32_t>(p.n_gates);
+  if (du == nullptr) {
+    transposed_job<T>(j, gates, gate_weights, ldg, 1, p.scalar_mul, p.scalar_off, grad_x, p.dim_in);
+    return;
+  }
+  transposed_job<T>(j, *du, static_cast<const T*>(weights) + m->woff, m->mul_out, 1, p.scalar_mul, p.scalar_off, grad_x,
+                    p.dim_in);
+  j.gate.src = gates;
+  j.gate.weights = gate_weights;
+  j.gate.ldw = ldg;
+  j.gate.packed = pieces16<T>(gate_weights, ldg, 0, 0);
+}
+
+// The gradients in one pass over the rows (node_dense_back.hip), where the plan and the rows' places allow it.
+hipError_t back_in_one(const Dense& p, int64_t n_rows, const DenseInput& x, const void* weights,
+                       const void* gate_weights, const void* bias, const void* grad_out, void* grad_x,
+                       void* grad_weights, void* grad_gate_weights, void* grad_bias, char* mem,
+                       const DenseSpace& space, hipStream_t s, bool& done) {
+  using T = float;
+  const int C = back_channels(p);
+  const bool params = grad_weights != nullptr || grad_gate_weights != nullptr || grad_bias != nullptr;
+  // rows alone of a linear map without activation have nothing to share
+  if (C == 0 || n_rows == 0 || (!params && !p.gated && !p.sloped())) return hipSuccess;
+  const bool x8 = x.codes != nullptr;
+  BackArgs a{};
+  a.n_rows = n_rows;
+  back_jobs(p, a);
+  cut_back(a, C, p.gated);
+  bool fits = in_fours<T>(grad_out, p.dim_out, 0, 0) && (grad_x == nullptr || in_fours<T>(grad_x, p.dim_in, 0, 0));
+  for (int i = 0; i < a.n_jobs; ++i) {
+    const DenseMap& m = p.maps[i];
+    BackJob& j = a.job[i];
+    j.main.src = source_of<T>(p, x, m.in_off, m.mul_in, m.d, m.seg_in);
+    j.main.weights = static_cast<const T*>(weights) + m.woff;
+    j.main.ldw = m.mul_out;
+    j.main.packed = pieces16<T>(j.main.weights, m.mul_out, 0, 0);
+    j.g = source_rows<T>(grad_out, p.dim_out, m.out_off, m.mul_out, m.d);
+    j.bias = -1;
+    fits = fits && j.main.src.packed && j.g.packed && m.in_off % 4 == 0;
+    if (p.gated) {
+      j.gate.src = source_of<T>(p, x, p.scalar_off, p.scalar_mul, 1, p.scalar_seg);
+      j.gate.weights = gate_weights;
+      j.gate.ldw = static_cast<int32_t>(p.n_gates);
+      fits = fits && j.gate.src.packed && m.gate % 4 == 0;
+      if (bias != nullptr) j.bias = m.gate;
+    } else if (m.even && bias != nullptr) {
+      j.bias = 0;
+    }
+  }
+  if (!fits) return hipSuccess;
+  done = true;
+  a.ld_x = static_cast<int32_t>(p.dim_in);
+  a.ld_g = static_cast<int32_t>(p.dim_out);
+  a.n_gates = static_cast<int32_t>(p.n_gates);
+  a.n_scalars = p.scalar_out_mul;
+  a.params = params;
+  a.bias = bias;
+  a.grad_x = static_cast<T*>(grad_x);
+  a.du = reinterpret_cast<T*>(mem);
+  a.dz = reinterpret_cast<T*>(mem + space.gates);
+  a.part = reinterpret_cast<T*>(mem + space.parts);
+  hipError_t he = p.gated ? (x8 ? run_back<true, true>(a, C, s) : run_back<true, false>(a, C, s))
+                          : (x8 ? run_back<false, true>(a, C, s) : run_back<false, false>(a, C, s));
+  if (he != hipSuccess) return he;
+  if (grad_x != nullptr) {
+    if (p.gated) {
+      const DenseMap* even = nullptr;
+      for (const DenseMap& m : p.maps)
+        if (m.even) even = &m;
+      RowSource du{};
+      if (even != nullptr) du = source_rows<T>(a.du, p.scalar_out_mul, 0, even->mul_out, 1);
+      DenseArgs t{};
+      t.n_rows = n_rows;
+      t.out = grad_x;
+      t.ld_out = static_cast<int32_t>(p.dim_in);
+      t.n_jobs = 1;
+      even_job<T>(p, t.job[0], even != nullptr ? &du : nullptr, even, a.dz, weights, gate_weights, grad_x);
+      he = run_dense<T, kTransposed, false>(t, s);
+      if (he != hipSuccess) return he;
+    }
+    he = clear_bare<T>(p, n_rows, grad_x, s);
+    if (he != hipSuccess) return he;
+  }
+  if (!params) return hipSuccess;
+  JoinArgs join{};
+  int joins = 0;
+  auto add = [&](const BackJob& j, int64_t at, int rows, int sums, int ld, T* matrix, T* columns) {
+    if (matrix == nullptr && columns == nullptr) return;
+    const int64_t per = int64_t(j.K + j.K0) * j.N + (p.gated || (j.d == 1 && j.even) ? j.N : 0);
+    join.job[join.n_jobs++] = JoinJob{j.at + at, per, rows, j.N, sums, ld, j.blocks, joins, matrix, columns};
+    joins += (rows * j.N + sums + 63) / 64;
+  };
+  for (int i = 0; i < a.n_jobs; ++i) {
+    const BackJob& j = a.job[i];
+    T* const gw = grad_weights != nullptr ? static_cast<T*>(grad_weights) + p.maps[i].woff : nullptr;
+    const int64_t numel = int64_t(j.K) * j.N;
+    if (p.gated) {
+      add(j, 0, j.K, 0, j.N, gw, nullptr);
+      add(j, numel, j.K0, j.N, static_cast<int>(p.n_gates),
+          grad_gate_weights != nullptr ? static_cast<T*>(grad_gate_weights) + j.gate0 : nullptr,
+          grad_bias != nullptr ? static_cast<T*>(grad_bias) + j.gate0 : nullptr);
+    } else {
+      add(j, 0, j.K, j.d == 1 && j.even ? j.N : 0, j.N, gw, j.even ? static_cast<T*>(grad_bias) : nullptr);
+    }
+  }
+  if (joins == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_param_join<T>, dim3(static_cast<unsigned>(joins)), dim3(1024), 0, s, join,
+                     static_cast<const T*>(a.part));
+  return hipGetLastError();
 }
 
 template <class T>
@@ -361,6 +562,12 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
                           void* grad_weights, void* grad_gate_weights, void* grad_bias, void* ws, hipStream_t s) {
   const DenseSpace space = dense_space<T>(p, n_rows);
   char* const mem = static_cast<char*>(ws);
+  if constexpr (sizeof(T) == 4) {
+    bool done = false;
+    const hipError_t he = back_in_one(p, n_rows, x, weights, gate_weights, bias, grad_out, grad_x, grad_weights,
+                                      grad_gate_weights, grad_bias, mem, space, s, done);
+    if (he != hipSuccess || done) return he;
+  }
   // grad_out through the activations: rows (gated), their gates, or the even scalars alone (linear)
   T* const dz = reinterpret_cast<T*>(p.gated ? mem + space.gates : mem);
   const T* du = static_cast<const T*>(grad_out);
@@ -410,44 +617,18 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
     a.out = grad_x;
     a.ld_out = static_cast<int32_t>(p.dim_in);
     for (const DenseMap& m : p.maps) {
-      DenseJob& j = a.job[a.n_jobs++];
-      j.main.src = grad_rows(m);
-      j.main.weights = static_cast<const T*>(weights) + m.woff;
-      j.main.ldw = m.mul_out;
-      j.d = m.d;
-      j.N = m.mul_in;
-      j.out_off = m.in_off;
-      j.bias = -1;
-      if (p.gated && m.even) {
-        j.gate.src = source_rows<T>(dz, p.n_gates, 0, static_cast<int32_t>(p.n_gates), 1);
-        j.gate.weights = gate_weights;
-        j.gate.ldw = static_cast<int32_t>(p.n_gates);
-        j.gate.packed = pieces16<T>(gate_weights, p.n_gates, 0, 0);
-      }
-      j.main.packed = pieces16<T>(j.main.weights, m.mul_out, 0, 0);
-      j.packed_out = in_fours<T>(grad_x, p.dim_in, m.in_off, m.mul_in);
+      const RowSource src = grad_rows(m);
+      if (p.gated && m.even)
+        even_job<T>(p, a.job[a.n_jobs++], &src, &m, dz, weights, gate_weights, grad_x);
+      else
+        transposed_job<T>(a.job[a.n_jobs++], src, static_cast<const T*>(weights) + m.woff, m.mul_out, m.d, m.mul_in,
+                          m.in_off, grad_x, p.dim_in);
     }
-    if (p.gated && !p.even_out) {  // the even scalars reach the gates alone
-      DenseJob& j = a.job[a.n_jobs++];
-      j.main.src = source_rows<T>(dz, p.n_gates, 0, static_cast<int32_t>(p.n_gates), 1);
-      j.main.weights = gate_weights;
-      j.main.ldw = static_cast<int32_t>(p.n_gates);
-      j.d = 1;
-      j.N = p.scalar_mul;
-      j.out_off = p.scalar_off;
-      j.bias = -1;
-      j.main.packed = pieces16<T>(gate_weights, p.n_gates, 0, 0);
-      j.packed_out = in_fours<T>(grad_x, p.dim_in, p.scalar_off, p.scalar_mul);
-    }
+    if (p.gated && !p.even_out)  // the even scalars reach the gates alone
+      even_job<T>(p, a.job[a.n_jobs++], nullptr, nullptr, dz, weights, gate_weights, grad_x);
     hipError_t he = run_dense<T, kTransposed, false>(a, s);
+    if (he == hipSuccess) he = clear_bare<T>(p, n_rows, grad_x, s);
     if (he != hipSuccess) return he;
-    for (const ColumnRun& r : p.bare_in) {
-      const int64_t b = (n_rows * r.len + 255) / 256;
-      hipLaunchKernelGGL(k_clear_columns<T>, dim3(static_cast<unsigned>(b > 65536 ? 65536 : b)), dim3(256), 0, s, n_rows,
-                         p.dim_in, r.off, r.len, static_cast<T*>(grad_x));
-      he = hipGetLastError();
-      if (he != hipSuccess) return he;
-    }
   }
   if (grad_weights == nullptr && grad_gate_weights == nullptr && grad_bias == nullptr) return hipSuccess;
   const ParamShape h = param_shape<T>(p, n_rows);
@@ -485,7 +666,7 @@ hipError_t dense_backward(const Dense& p, int64_t n_rows, const DenseInput& x, c
     j.sums = sums;
     blocks += int64_t(h.nu[i]) * h.nv[i] * h.runs[i];
     JoinJob& q = join.job[a.n_jobs++];
-    q = JoinJob{h.at[i], int64_t(h.U[i]) * h.V[i], h.sums[i] ? h.V[i] : 0, h.runs[i], joins, matrix, sums};
+    q = JoinJob{h.at[i], h.per[i], h.U[i], h.V[i], h.sums[i] ? h.V[i] : 0, h.V[i], h.runs[i], joins, matrix, sums};
     joins += static_cast<int>((h.per[i] + 63) / 64);
     lds = std::max(lds, sizeof(T) * 2 * stage_atoms(j.d) * (tile_side<T>() * j.d + 16));
   }

@@ -371,16 +371,16 @@ struct LanePart {
   int n;            // row of the weights
   T bias[4];
 
-  __device__ __forceinline__ LanePart(const Place& p, const DenseArgs& a, const DenseJob& j, int n0) {
+  __device__ __forceinline__ LanePart(const Place& p, int n0, int N, const void* first_bias) {
     i16 = p.lane & 15;
     g4 = p.lane >> 4;
     wa = p.wave / (C / 16);
     const int n16 = n0 + 16 * (p.wave % (C / 16));
     c0 = n16 + 4 * g4;
-    there = min(4, j.N - c0);
-    n = min(n16 + (sizeof(T) == 8 ? 4 * (i16 % 4) + i16 / 4 : i16), j.N - 1);
+    there = min(4, N - c0);
+    n = min(n16 + (sizeof(T) == 8 ? 4 * (i16 % 4) + i16 / 4 : i16), N - 1);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) bias[q] = j.bias >= 0 && q < there ? static_cast<const T*>(a.bias)[j.bias + c0 + q] : T(0);
+    for (int q = 0; q < 4; ++q) bias[q] = first_bias != nullptr && q < there ? static_cast<const T*>(first_bias)[c0 + q] : T(0);
   }
 };
 
@@ -481,7 +481,7 @@ __device__ __forceinline__ void whole_job(const DenseArgs& a, const DenseJob& j,
   constexpr bool kGates = has_gates(MODE), kExtra = MODE == kLinear || has_grad(MODE);
   using Acc = typename Mfma<T>::Acc;
   const Place p;
-  const LanePart<T, C> l(p, a, j, n0);
+  const LanePart<T, C> l(p, n0, j.N, j.bias >= 0 ? static_cast<const T*>(a.bias) + j.bias : nullptr);
   const int64_t n_tiles = (a.n_rows + TA - 1) / TA;
   T* const gate_lds = lds + TA * P;
   const int K = j.main.src.K, K0 = j.gate.src.K;
@@ -556,7 +556,7 @@ __device__ __forceinline__ void chunked_job(const DenseArgs& a, const DenseJob& 
   constexpr bool kGates = has_gates(MODE), kExtra = MODE == kLinear || has_grad(MODE);
   using Acc = typename Mfma<T>::Acc;
   const Place p;
-  const LanePart<T, C> l(p, a, j, n0);
+  const LanePart<T, C> l(p, n0, j.N, j.bias >= 0 ? static_cast<const T*>(a.bias) + j.bias : nullptr);
   const int64_t n_tiles = (a.n_rows + TA - 1) / TA;
   const bool with_extra = has_grad(MODE) || (MODE == kLinear && a.extra != nullptr);
   for (int64_t t = index; t < n_tiles; t += j.blocks) {
@@ -658,6 +658,39 @@ hipError_t launch_jobs(DenseArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * kWaves), lds, s, a);
   return hipGetLastError();
 }
+
+// ------------------------------------------------ gradients in one pass (fp32)
+struct BackJob {
+  Term main, gate;      // x and the maps; gated: the rows of 0e and the gates' weights
+  RowSource g;          // grad_out
+  int32_t d, K, N, K0;  // channels of x, of the result, of 0e
+  int32_t x_off;        // first column in a row of grad_x
+  int32_t bias, gate0, act;
+  int32_t even;         // the even scalars' map
+  int32_t first, blocks;
+  int64_t at;           // first value of the job's parts: K x N, gated: K0 x N, N column sums
+};
+
+struct BackArgs {
+  int64_t n_rows;
+  int32_t ld_x, ld_g, n_gates, n_scalars;
+  int32_t n_jobs;
+  int32_t params;       // parameters' gradients are wanted
+  const void* bias;
+  float* grad_x;        // or NULL
+  float* dz;            // gated: [n_rows][n_gates]
+  float* du;            // gated: the even scalars' [n_rows][n_scalars]
+  float* part;
+  BackJob job[kMaxMaps];
+};
+
+constexpr int kBackBlocks = 512;  // as many as the CUs hold at a time
+
+template <bool GATED, bool X8>
+hipError_t run_back(BackArgs& a, int C, hipStream_t s);
+
+// Blocks of the jobs for n_rows, and where their parts start; returns the parts' values.
+int64_t cut_back(BackArgs& a, int C, bool gated);
 
 // All jobs of a pass; node_dense_rows.hip holds one of each for a type and mode.
 template <class T, int MODE, bool X8>
