@@ -292,17 +292,24 @@ hipError_t dense_forward(const Dense& p, int64_t n_rows, const void* x, const vo
 }  // namespace
 
 int64_t cut_back(BackArgs& a, int C, bool gated) {
-  int64_t work = 0, parts = 0;
-  auto cost = [&](const BackJob& j) { return j.d + (gated ? 1 : 0); };
-  for (int i = 0; i < a.n_jobs; ++i) work += cost(a.job[i]);
+  int64_t parts = 0, tiles[kMaxMaps], cost[kMaxMaps];
+  int32_t shares[kMaxMaps], of[kMaxMaps];
+  for (int i = 0; i < a.n_jobs; ++i) {
+    const BackJob& j = a.job[i];
+    const int atoms = atoms_of<float>(j.d, C);
+    tiles[i] = (a.n_rows + atoms - 1) / atoms;
+    // products a tile: the map's, its transposed one (but gated 0e's) and its gradient's, the gates' and their gradient's
+    const bool sloped = !gated && j.even && j.act != TPCONV_ACT_IDENTITY;
+    cost[i] = atoms * (gated ? 3 * j.d + 2 - (j.even ? 1 : 0) : 2 * j.d + (sloped ? 1 : 0));
+    shares[i] = 1;
+  }
+  share_out(a.n_jobs, tiles, cost, shares, kBackBlocks, of);
   int32_t blocks = 0;
   for (int i = 0; i < a.n_jobs; ++i) {
     BackJob& j = a.job[i];
-    const int atoms = atoms_of<float>(j.d, C);
-    const int64_t tiles = (a.n_rows + atoms - 1) / atoms;
     j.first = blocks;
-    j.blocks = static_cast<int32_t>(std::min<int64_t>(tiles, (kBackBlocks * cost(j) + work - 1) / work));
-    blocks += j.blocks;
+    j.blocks = of[i];
+    blocks += (j.blocks + 7) / 8 * 8;
     j.at = parts;
     parts += j.blocks * (int64_t(j.K) * j.N + int64_t(j.K0) * j.N + (gated || (j.d == 1 && j.even) ? j.N : 0));
   }

@@ -537,6 +537,27 @@ __device__ __forceinline__ void add_chunks(const Place& p, const LanePart<T, C>&
                                            int64_t base, int rows, T* lds, typename Mfma<T>::Acc (&acc)[MT][D]) {
   constexpr int KS = C / 4, P = pitch_of<T>(D, C), TA = 16 * MT * (64 / C);
   const int K = term.src.K, own = rows - 16 * MT * l.wa;
+  if constexpr (sizeof(T) == 4 && ADJ && D == 1 && VEC) {  // the next channels are on their way while some are multiplied
+    Mover<T, C * D, TA, P, VEC, X8> mover;
+    T w[KS], next[KS];
+    mover.issue(p, term.src, base, rows, 0, min(C, K), D);
+    load_weights<T, KS, ADJ>(term, n, l.g4, 0, min(C, K), next);
+    for (int k0 = 0; k0 < K; k0 += C) {
+      const int count = min(C, K - k0), after = min(C, K - k0 - C);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) w[s] = next[s];
+      __syncthreads();
+      mover.land(p, lds, rows, count * D);
+      if (count < C) clear_channels<T, D, C, P>(p, lds, TA, count);
+      __syncthreads();
+      if (after > 0) {
+        mover.issue(p, term.src, base, rows, k0 + C, after, D);
+        load_weights<T, KS, ADJ>(term, n, l.g4, k0 + C, after, next);
+      }
+      multiply<T, D, KS, MT, P>(lds + 16 * MT * l.wa * P, l.i16, l.g4, own, w, acc);
+    }
+    return;
+  }
   for (int k0 = 0; k0 < K; k0 += C) {
     const int count = min(C, K - k0);
     T w[KS];
@@ -623,6 +644,43 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && MODE != kGatedGrad ?
 }
 
 // -------------------------------------------------------------------- host
+// Blocks for each of n jobs of tiles[i] tiles that take cost[i] each, `most` in
+// all (but one for each job), so that the last to end ends early: the shortest
+// time in which whole numbers of tiles fit, within 2 %, and what is left over
+// where most is to do, so that all jobs last as long (their segments lie at
+// different places of the rows, and a job alone keeps some memory channels idle).
+// Blocks go round the 8 XCDs, and a job's are a multiple of 8, so one XCD has the
+// same rows of all jobs.  (28000 rows' linear gradients in one pass: 117 us;
+// without what is left over 145, not in multiples of 8 135.)
+inline void share_out(int n, const int64_t* tiles, const int64_t* cost, const int32_t* shares, int64_t most,
+                      int32_t* blocks) {
+  auto in_eights = [](int64_t b) { return (b + 7) / 8 * 8; };
+  double time = 0;
+  for (int i = 0; i < n; ++i) time += double(tiles[i]) * double(cost[i]) * shares[i];
+  time /= double(most);
+  int64_t used = 0;
+  for (int tries = 0; tries < 500; ++tries, time *= 1.02) {
+    used = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t each = std::max<int64_t>(1, static_cast<int64_t>(time / double(cost[i])));
+      blocks[i] = static_cast<int32_t>(std::min(in_eights((tiles[i] + each - 1) / each), tiles[i]));
+      used += in_eights(blocks[i]) * shares[i];
+    }
+    if (used <= most) break;
+  }
+  for (;;) {
+    int best = -1;
+    for (int i = 0; i < n; ++i)
+      if (blocks[i] + 8 <= tiles[i] && used + 8 * shares[i] <= most &&
+          (best < 0 || double(tiles[i]) * double(cost[i]) / blocks[i] >
+                           double(tiles[best]) * double(cost[best]) / blocks[best]))
+        best = i;
+    if (best < 0) return;
+    blocks[best] += 8;
+    used += 8 * shares[best];
+  }
+}
+
 // Blocks of a launch, two for each that a CU holds at a time (28000 rows of 64 channels l <= 3, linear and its
 // transposed products: 512 blocks 109 and 87 us, 768: 95 and 77, 1024: 95 and 76, 1536: 88 and 74).
 constexpr int64_t kDenseBlocks = 1536;
@@ -631,23 +689,23 @@ constexpr int64_t kDenseBlocks = 1536;
 template <class T, int C, int MODE, bool X8>
 hipError_t launch_jobs(DenseArgs& a, hipStream_t s) {
   size_t lds = 0;
-  int64_t work = 0;
-  auto cost = [](const DenseJob& j) -> int64_t {  // of a share's atom
-    return (j.main.src.K + C - 1) / C * j.d + (j.gate.src.K + C - 1) / C;
-  };
-  for (int i = 0; i < a.n_jobs; ++i) {
-    a.job[i].shares = (a.job[i].N + C - 1) / C;
-    work += a.job[i].shares * cost(a.job[i]);
-  }
-  int32_t blocks = 0;
+  int64_t tiles[kMaxMaps], cost[kMaxMaps];
+  int32_t shares[kMaxMaps], of[kMaxMaps];
   for (int i = 0; i < a.n_jobs; ++i) {
     DenseJob& j = a.job[i];
     const int atoms = atoms_of<T>(j.d, C);
-    const int64_t tiles = (a.n_rows + atoms - 1) / atoms;
-    j.first = blocks;
-    j.blocks = static_cast<int32_t>(std::min(tiles, (kDenseBlocks * cost(j) + work - 1) / work));
-    blocks += (j.blocks + 7) / 8 * 8 * j.shares;
+    shares[i] = j.shares = (j.N + C - 1) / C;
+    tiles[i] = (a.n_rows + atoms - 1) / atoms;
+    cost[i] = atoms * ((j.main.src.K + C - 1) / C * j.d + (j.gate.src.K + C - 1) / C);
     lds = std::max(lds, sizeof(T) * atoms * (pitch_of<T>(j.d, C) + (j.gate.src.K > 0 ? pitch_of<T>(1, C) : 0)));
+  }
+  share_out(a.n_jobs, tiles, cost, shares, kDenseBlocks, of);
+  int32_t blocks = 0;
+  for (int i = 0; i < a.n_jobs; ++i) {
+    DenseJob& j = a.job[i];
+    j.first = blocks;
+    j.blocks = of[i];
+    blocks += (j.blocks + 7) / 8 * 8 * j.shares;
   }
   auto* const f = k_dense<T, C, MODE, X8>;
   if (lds > 64 * 1024) {  // above the default limit of dynamic LDS

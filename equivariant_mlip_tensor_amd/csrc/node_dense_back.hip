@@ -268,6 +268,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_back(BackArgs a) {
   while (ji + 1 < a.n_jobs && static_cast<int>(blockIdx.x) >= a.job[ji + 1].first) ++ji;
   const BackJob j = a.job[ji];
   const int index = static_cast<int>(blockIdx.x) - j.first;
+  if (index >= j.blocks) return;
   float* const lds = reinterpret_cast<float*>(dynamic);
   switch (j.d) {
     case 1: back_job<1, C, GATED, X8>(a, j, index, lds); break;
