@@ -29,12 +29,38 @@ __device__ __forceinline__ T normal_below(T z) {  // Phi(z)
   return T(0.5) * erfc(z * T(-0.70710678118654752440));
 }
 
-// The activation and its slope, the slope in forms that do not cancel where it
-// saturates: 1 - s as the sigmoid of -z, 1 - tanh^2 by exponentials.
+// e^v for v <= 0, and 1/v for v in [1, 2]: fp32 by the hardware's 2^v and
+// reciprocal, the product with log2(e) carried in two parts (2 units of error
+// each; 214648 edges of 64 scalars, silu and its gradient: TODO us, by the
+// library's functions, with their cases for other arguments, 132).
+__device__ __forceinline__ float exp_below(float v) {
+  constexpr float kLog2e = 1.44269504088896340736f;
+  const float t = v * kLog2e, rest = fmaf(v, kLog2e, -t);
+  return __builtin_amdgcn_exp2f(t) * fmaf(rest, 0.69314718055994530942f, 1.0f);
+}
+__device__ __forceinline__ double exp_below(double v) { return exp(v); }
+__device__ __forceinline__ float reciprocal(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ double reciprocal(double v) { return 1.0 / v; }
+
+// 1/(1 + e^-z) and 1/(1 + e^z), neither by a difference; one exponential and one
+// reciprocal for both.
+template <class T>
+struct Sigmoids {
+  T of, other;
+  __device__ __forceinline__ explicit Sigmoids(T z) {
+    const T e = exp_below(-fabs(z)), q = reciprocal(T(1) + e);
+    of = z < T(0) ? e * q : q;
+    other = z < T(0) ? q : e * q;
+    of = z != z ? z : of;
+    other = z != z ? z : other;
+  }
+};
+
+// The activation and its slope, in forms that do not cancel where they saturate.
 template <int KIND, class T>
 __device__ __forceinline__ T activated(T z) {
-  if constexpr (KIND == TPCONV_ACT_SILU) return z / (T(1) + exp(-z));
-  if constexpr (KIND == TPCONV_ACT_SIGMOID) return T(1) / (T(1) + exp(-z));
+  if constexpr (KIND == TPCONV_ACT_SILU) return z * Sigmoids<T>(z).of;
+  if constexpr (KIND == TPCONV_ACT_SIGMOID) return Sigmoids<T>(z).of;
   if constexpr (KIND == TPCONV_ACT_TANH) return tanh(z);
   if constexpr (KIND == TPCONV_ACT_GELU) return z * normal_below(z);
   return z;
@@ -43,13 +69,16 @@ __device__ __forceinline__ T activated(T z) {
 template <int KIND, class T>
 __device__ __forceinline__ T slope_of(T z) {
   if constexpr (KIND == TPCONV_ACT_SILU) {
-    const T s = T(1) / (T(1) + exp(-z)), t = T(1) / (T(1) + exp(z));
-    return s + z * s * t;
+    const Sigmoids<T> s(z);
+    return s.of + z * s.of * s.other;
   }
-  if constexpr (KIND == TPCONV_ACT_SIGMOID) return T(1) / ((T(1) + exp(-z)) * (T(1) + exp(z)));
+  if constexpr (KIND == TPCONV_ACT_SIGMOID) {
+    const Sigmoids<T> s(z);
+    return s.of * s.other;
+  }
   if constexpr (KIND == TPCONV_ACT_TANH) {
-    const T e = exp(T(-2) * fabs(z)), q = T(1) / (T(1) + e);
-    return T(4) * e * q * q;
+    const Sigmoids<T> s(T(2) * z);  // 1 - tanh^2
+    return T(4) * s.of * s.other;
   }
   if constexpr (KIND == TPCONV_ACT_GELU) return normal_below(z) + z * exp(T(-0.5) * z * z) * T(0.39894228040143267794);
   return T(1);

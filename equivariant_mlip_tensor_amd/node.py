@@ -30,6 +30,7 @@ Each forward has its backward; the layouts are those of the header.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -464,17 +465,22 @@ def _dtype_code(dtype):
 
 # The calls below launch on the current device, where all of their tensors have to be.
 def _here(t, shape, dtype, name):
-    _need(t, shape, dtype, name)
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _explain(t, shape, dtype, name)
+    at = torch._C._cuda_getDevice()
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{at}")
     return t
 
 
 def _scratch(need: int, workspace, device):
-    """(pointer, bytes) of the workspace given, or of one made for the call."""
+    """The workspace given, or one made for the call, and its bytes."""
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        need = max(need, 256)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     _need_bytes(workspace, "workspace")
+    if workspace.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"workspace is on cuda:{workspace.get_device()}, not on the current device")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -548,19 +554,19 @@ def tpconv_norm_forward(plan: NormPlan, x, residual=None, gamma=None, out=None, 
         _here(residual, shape, dt, "residual")
     if gamma is not None:
         _here(gamma, (plan.channels,), dt, "gamma")
-    if need[0] and out is None:
-        out = torch.empty_like(x)
-    if need[1] and sum is None and residual is not None:
-        sum = torch.empty_like(x)
-    if need[2] and packed is None:
-        packed = PackedRows(torch.empty(shape, dtype=torch.uint8, device=x.device),
-                            torch.empty((n, plan.n_segments), dtype=torch.float32, device=x.device))
     if out is not None:
         _here(out, shape, dt, "out")
+    elif need[0]:
+        out = torch.empty_like(x)
     if sum is not None:
         _here(sum, shape, dt, "sum")
+    elif need[1] and residual is not None:
+        sum = torch.empty_like(x)
     if packed is not None:
         _packed_here(packed, n, plan.dim, plan.n_segments)
+    elif need[2]:
+        packed = PackedRows(x.new_empty(shape, dtype=torch.uint8),
+                            x.new_empty((n, plan.n_segments), dtype=torch.float32))
     if out is not None or sum is not None or packed is not None:
         _check(_lib.tpconv_norm_forward(plan.handle, n, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum), _ptr(out),
                                         None if packed is None else packed.codes.data_ptr(),
@@ -583,23 +589,25 @@ def tpconv_norm_backward(plan: NormPlan, h, gamma, grad_out, grad_sum=None, grad
         _here(gamma, (plan.channels,), dt, "gamma")
     if grad_sum is not None:
         _here(grad_sum, shape, dt, "grad_sum")
-    if need[0] and grad_x is None:
-        grad_x = torch.empty_like(h)
-    if need[1] and grad_gamma is None:
-        grad_gamma = h.new_empty(plan.channels)
     if grad_x is not None:
         _here(grad_x, shape, dt, "grad_x")
-    held = 0
+    elif need[0]:
+        grad_x = torch.empty_like(h)
     if grad_gamma is not None:
         _here(grad_gamma, (plan.channels,), dt, "grad_gamma")
+    elif need[1]:
+        grad_gamma = h.new_empty(plan.channels)
+    held = 0
+    if grad_gamma is not None:
         workspace, held = _scratch(int(_lib.tpconv_norm_workspace_bytes(plan.handle, n)), workspace, h.device)
     _check(_lib.tpconv_norm_backward(plan.handle, n, _ptr(h), _ptr(gamma), _ptr(grad_out), _ptr(grad_sum),
                                      _ptr(grad_x), _ptr(grad_gamma), _ptr(workspace), held, _stream_handle(stream)))
     return grad_x, grad_gamma
 
 
-def _segments_of(irreps: str) -> int:
-    return irreps.count("+") + 1
+@functools.lru_cache(maxsize=256)
+def _text_and_segments(irreps: str):
+    return irreps.encode(), irreps.count("+") + 1
 
 
 @_on_launch_stream
@@ -608,12 +616,13 @@ def tpconv_pack8(irreps: str, x, packed: Optional[PackedRows] = None, stream=Non
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     _here(x, x.shape, torch.float32, "x")
+    text, n_segments = _text_and_segments(irreps)
     n, dim = x.shape
     if packed is None:
-        packed = PackedRows(torch.empty((n, dim), dtype=torch.uint8, device=x.device),
-                            torch.empty((n, _segments_of(irreps)), dtype=torch.float32, device=x.device))
-    _packed_here(packed, n, dim, _segments_of(irreps))
-    _check(_lib.tpconv_pack8(irreps.encode(), n, dim, _ptr(x), _ptr(packed.codes), _ptr(packed.scales),
+        packed = PackedRows(x.new_empty((n, dim), dtype=torch.uint8), x.new_empty((n, n_segments)))
+    else:
+        _packed_here(packed, n, dim, n_segments)
+    _check(_lib.tpconv_pack8(text, n, dim, x.data_ptr(), packed.codes.data_ptr(), packed.scales.data_ptr(),
                              _stream_handle(stream)))
     return packed
 
@@ -624,11 +633,13 @@ def tpconv_unpack8(irreps: str, packed: PackedRows, out=None, stream=None) -> to
     if packed.codes.dim() != 2:
         raise ValueError("codes must be 2-D")
     n, dim = packed.codes.shape
-    _packed_here(packed, n, dim, _segments_of(irreps))
+    text, n_segments = _text_and_segments(irreps)
+    _packed_here(packed, n, dim, n_segments)
     if out is None:
-        out = torch.empty((n, dim), dtype=torch.float32, device=packed.codes.device)
-    _here(out, (n, dim), torch.float32, "out")
-    _check(_lib.tpconv_unpack8(irreps.encode(), n, dim, _ptr(packed.codes), _ptr(packed.scales), _ptr(out),
+        out = packed.scales.new_empty((n, dim))
+    else:
+        _here(out, (n, dim), torch.float32, "out")
+    _check(_lib.tpconv_unpack8(text, n, dim, packed.codes.data_ptr(), packed.scales.data_ptr(), out.data_ptr(),
                                _stream_handle(stream)))
     return out
 
@@ -709,7 +720,8 @@ def tpconv_gated_forward(plan: DensePlan, x, weights, gate_weights, gate_bias=No
         _here(gate_bias, (plan.n_gates,), dt, "gate_bias")
     if out is None:
         out = x.new_empty((n, plan.dim_out))
-    _here(out, (n, plan.dim_out), dt, "out")
+    else:
+        _here(out, (n, plan.dim_out), dt, "out")
     _check(_lib.tpconv_gated_forward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(gate_weights), _ptr(gate_bias),
                                      _ptr(out), _stream_handle(stream)))
     return out
@@ -729,7 +741,8 @@ def tpconv_linear_forward(plan: DensePlan, x, weights, bias=None, residual=None,
         _here(residual, (n, plan.dim_out), dt, "residual")
     if out is None:
         out = x.new_empty((n, plan.dim_out))
-    _here(out, (n, plan.dim_out), dt, "out")
+    else:
+        _here(out, (n, plan.dim_out), dt, "out")
     _check(_lib.tpconv_linear_forward(plan.handle, n, _ptr(x), _ptr(weights), _ptr(bias), _ptr(residual), _ptr(out),
                                       _stream_handle(stream)))
     return out
