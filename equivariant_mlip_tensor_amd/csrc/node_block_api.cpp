@@ -157,7 +157,7 @@ extern "C" tpconv_status tpconv_norm_plan(const char* irreps, int scope, double 
     *out = nullptr;
     if (!known(dtype)) return bad("unknown dtype");
     if (scope != TPCONV_NORM_SEGMENT && scope != TPCONV_NORM_ROW) return bad("norm: unknown scope");
-    if (!(std::isfinite(eps) && eps > 0)) return bad("norm: eps must be finite and above 0");
+    if (!(std::isfinite(eps) && eps >= 0x1p-126)) return bad("norm: eps must be finite and at least 2^-126");
     Norm p{};
     const tpconv_status st = rows_of(irreps, p.args);
     if (st != TPCONV_OK) return st;

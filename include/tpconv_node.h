@@ -265,7 +265,7 @@ typedef struct {
 
 /* tpconv_norm_plan: host only.  irreps as for tpconv_dropout_forward (any mul,
  * repeated (l, parity) too), at most 32 segments and TPCONV_MAX_NORM_DIM
- * columns; eps finite and above 0.  Errors: TPCONV_E_INVALID_ARG,
+ * columns; eps finite and at least 2^-126.  Errors: TPCONV_E_INVALID_ARG,
  * TPCONV_E_IRREPS, TPCONV_E_UNSUPPORTED. */
 tpconv_status tpconv_norm_plan(const char* irreps, int scope, double eps, tpconv_dtype dtype, tpconv_norm_t* out);
 tpconv_status tpconv_norm_query(tpconv_norm_t plan, tpconv_norm_info* info);

@@ -38,7 +38,7 @@ def test_norm_plan(node):
     ("4x0z", 0, 1e-6, 0, IRREPS), ("", 0, 1e-6, 0, IRREPS), ("4x5e", 0, 1e-6, 0, UNSUPPORTED),
     ("+".join(["1x0e"] * 33), 0, 1e-6, 0, UNSUPPORTED), ("8193x0e", 0, 1e-6, 0, UNSUPPORTED),
     ("2000x2e", 0, 1e-6, 0, UNSUPPORTED), ("16777216x4e", 0, 1e-6, 0, UNSUPPORTED), ("4x0e", 2, 1e-6, 0, INVALID),
-    ("4x0e", -1, 1e-6, 0, INVALID), ("4x0e", 0, 0.0, 0, INVALID), ("4x0e", 0, -1.0, 0, INVALID),
+    ("4x0e", -1, 1e-6, 0, INVALID), ("4x0e", 0, 0.0, 0, INVALID), ("4x0e", 0, -1.0, 0, INVALID), ("4x0e", 0, 1e-40, 0, INVALID),
     ("4x0e", 0, float("inf"), 0, INVALID), ("4x0e", 0, float("nan"), 0, INVALID), ("4x0e", 0, 1e-6, 2, INVALID)])
 def test_norm_plan_errors(node, irreps, scope, eps, dt, status):
     h = ctypes.c_void_p()
@@ -169,6 +169,23 @@ def test_dense_refusals(node):
     assert lb(plan=plain.handle, n=4, x=None, outs=(None, PTR, None)) == INVALID
     assert lb(plan=plain.handle, n=4, x=None, outs=(None, None, PTR)) == INVALID
     assert lb(plan=plain.handle, n=4, x=None, w=None, outs=(PTR, None, None)) == INVALID
+
+
+def test_sizes_past_every_grid(node):
+    """Plans with the most maps and channels, and the most rows: sizes in 64 bits, found at once."""
+    import time
+    wide = "+".join(f"1024x{l}{p}" for l in range(5) for p in "eo")
+    for dt, size in (("f32", 4), ("f64", 8)):
+        gated, linear = node.tpconv_gated_plan(wide, wide, dtype=dt), node.tpconv_linear_plan(wide, wide, "silu", dtype=dt)
+        assert gated.weight_numel == linear.weight_numel == 10 << 20 and gated.n_gates == 10240
+        for n in ((1 << 31) - 1, 1 << 20, 1):
+            begin = time.perf_counter()
+            held = node.tpconv_dense_workspace_bytes(gated, n)
+            assert held >= size * n * (gated.dim_out + gated.n_gates)
+            assert node.tpconv_dense_workspace_bytes(linear, n) >= size * n * linear.n_bias
+            assert time.perf_counter() - begin < 0.05
+        norm = node.tpconv_norm_plan("8192x0e", dtype=dt)
+        assert 0 < node.tpconv_norm_workspace_bytes(norm, (1 << 31) - 1) < 1 << 28
 
 
 def test_dense_workspace_is_bounded(node):

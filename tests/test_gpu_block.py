@@ -567,6 +567,103 @@ def test_dense_keeps_not_numbers_in_their_row(node):  # noqa: F811
     assert torch.isnan(runs[1][0][3]).all()
 
 
+@pytest.mark.parametrize("irr_in,irr_out", [
+    ("32x0e+8x1o+4x2e", "32x0e+16x1o+4x2e"), ("64x0e+36x1o+4x3o", "60x0e+64x1o+8x3o"), ("64x0e+32x1o", "64x1o"),
+    ("32x1o+16x0e+4x0o", "8x0o+24x1o"), ("4x3o+48x0e+20x2e+4x1e", "64x0e+4x3o"), ("64x0e", "64x0e")])
+def test_gradients_in_one_pass(node, irr_in, irr_out):  # noqa: F811
+    """Maps whose fp32 gradients take one pass over the rows: tiles that end early, blocks of one tile and of many,
+    every choice of outputs, rows of NaN, and the same from rows that lie off the alignment (the other way)."""
+    import torch
+    for n in (1, 16, 31, 64, 65, 130, 1000, 9001):
+        log(f"[block] gradients in one pass {irr_in} -> {irr_out} n={n}")
+        g = check_gated(node, "f32", irr_in, irr_out, n, bias=n % 2 == 0, packed=n % 5 == 0)
+        lin = check_linear(node, "f32", irr_in, irr_out, n, act="silu" if n % 2 else "identity", packed=n % 5 == 0)
+        if n not in (65, 130):
+            continue
+        plan, kept, W, Wg, b, G, _, full = g
+        for need in ((1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 0, 0, 1), (0, 1, 1, 0)):
+            got = node.tpconv_gated_backward(plan, kept, W, Wg, b, G, need=need)
+            for p, q, asked in zip(got, full, need):
+                assert torch.equal(p, q) if asked else p is None
+        plan, kept, W, b, _, G, _, full = lin
+        for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0)):
+            got = node.tpconv_linear_backward(plan, kept, W, b, G, need=need)
+            for p, q, asked in zip(got, full, need):
+                assert torch.equal(p, q) if asked else p is None
+    check_gated(node, "f32", irr_in, irr_out, 130, place=shifted)
+    check_linear(node, "f32", irr_in, irr_out, 130, place=shifted)
+    rng = np.random.default_rng(14)
+    x, G, W = block_inputs(rng, "f32", irr_in, irr_out, 130)
+    spoiled = x.copy()
+    spoiled[3], spoiled[77], spoiled[129] = np.nan, np.inf, -np.inf
+    keep = torch.ones(130, dtype=torch.bool, device="cuda")
+    keep[[3, 77, 129]] = False
+    gated, linear = node.tpconv_gated_plan(irr_in, irr_out), node.tpconv_linear_plan(irr_in, irr_out, "gelu")
+    Wg = dev(rng.standard_normal((gated.n_scalars, gated.n_gates)).astype(np.float32))
+    a, c = (node.tpconv_gated_backward(gated, dev(v), dev(W), Wg, None, dev(G))[0] for v in (x, spoiled))
+    assert torch.equal(a[keep], c[keep])
+    a, c = (node.tpconv_linear_backward(linear, dev(v), dev(W), None, dev(G))[0] for v in (x, spoiled))
+    assert torch.equal(a[keep], c[keep])
+
+
+def test_activations_at_large_arguments(node):  # noqa: F811
+    """Gates from -3e38 to 3e38: values and slopes stay numbers, and take their limits."""
+    import torch
+    big = np.array([-3e38, -1e30, -1e4, -200, -90, 0, 90, 200, 1e4, 1e30, 3e38], np.float32)
+    for act in sorted(ob.GROWTH):
+        for irr in ("1x0e", "4x0e"):
+            log(f"[block] {act} at large arguments {irr}")
+            mul = int(irr[0])
+            x = np.zeros((len(big), mul), np.float32)
+            x[:, 0] = big
+            W = np.eye(mul, dtype=np.float32).reshape(-1)
+            linear = node.tpconv_linear_plan(irr, irr, act)
+            out = host(node.tpconv_linear_forward(linear, dev(x), dev(W)))
+            G = dev(np.ones_like(x))
+            gx = host(node.tpconv_linear_backward(linear, dev(x), dev(W), None, G)[0])
+            value, slope = ob.activation(act, x.astype(np.float64))
+            assert (np.abs(out - value) <= 40 * EPS["f32"] * (1 + np.abs(value))).all(), (act, out, value)
+            assert (np.abs(gx - slope) <= 40 * EPS["f32"] * (1 + np.abs(slope))).all(), (act, gx, slope)
+
+
+def test_offsets_past_32_bits(node):  # noqa: F811
+    """Rows whose elements number over 2^31: the last ones' results are those of a call on them alone."""
+    import torch
+    n, irreps, tail = 2_200_003, "64x0e+64x1o+64x2e+64x3o", 77
+    x = torch.zeros(n, 1024, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[-tail:] = torch.randn(tail, 1024, generator=g, device="cuda")
+    end = x[-tail:].clone()
+    norm = node.tpconv_norm_plan(irreps)
+    log("[block] norm past 32 bits")
+    y, _, p = node.tpconv_norm_forward(norm, x, need=(True, True, True))
+    want, _, q = node.tpconv_norm_forward(norm, end, need=(True, True, True))
+    assert torch.equal(y[-tail:], want) and torch.equal(p.codes[-tail:], q.codes)
+    assert torch.equal(p.scales[-tail:], q.scales) and not y[:-tail].any()
+    back = node.tpconv_unpack8(irreps, p, out=y)
+    assert torch.equal(back[-tail:], node.tpconv_unpack8(irreps, q))
+    gx, _ = node.tpconv_norm_backward(norm, x, None, x, grad_x=y)
+    assert torch.equal(gx[-tail:], node.tpconv_norm_backward(norm, end, None, end)[0])
+    gated, linear = node.tpconv_gated_plan(irreps, irreps), node.tpconv_linear_plan(irreps, irreps)
+    W = torch.randn(gated.weight_numel, generator=g, device="cuda") / 8
+    Wg = torch.randn(64, 256, generator=g, device="cuda") / 8
+    log("[block] linear and gated past 32 bits")
+    assert torch.equal(node.tpconv_linear_forward(linear, x, W, residual=x, out=y)[-tail:],
+                       node.tpconv_linear_forward(linear, end, W, residual=end))
+    assert torch.equal(node.tpconv_gated_forward(gated, x, W, Wg, out=y)[-tail:],
+                       node.tpconv_gated_forward(gated, end, W, Wg))
+    for kept, kept_end in ((x, end), (p, q)):
+        got = node.tpconv_gated_backward(gated, kept, W, Wg, None, x, grad_x=y)
+        want = node.tpconv_gated_backward(gated, kept_end, W, Wg, None, end)
+        assert torch.equal(got[0][-tail:], want[0])
+        # rows of zeros add nothing but another order of the sums: both are within the bounds of these rows alone
+        rows = end if kept is x else node.tpconv_unpack8(irreps, q)
+        bounds = gated_bounds("f32", irreps, irreps, "silu", "sigmoid", rows.cpu().numpy(), W.cpu().numpy(),
+                              Wg.cpu().numpy(), None, end.cpu().numpy())
+        for a, c, bound in zip(got[1:], want[1:], bounds[1:]):
+            within(a, host(c), 2 * bound, "parameters' gradients")
+
+
 def test_linear_onto_its_residual(node):  # noqa: F811
     import torch
     for irr_in, irr_out in (PAIRS[4], PAIRS[5]):
