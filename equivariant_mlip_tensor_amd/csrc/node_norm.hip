@@ -600,7 +600,10 @@ hipError_t backward(NormArgs a, const T* h, const T* gamma, const T* grad_out, c
 }  // namespace
 
 size_t norm_workspace(bool f64, const NormArgs& a, int64_t n_rows) {
-  // rows of column sums for the most blocks that any spread of the row takes: one team a block at least
+  // none where one block has all rows, whichever way they are spread (by single elements over the most lanes); else rows
+  // of column sums for the most blocks: a row each
+  const Spread sp = spread(a.dim, true);
+  if (!sp.all && n_rows <= kThreads / sp.lanes) return 0;
   const int64_t blocks = n_rows < 1 ? 1 : (n_rows > kMostGradBlocks ? kMostGradBlocks : n_rows);
   return align_up((f64 ? 8 : 4) * static_cast<size_t>(blocks) * a.dim);
 }

@@ -474,9 +474,10 @@ def _here(t, shape, dtype, name):
 
 
 def _scratch(need: int, workspace, device):
-    """The workspace given, or one made for the call, and its bytes."""
+    """The workspace given, or one made for the call where it needs one, and its bytes."""
     if workspace is None:
-        need = max(need, 256)
+        if need == 0:
+            return None, 0
         return torch.empty(need, dtype=torch.uint8, device=device), need
     _need_bytes(workspace, "workspace")
     if workspace.get_device() != torch._C._cuda_getDevice():

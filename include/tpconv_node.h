@@ -290,8 +290,8 @@ tpconv_status tpconv_norm_forward(tpconv_norm_t plan, int64_t n_rows, const void
  *   grad_gamma [channels], the sum over rows and components of grad_out u.
  * Each is overwritten; NULL skips one.  grad_x may be h, grad_out or grad_sum
  * itself; no other overlap.  workspace: caller-owned, 256-byte aligned,
- * at least tpconv_norm_workspace_bytes (0 for bad sizes), needed for
- * grad_gamma; holds nothing between calls.  Errors: TPCONV_E_INVALID_ARG,
+ * at least tpconv_norm_workspace_bytes (0 for bad sizes, and for few rows, which
+ * need none), needed for grad_gamma; holds nothing between calls.  Errors: TPCONV_E_INVALID_ARG,
  * TPCONV_E_WORKSPACE, TPCONV_E_HIP. */
 size_t tpconv_norm_workspace_bytes(tpconv_norm_t plan, int64_t n_rows);
 tpconv_status tpconv_norm_backward(tpconv_norm_t plan, int64_t n_rows, const void* h, const void* gamma,

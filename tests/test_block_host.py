@@ -66,8 +66,9 @@ def test_norm_refusals(node):
         return lib.tpconv_norm_backward(plan, n, rows, None, g, None, gx, gg, ws, held, None)
     for kw in (dict(plan=None), dict(n=-1), dict(n=1 << 31), dict(rows=None), dict(g=None)):
         assert bwd(**kw) == INVALID, kw
-    assert bwd(ws=None) == WORKSPACE and bwd(ws=ODD) == WORKSPACE
-    assert bwd(held=lib.tpconv_norm_workspace_bytes(p32.handle, 4) - 1) == WORKSPACE
+    assert lib.tpconv_norm_workspace_bytes(p32.handle, 4) == 0                    # a block's rows need none
+    assert bwd(n=4000, ws=None) == WORKSPACE and bwd(n=4000, ws=ODD) == WORKSPACE
+    assert bwd(n=4000, held=lib.tpconv_norm_workspace_bytes(p32.handle, 4000) - 1) == WORKSPACE
     assert bwd(gx=None, gg=None) == OK and bwd(n=0, gg=None, rows=None, g=None) == OK
 
 
