@@ -303,7 +303,7 @@ int64_t cut_back(BackArgs& a, int C, bool gated) {
     cost[i] = atoms * (gated ? 3 * j.d + 2 - (j.even ? 1 : 0) : 2 * j.d + (sloped ? 1 : 0));
     shares[i] = 1;
   }
-  share_out(a.n_jobs, tiles, cost, shares, kBackBlocks, of);
+  share_out(a.n_jobs, tiles, cost, shares, back_blocks(gated), of);
   int32_t blocks = 0;
   for (int i = 0; i < a.n_jobs; ++i) {
     BackJob& j = a.job[i];

@@ -680,8 +680,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 4 && MODE != kGatedGrad ?
 // where most is to do, so that all jobs last as long (their segments lie at
 // different places of the rows, and a job alone keeps some memory channels idle).
 // Blocks go round the 8 XCDs, and a job's are a multiple of 8, so one XCD has the
-// same rows of all jobs.  (28000 rows' linear gradients in one pass: 117 us;
-// without what is left over 145, not in multiples of 8 135.)
+// same rows of all jobs.  (28000 rows' gated gradients in one pass, 512 blocks:
+// 167 us; without what is left over 183, and not in multiples of 8 193.)
 inline void share_out(int n, const int64_t* tiles, const int64_t* cost, const int32_t* shares, int64_t most,
                       int32_t* blocks) {
   auto in_eights = [](int64_t b) { return (b + 7) / 8 * 8; };
@@ -774,7 +774,10 @@ struct BackArgs {
   BackJob job[kMaxMaps];
 };
 
-constexpr int kBackBlocks = 512;  // as many as the CUs hold at a time
+// Blocks of that pass and its sums' join, about what a CU holds at a time by LDS, two gated and three linear (28000
+// rows of 64 channels l <= 3, gated: 512 blocks 174 us, 768: 204, 1024: 180, 1536: 181, 2048: 191; linear: 149, 123,
+// 130, 123, 128; each block leaves its sums to be joined).
+constexpr int back_blocks(bool gated) { return gated ? 512 : 768; }
 
 template <bool GATED, bool X8>
 hipError_t run_back(BackArgs& a, int C, hipStream_t s);
