@@ -774,10 +774,10 @@ struct BackArgs {
   BackJob job[kMaxMaps];
 };
 
-// Blocks of that pass and its sums' join, about what a CU holds at a time by LDS, two gated and three linear (28000
-// rows of 64 channels l <= 3, gated: 512 blocks 174 us, 768: 204, 1024: 180, 1536: 181, 2048: 191; linear: 149, 123,
-// 130, 123, 128; each block leaves its sums to be joined).
-constexpr int back_blocks(bool gated) { return gated ? 512 : 768; }
+// Blocks of that pass, 512: two to a CU.  Several linear maps get 768, whose last take the place of those that end
+// first.  (With the sums' join, 28000 rows of 64 channels l <= 3, gated: 512 blocks 174 us, 768: 204, 1024: 180, 1536:
+// 181; linear: 149, 118, 130, 123; 214648 rows of one map of 64 scalars: 82, 97, 88, 93.)
+constexpr int back_blocks(bool gated, int n_jobs) { return gated || n_jobs == 1 ? 512 : 768; }
 
 template <bool GATED, bool X8>
 hipError_t run_back(BackArgs& a, int C, hipStream_t s);
