@@ -15,6 +15,10 @@ namespace {
 // its 4 wavefronts share the tile.  Runs' matrices go to the workspace and are
 // added in order; one run writes the gradient itself.  The first row of tiles
 // also sums its columns of g, for the bias.
+// Only plans that the one pass over the rows does not take come here.  Bound by
+// latency at their sizes: 2048 fp64 rows of 16 channels l <= 4, with gates, 17 us
+// (x and du: 13 MB); 28000 fp32 rows of 64 channels l <= 3 by this way took 97 us
+// (229 MB, 2.4 TB/s).
 struct ParamJob {
   RowSource x, g;
   int32_t d, nu, nv;
@@ -321,7 +325,7 @@ namespace {
 
 // How the atoms of the parameters' jobs are cut into runs: about kParamBlocks
 // blocks of equal work, a run a whole number of stages.
-constexpr int kParamBlocks = 1024;
+constexpr int kParamBlocks = 1024;  // 4 for each CU
 
 struct ParamShape {
   int n_jobs = 0;

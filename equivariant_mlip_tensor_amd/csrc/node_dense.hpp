@@ -241,6 +241,11 @@ __device__ __forceinline__ void clear_channels(const Place& t, T* lds, int rows,
 // atoms' reads fall into all banks once.  Where a map's channels are read in one
 // go, the weights stay in registers and the next tile is on its way while one is
 // multiplied.
+// 28000 fp32 rows of 64 channels l <= 3: gated 82 us (229 MB, 2.8 TB/s; 4.6
+// GFLOP, 56 TFLOP/s), linear with residual 87 us (344 MB, 3.9 TB/s): memory's
+// latency, with three blocks a CU; with one tile staged and multiplied in turn
+// the gated one took 170.  2048 fp64 rows of 16 channels l <= 4: 15 us, latency
+// of a tile's loads, products and stores in turn.
 enum Mode { kLinear, kGated, kLinearGrad, kGatedGrad, kTransposed };
 
 constexpr bool has_gates(int mode) { return mode == kGated || mode == kGatedGrad; }

@@ -16,7 +16,7 @@
 // Sums, and the factors formed of them, run in 64 bits for both types, so that
 // squares of any fp32 value fit.
 // 28000 fp32 rows of 1024 with a residual: 78 us (459 MB, 5.9 TB/s); the gradient
-// 112 us (459 MB, 4.1 TB/s), joining grad_gamma's parts 10; into 8 bits 39 us (143
+// 111 us (459 MB, 4.1 TB/s), joining grad_gamma's parts 10; into 8 bits 38 us (143
 // MB, latency of the maxima), back 24 us (6.0 TB/s).  4096 rows of 512 with codes:
 // 12 us.  16 fp64 rows of 16: 2.5 and 4.4 us (latency).
 #include <hip/hip_runtime.h>
