@@ -8,6 +8,9 @@ namespace dense {
 template <class T, int MODE, bool X8>
 hipError_t run_dense(DenseArgs& a, hipStream_t s) {
   if (a.n_rows == 0 || a.n_jobs == 0) return hipSuccess;
+  // The fewest channels a block that hold the widest side: a narrow map in a wide block multiplies zeros.  (Gated, 2048
+  // fp64 rows of 16 channels l <= 4 with 16: 15 us, 32: 22; 4096 fp32 rows of 32 channels l <= 3 with 32: 12 us, 64: 18.)
+  // fp64 has no registers for 64.
   int widest = 1;
   for (int i = 0; i < a.n_jobs; ++i) widest = std::max({widest, a.job[i].N, a.job[i].main.src.K, a.job[i].gate.src.K});
   if (widest <= 16) return launch_jobs<T, 16, MODE, X8>(a, s);
