@@ -111,7 +111,10 @@ __device__ __forceinline__ void back_job(const BackArgs& a, const BackJob& j, in
   issue();
   float w[KS], wt[KS], wg[GATED ? KS : 1];
   if (again) load_weights<float, KS, false>(j.main, v.n, g4, 0, j.K, w);
-  load_weights<float, KS, true>(j.main, u.n, g4, 0, j.N, wt);
+  // the transposed ones with grad_x alone: without it a linear map may have none to read (weights NULL)
+#pragma unroll
+  for (int s = 0; s < KS; ++s) wt[s] = 0;
+  if (to_x) load_weights<float, KS, true>(j.main, u.n, g4, 0, j.N, wt);
   if constexpr (GATED) load_weights<float, KS, false>(j.gate, j.gate0 + v.n, g4, 0, j.K0, wg);
   // channels that are not there stay zero
   if (j.K < C) clear_channels<float, D, C, P>(p, xs, TA, j.K);

@@ -380,7 +380,8 @@ tpconv_status tpconv_linear_forward(tpconv_dense_t plan, int64_t n_rows, const v
  * the formulas' gradients at the restored rows; nothing else is kept from the
  * forward, gates and products are formed again.  Each output is overwritten;
  * NULL skips one.  The linear map's grad_x reads no x, and may be asked for
- * without it, where its activation is the identity.  workspace: caller-owned, 256-byte aligned, at least
+ * without it, where its activation is the identity; grad_weights and grad_bias
+ * then read no weights, which may be NULL without grad_x.  workspace: caller-owned, 256-byte aligned, at least
  * tpconv_dense_workspace_bytes (0 for bad sizes; gated: the rows of grad_out
  * and of its gates, and parts of the parameters' gradients, at most some 20 MB
  * or the parameters themselves); holds nothing between calls.  Errors: as the
