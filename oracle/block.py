@@ -143,7 +143,7 @@ def activation(kind, z):
         if kind == "identity":
             return z, np.ones_like(z)
         if kind == "tanh":
-            return np.tanh(z), 4.0 / (np.exp(np.minimum(z, 300)) + np.exp(-np.maximum(z, -300))) ** 2
+            return np.tanh(z), 4.0 / (np.exp(z) + np.exp(-z)) ** 2
         if kind == "gelu":
             below = np.array([0.5 * math.erfc(-v / math.sqrt(2.0)) for v in z.reshape(-1)]).reshape(z.shape)
             return z * below, below + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)

@@ -1,6 +1,8 @@
 """Pins of the fp64 definitions in oracle/block.py: closed forms, differences,
 rotation equivariance, torch's 8-bit conversion."""
 
+import math
+
 import numpy as np
 import pytest
 
@@ -158,3 +160,11 @@ def test_linear(act):
     R = rotation(rng)
     turned = ob.linear_forward(irr_in, irr_out, act, rotated(irr_in, R, x), W, b, rotated(irr_out, R, res))
     assert np.allclose(turned, rotated(irr_out, R, out), atol=1e-12)
+
+
+def test_slope_of_tanh_far_out():
+    """1/cosh^2, down to where it is no longer a normal number."""
+    z = np.array([-354, -320.5, -300, -17, 0, 3, 299, 310, 354, 400, 1e6])
+    value, slope = ob.activation("tanh", z)
+    want = np.array([0.0 if abs(v) > 355 else 1 / math.cosh(v) ** 2 for v in z])
+    assert np.array_equal(value, np.tanh(z)) and np.allclose(slope, want, rtol=1e-13, atol=0)
