@@ -1,13 +1,16 @@
 """The feed-forward block's operators where the general bounds of
-test_gpu_block.py are too wide to tell, and calls that the binding does not make."""
+test_gpu_block.py are too wide to tell, against the fp64 oracle, and calls that
+the binding does not make.  eps is the unit roundoff of the data type (2^-24,
+2^-53)."""
 
 import ctypes
 
 import numpy as np
 import pytest
 
-from test_gpu_block import block_inputs, log, shifted
-from test_gpu_node import dev, node  # noqa: F401  (node is a fixture)
+from oracle import block as ob
+from test_gpu_block import TOL, block_inputs, host, log, shifted
+from test_gpu_node import EPS, NP, dev, node, within  # noqa: F401  (node is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +43,65 @@ def test_linear_parameters_without_weights(node, dt, irr_in, irr_out, place):  #
                 plan.handle, n, *rows, None, None, Gd.data_ptr(), None, gW.data_ptr(), gb.data_ptr(), ws.data_ptr(),
                 held, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
             assert torch.equal(gW, want_W) and torch.equal(gb, want_b)
+
+
+# ---------------------------------------------------------------- activations
+def arguments(dt, act, slope, mul):
+    """[n, mul] arguments over the range in which the result is a number in full precision: it reaches far down one
+    side (both sides for a slope), to where that is subnormal or 0.  fp64: not beyond the exponential's range."""
+    low = 102.0 if dt == "f32" else 700.0
+    if slope and dt == "f32":
+        low = 86.0                     # the gradient passes the matrix cores: normal numbers alone
+    if act == "tanh":
+        low /= 2
+    return np.concatenate([np.linspace(-low, low, 16384 - 512), np.linspace(-2, 2, 512)]).reshape(-1, mul).astype(NP[dt])
+
+
+def activation_bounds(dt, act, z):
+    """Bounds of sigmoid, silu and their and tanh's slopes relative to their own size.  With e = e^-|z|, its hardware
+    exponential and the factor with it are within 4 eps (a unit is up to 2), 1 + e within 3, its reciprocal within 5; so
+    one sigmoid is within 5 and the other, times e, within 10; products and sums round once each.  What is formed of
+    subnormal numbers is off by half of the least one for each product, once times z.  tanh's slope: 4 s t at 2 z."""
+    e, least = EPS[dt], 2.0 ** (-149 if dt == "f32" else -1074)
+    value, slope = ob.activation(act, z)
+    s, t = ob.activation("sigmoid", z)[0], ob.activation("sigmoid", -z)[0]
+    of_value = {"sigmoid": 10 * e * s, "silu": 11 * e * np.abs(value)}.get(act)
+    of_slope = {"sigmoid": 16 * e * slope, "tanh": 16 * e * slope,
+                "silu": 10 * e * s + 18 * e * np.abs(z) * s * t + e * np.abs(slope)}[act]
+    tiny = 3 * least * (1 + np.abs(z))
+    return value, slope, None if of_value is None else TOL[dt] * of_value + tiny, TOL[dt] * of_slope + tiny
+
+
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu", "tanh"])
+def test_activations_relative_to_their_size(node, dt, act):  # noqa: F811
+    """Where an activation or its slope saturates at 0, its small values are right too: linear maps with W = 1 (in the
+    one-pass gradients and the other way), and gates."""
+    for mul in (1, 4):
+        irr = f"{mul}x0e"
+        log(f"[block] {act} {dt} relative to its size, {mul} channels")
+        W = dev(np.eye(mul, dtype=NP[dt]).reshape(-1))
+        linear = node.tpconv_linear_plan(irr, irr, act, dt)
+        z = arguments(dt, act, False, mul)
+        value, _, bound, _ = activation_bounds(dt, act, z.astype(np.float64))
+        if bound is not None:
+            within(node.tpconv_linear_forward(linear, dev(z), W), value, bound, "value")
+        z = arguments(dt, act, True, mul)
+        _, slope, _, bound = activation_bounds(dt, act, z.astype(np.float64))
+        got = node.tpconv_linear_backward(linear, dev(z), W, None, dev(np.ones_like(z)), need=(True, False, False))[0]
+        within(got, slope, bound, "slope")
+        # gates of 0e: channels 0 .. mul are the arguments, the next is 1 and every product's row
+        wide = f"{2 * mul}x0e"
+        gated = node.tpconv_gated_plan(wide, irr, scalar_act=act, dtype=dt)
+        M, Wg = np.zeros((2 * mul, mul), NP[dt]), np.zeros((2 * mul, mul), NP[dt])
+        M[mul] = 1
+        Wg[:mul] = np.eye(mul)
+        one = np.ones_like(z)
+        got = node.tpconv_gated_backward(gated, dev(np.concatenate([z, one], 1)), dev(M.reshape(-1)), dev(Wg), None,
+                                         dev(one), need=(True, False, False, False))[0]
+        within(host(got)[:, :mul], slope, bound, "gate's slope")
+        z = arguments(dt, act, False, mul)
+        value, _, bound, _ = activation_bounds(dt, act, z.astype(np.float64))
+        if bound is not None:
+            x = dev(np.concatenate([z, np.ones_like(z)], 1))
+            within(node.tpconv_gated_forward(gated, x, dev(M.reshape(-1)), dev(Wg)), value, bound, "gate's value")
