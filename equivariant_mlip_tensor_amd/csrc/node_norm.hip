@@ -359,15 +359,16 @@ __global__ __launch_bounds__(THREADS) void k_norm_grad(NormArgs a, const T* h_ro
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const double r = inverse_root(total[0][j], a.eps);
-      const T pull = static_cast<T>(total[1][j] * r * cols.share[j]), by = static_cast<T>(r);
+      const double pull = total[1][j] * r * cols.share[j];
       T gamma[PER];
       load_piece(gamma, weight, cols.col[j]);
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const T u = static_cast<T>(double(h[j][e]) * r);
-        mine[j][e] = fma(g[j][e], u, mine[j][e]);
-        h[j][e] = by * fma(-u, pull, g[j][e] * gamma[e]);
-        if (grad_sum != nullptr) h[j][e] += more[j][e];
+        const double ge = g[j][e], u = double(h[j][e]) * r;
+        mine[j][e] = fma(g[j][e], static_cast<T>(u), mine[j][e]);
+        // rounded once: in a segment of one column the difference is what eps leaves of its terms
+        const double grad = r * fma(-u, pull, ge * double(gamma[e]));
+        h[j][e] = static_cast<T>(grad_sum != nullptr ? grad + double(more[j][e]) : grad);
       }
     }
     if (grad_x != nullptr) store_row(h, grad_x + at, cols.col);

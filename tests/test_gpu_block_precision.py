@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 
 from oracle import block as ob
-from test_gpu_block import TOL, block_inputs, host, log, shifted
+from oracle.node import segments
+from test_gpu_block import TOL, block_inputs, features, host, log, shifted
 from test_gpu_node import EPS, NP, dev, node, within  # noqa: F401  (node is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +106,27 @@ def test_activations_relative_to_their_size(node, dt, act):  # noqa: F811
         if bound is not None:
             x = dev(np.concatenate([z, np.ones_like(z)], 1))
             within(node.tpconv_gated_forward(gated, x, dev(M.reshape(-1)), dev(Wg)), value, bound, "gate's value")
+
+
+# ----------------------------------------------------------------------- norm
+@pytest.mark.parametrize("scope", ["segment", "row"])
+@pytest.mark.parametrize("irreps", ["1x0e", "2x0e", "1x0e+6x0e+3x1o", "1x1o+4x0e", "64x0e+64x1o+64x2e+64x3o", "1000x1o+1x0e",
+                                    "8192x0e"])
+def test_norm_gradient_is_rounded_once(node, irreps, scope):  # noqa: F811
+    """fp32 grad_x is formed in 64 bits and rounded once, so it is within eps of itself however much of its two terms
+    cancels (in a segment of one column all but what eps leaves), and (8 width + 256) 2^-53 of these: a sum over
+    `width` columns is off by width 2^-53 of its absolute values, r by half that of the mean square, and each enters up
+    to three times, in the oracle as in the kernel."""
+    e, width = EPS["f32"], segments(irreps)[1]
+    for n, scale in ((1, 1.0), (37, 1.0), (37, 1e18), (37, 1e-3), (700, 1.0)):
+        for more in (False, True):
+            log(f"[block] norm gradient {irreps} {scope} n={n} scale {scale} {more}")
+            rng = np.random.default_rng([n, width, more])
+            h, G, H = ((s * features(rng, irreps, n, "f32")).astype(np.float32) for s in (scale, 1, 1e-3))
+            gamma = rng.standard_normal(ob.channels(irreps)[1]).astype(np.float32)
+            plan = node.tpconv_norm_plan(irreps, scope=scope, eps=1e-6)
+            args = (h, gamma, G, H if more else None)
+            gx = node.tpconv_norm_backward(plan, *(None if a is None else dev(a) for a in args), need=(True, False))[0]
+            want = ob.norm_backward(irreps, scope, 1e-6, *args)[0]
+            size = ob.norm_backward(irreps, scope, 1e-6, *args, size=True)[0]
+            within(gx, want, e * np.abs(want) + (8 * width + 256) * 2.0 ** -53 * size + 2.0 ** -149, "grad_x")
