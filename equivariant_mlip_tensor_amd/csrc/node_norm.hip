@@ -299,7 +299,7 @@ __global__ __launch_bounds__(THREADS) void k_norm(NormArgs a, const T* x, const 
       for (int j = 0; j < NP; ++j) {
         const double r = inverse_root(total[0][j], a.eps);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) h[j][e] = static_cast<T>(double(h[j][e]) * r) * cols.gamma[j][e];
+        for (int e = 0; e < PER; ++e) h[j][e] = static_cast<T>(double(h[j][e]) * r * double(cols.gamma[j][e]));
       }
       if (out != nullptr) store_row(h, out + at, cols.col);
     }
