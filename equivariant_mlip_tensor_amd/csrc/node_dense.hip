@@ -369,7 +369,7 @@ ParamShape param_shape(const Dense& p, int64_t n_rows) {
 }
 
 struct DenseSpace {
-  size_t rows, gates, parts, total;
+  size_t gates, parts, total;  // du of the rows, or the even scalars' gradient, stands at 0
 };
 
 // Whether the gradients' one pass over the rows takes the plan (its LDS and registers hold 64 channels of l <= 3 in
@@ -404,7 +404,6 @@ template <class T>
 DenseSpace dense_space(const Dense& p, int64_t n_rows) {
   DenseSpace w{};
   const ParamShape h = param_shape<T>(p, n_rows);
-  w.rows = 0;
   size_t at = 0;
   if (p.gated) {
     at = align_up(sizeof(T) * static_cast<size_t>(n_rows) * p.dim_out);

@@ -17,8 +17,9 @@ hipError_t run_dense(DenseArgs& a, hipStream_t s) {
   for (int i = 0; i < a.n_jobs; ++i)
     widest = std::max({widest, a.job[i].N, a.job[i].main.src.K, MODE == kTransposed ? 0 : a.job[i].gate.src.K});
   if (widest <= 16) return launch_jobs<T, 16, MODE, X8>(a, s);
-  if (widest <= 32 || sizeof(T) == 8) return launch_jobs<T, 32, MODE, X8>(a, s);
-  return launch_jobs<T, sizeof(T) == 4 ? 64 : 32, MODE, X8>(a, s);
+  if constexpr (sizeof(T) == 4)
+    if (widest > 32) return launch_jobs<T, 64, MODE, X8>(a, s);
+  return launch_jobs<T, 32, MODE, X8>(a, s);
 }
 
 #if TPCONV_DOUBLE
