@@ -10,7 +10,7 @@ import pytest
 
 from oracle import block as ob
 from oracle.node import segments
-from test_gpu_block import TOL, block_inputs, features, host, log, shifted
+from test_gpu_block import TOL, block_inputs, check_gated, features, host, log, shifted
 from test_gpu_node import EPS, NP, dev, node, within  # noqa: F401  (node is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +166,15 @@ def test_norm_is_rounded_once(node, irreps, scope):  # noqa: F811
             assert rows.mean() > 0.8 or n == 1
             assert np.array_equal(p.scales.cpu().numpy()[rows, i], scales[rows, i])
             assert np.array_equal(p.codes.cpu().numpy()[rows, cols], codes[rows, cols])
+
+
+# ---------------------------------------------------- few channels, many gates
+@pytest.mark.parametrize("dt", ["f32", "f64"])
+@pytest.mark.parametrize("irr_in,irr_out", [
+    ("16x0e+16x1o+16x2e+16x3o", "16x0e+64x1o+64x2e+64x3o"), ("8x0e+8x1o", "64x1o+8x0e"), ("1x0e+16x1o", "300x1o"),
+    ("32x0e+16x1o", "16x1o+500x0e")])
+def test_many_gates(node, dt, irr_in, irr_out):  # noqa: F811
+    """The even scalars' gradient, a product over many more gates than it has channels."""
+    for n in (1, 65, 333):
+        log(f"[block] many gates {dt} {irr_in} -> {irr_out} n={n}")
+        check_gated(node, dt, irr_in, irr_out, n)
