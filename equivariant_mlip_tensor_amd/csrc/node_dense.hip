@@ -303,7 +303,9 @@ int64_t cut_back(BackArgs& a, int C, bool gated) {
     const int atoms = atoms_of<float>(j.d, C);
     tiles[i] = (a.n_rows + atoms - 1) / atoms;
     // products a tile: the map's, its transposed one (but gated 0e's) and its gradient's, the gates' and their gradient's;
-    // linear: what the tile's way through LDS takes beside them (28000 rows of 64 channels l <= 3: 112 us, without 117)
+    // linear: what the tile's way through LDS takes beside them (with the sums' join, with and without it, 28000 rows of
+    // 64 channels l <= 3: 118 and 124 us, of 48 109 and 115, of 64 l <= 2 88 and 84, l <= 1 51 and 46, 80000 of the last
+    // two 193 and 224, 129 and 128)
     const bool sloped = !gated && j.even && j.act != TPCONV_ACT_IDENTITY;
     cost[i] = atoms * (gated ? 3 * j.d + 2 - (j.even ? 1 : 0) : 2 * j.d + (sloped ? 1 : 0)) + (gated ? 0 : 128);
     shares[i] = 1;

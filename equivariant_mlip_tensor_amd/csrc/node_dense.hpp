@@ -787,8 +787,11 @@ struct BackArgs {
 };
 
 // Blocks of that pass, 512: two to a CU.  Several linear maps get 768, whose last take the place of those that end
-// first.  (With the sums' join, 28000 rows of 64 channels l <= 3, gated: 512 blocks 174 us, 768: 204, 1024: 180, 1536:
-// 181; linear: 149, 118, 130, 123; 214648 rows of one map of 64 scalars: 82, 97, 88, 93.)
+// first: a gain where the maps' tiles last unequally long, a loss where they are alike (the shares know the products, not
+// the waits).  With the sums' join (us), linear, 768 and 512 blocks: 28000 rows of 64 channels l <= 3 118 and 143, of 48
+// 109 and 133, of 64 l <= 2 88 and 93, of 32 l <= 3 81 and 78, of 64 l <= 1 51 and 43, 80000 rows of these 309 and 384,
+// 283 and 352, 193 and 228, 215 and 196, 129 and 112; 4096 of the first 36 and 33.  214648 rows of one map of 64 scalars
+// 97 and 82, of 32 55 and 57.  Gated, 28000 rows of 64 channels l <= 3 204 and 174, of 32 145 and 135 with the forward.
 constexpr int back_blocks(bool gated, int n_jobs) { return gated || n_jobs == 1 ? 512 : 768; }
 
 template <bool GATED, bool X8>
