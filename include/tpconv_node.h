@@ -239,17 +239,19 @@ tpconv_status tpconv_dropout_backward(const char* irreps, tpconv_dtype dtype, in
  *                              one factor for the row, each segment counted alike;
  *   y[s][u][m] = gamma[c(s, u)] r h[s][u][m],
  * gamma a factor for each channel, channels counted over all segments (NULL:
- * ones).  Equivariant.  A padding row of zeros has y = 0.  Sums, and what is
- * formed of them, are held in 64 bits for both types, so squares of any F32
- * value fit (those of F64 values have to).  Infinities and NaN stay in their
+ * ones).  Equivariant.  A padding row of zeros has y = 0.  h is of the data type.
+ * Sums over a row, and what is formed of them, are held in 64 bits for both types
+ * and rounded once to an F32 y or grad_x, so squares of any F32 value fit (those
+ * of F64 values have to); grad_gamma is summed in the data type.  Infinities and NaN stay in their
  * row (scope segment: in their segment).
  *
  * 8 bits: a row and segment have one fp32 scale, max(2^-126, c a) with a the
  * largest magnitude in it and c the fp32 number next to 1/448; a value v is
  * held as the e4m3 code (OCP, 1-4-3 bits, largest 448) nearest to the fp32
  * product v i, ties to the even code, i the fp32 number next to 1/scale; it is
- * restored as code times scale, at most a/28 off.  A segment with an infinity
- * or NaN is restored as NaN. */
+ * restored as code times scale, off by at most the larger of 1/16 of itself and
+ * 2^-10 of the scale (and the roundings of i, v i and the product).  A segment
+ * with an infinity or NaN is restored as NaN. */
 #define TPCONV_MAX_NORM_DIM 8192
 
 typedef enum { TPCONV_NORM_SEGMENT = 0, TPCONV_NORM_ROW = 1 } tpconv_norm_scope;
